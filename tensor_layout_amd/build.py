@@ -16,7 +16,8 @@ LIB = os.path.join(HERE, "libtpl.so")
 # One translation unit per kernel family, compiled in parallel.
 SOURCES = ["planner.cpp", "kernels.hip", "kernels_stream.hip", "kernels_quad.hip", "kernels_lds.hip",
            "kernels_lds_w12.hip", "kernels_lds_w48.hip", "kernels_lds_w16.hip",
-           "kernels_swap.hip", "kernels_rec.hip", "kernels_etile.hip", "staged.hip"]
+           "kernels_swap.hip", "kernels_rec.hip", "kernels_etile.hip", "staged.hip",
+           "kv_append.hip", "kv_attend.hip", "kv_few.hip", "kv_tile.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [

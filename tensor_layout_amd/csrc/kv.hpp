@@ -1,0 +1,99 @@
+// kv.hpp -- what the paged key/value cache kernels share: argument blocks,
+// 16-bit and e4m3 conversions, and the reading of a batch's device arrays.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+#include <string>
+
+#include "../../include/tpl_kv.h"
+
+namespace tpl {
+
+int fail_status(int status, const std::string& why);   // kernels.hip
+
+namespace kv {
+
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x3 __attribute__((ext_vector_type(3)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+
+// The two 16-bit types: their vectors, matrix instructions and conversions.
+// e4m3 converts to either without rounding (4 significant bits, 2^-9 .. 448).
+struct Bf16 {
+    typedef __bf16 one;
+    typedef bf16x2 x2;
+    typedef bf16x8 x8;
+    static __device__ __forceinline__ f32x4 mfma16(x8 a, x8 b, f32x4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+    }
+    static __device__ __forceinline__ f32x16 mfma32(x8 a, x8 b, f32x16 c) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+    }
+    template <bool HI>
+    static __device__ __forceinline__ uint32_t from_e4m3(uint32_t w) {
+        return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, HI));
+    }
+};
+
+struct Fp16 {
+    typedef _Float16 one;
+    typedef f16x2 x2;
+    typedef f16x8 x8;
+    static __device__ __forceinline__ f32x4 mfma16(x8 a, x8 b, f32x4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+    }
+    static __device__ __forceinline__ f32x16 mfma32(x8 a, x8 b, f32x16 c) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+    }
+    template <bool HI>
+    static __device__ __forceinline__ uint32_t from_e4m3(uint32_t w) {
+        return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, HI));
+    }
+};
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    typename T::x2 r;
+    r[0] = (typename T::one)a;
+    r[1] = (typename T::one)b;
+    return __builtin_bit_cast(uint32_t, r);
+}
+
+template <typename T>
+__device__ __forceinline__ float lo16(uint32_t w) { return (float)__builtin_bit_cast(typename T::x2, w)[0]; }
+template <typename T>
+__device__ __forceinline__ float hi16(uint32_t w) { return (float)__builtin_bit_cast(typename T::x2, w)[1]; }
+
+// Tokens of a sequence: far enough from 2^31 that sums of positions and tile
+// offsets stay 32-bit numbers.
+constexpr int kMaxLength = 1 << 30;
+
+// A sequence of the batch as its device arrays give it; one that is not in
+// order (see tpl_kv.h) has no new tokens.
+struct Seq {
+    int row0;    // its first row
+    int n;       // new tokens
+    int length;  // tokens with them
+};
+
+__device__ __forceinline__ Seq read_seq(const tpl_kv_batch& g, int b) {
+    Seq s;
+    s.row0 = g.starts[b];
+    const int end = g.starts[b + 1];
+    s.length = g.lengths[b];
+    const bool ok = s.row0 >= 0 && end > s.row0 && end <= g.tokens && s.length >= end - s.row0 && s.length <= kMaxLength;
+    s.n = ok ? end - s.row0 : 0;
+    if (!ok) s.row0 = s.length = 0;
+    return s;
+}
+
+}  // namespace kv
+}  // namespace tpl

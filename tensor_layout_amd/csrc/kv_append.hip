@@ -1,0 +1,393 @@
+// kv_append.hip -- rotation of new keys and queries to their positions and
+// their writing, with the values, into the pages of a key/value cache.
+//
+// y[c] = x[c] cos a - x[c'] sin a, y[c'] = x[c'] cos a + x[c] sin a for the
+// pair (c, c') of a head, a = position * inv_freq.  For an e4m3 cache a block
+// of tokens of one head is scaled by the least power of two s with
+// max |y| <= 448 s, and y / s is rounded once.
+//
+// Bound: HBM bytes for prompts (each input read and each output written
+// once), the call's own latency for single tokens.  So one workgroup takes
+// the new tokens of one block (they share scales and angles: the angles'
+// cosines and sines are taken once, in LDS) and grid.y splits its heads where
+// blocks are few.  Within it a wave takes a head's keys or values at a time:
+// 8 channels a lane, so a wave reads 64 / (dim / 8) whole rows.
+#include "kv.hpp"
+
+namespace tpl {
+namespace kv {
+
+struct AppendArgs {
+    tpl_kv_cache c;
+    tpl_kv_batch g;
+    tpl_kv_new a;
+    int32_t unit;       // tokens of a group: the block, or kGroup where blocks bear no scale
+    int32_t by_token;   // grid.x: 1 a group for each row that begins one, 0 numbered by sequence
+    int32_t sec_end[TPL_KV_MAX_AXES];
+};
+
+constexpr int kGroup = 16;
+
+// cos and sin of an angle in 64 bits, rounded to 32.  The angle is brought
+// into [-pi/4, pi/4] with pi/2 in two parts (a product of up to 31 bits times
+// the first is exact inside the fused multiply-add); the Taylor series end
+// where the next term is under 2^-44, far below a 32-bit rounding.
+__device__ __forceinline__ float2 cos_sin(double angle) {
+    const double n = __builtin_rint(angle * 0.63661977236758134308);   // 2 / pi
+    double r = __builtin_fma(-n, 1.57079632679489655800, angle);
+    r = __builtin_fma(-n, 6.12323399573676603587e-17, r);
+    const double z = r * r;
+    double s = 1.0 / 6227020800.0;
+    s = __builtin_fma(s, z, -1.0 / 39916800.0);
+    s = __builtin_fma(s, z, 1.0 / 362880.0);
+    s = __builtin_fma(s, z, -1.0 / 5040.0);
+    s = __builtin_fma(s, z, 1.0 / 120.0);
+    s = __builtin_fma(s, z, -1.0 / 6.0);
+    s = __builtin_fma(s * z, r, r);
+    double c = -1.0 / 87178291200.0;
+    c = __builtin_fma(c, z, 1.0 / 479001600.0);
+    c = __builtin_fma(c, z, -1.0 / 3628800.0);
+    c = __builtin_fma(c, z, 1.0 / 40320.0);
+    c = __builtin_fma(c, z, -1.0 / 720.0);
+    c = __builtin_fma(c, z, 1.0 / 24.0);
+    c = __builtin_fma(c, z, -0.5);
+    c = __builtin_fma(c, z, 1.0);
+    // |n| is under 2^53 and r is no number where the angle is none.
+    const int q = (int)((int64_t)n & 3);
+    const double cc = (q & 1) ? s : c, ss = (q & 1) ? c : s;
+    return make_float2((float)((q == 1 || q == 2) ? -cc : cc), (float)((q & 2) ? -ss : ss));
+}
+
+// The 8 channels from `ch` of a row, rotated.  `cs`: the row's table of
+// (cos, sin), or NULL.  Products are rounded before they are added, as the
+// formula's plain evaluation does, so that a block's maximum does not depend
+// on which of the two products a fused multiply-add would keep whole.
+template <typename T>
+__device__ __forceinline__ void load_rotated(const typename T::one* row, int ch, int rot, bool interleaved,
+                                             const float2* cs, float y[8]) {
+#pragma clang fp contract(off)
+    const u32x4 w = *reinterpret_cast<const u32x4*>(row + ch);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        y[2 * i] = lo16<T>(w[i]);
+        y[2 * i + 1] = hi16<T>(w[i]);
+    }
+    if (!cs || ch >= rot) return;
+    const int half = rot >> 1;
+    if (interleaved) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (ch + 2 * i < rot) {
+                const float2 t = cs[(ch >> 1) + i];
+                const float a = y[2 * i], b = y[2 * i + 1];
+                y[2 * i] = a * t.x - b * t.y;
+                y[2 * i + 1] = b * t.x + a * t.y;
+            }
+        }
+        return;
+    }
+    if ((half & 7) == 0) {   // the partners are 8 aligned channels too
+        const bool first = ch < half;
+        const u32x4 p = *reinterpret_cast<const u32x4*>(row + (first ? ch + half : ch - half));
+        const float2* t = cs + (first ? ch : ch - half);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float b = (i & 1) ? hi16<T>(p[i >> 1]) : lo16<T>(p[i >> 1]);
+            const float x = y[i] * t[i].x, z = b * t[i].y;
+            y[i] = first ? x - z : x + z;
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int c = ch + i;
+        if (c < rot) {
+            const bool first = c < half;
+            const float b = (float)row[first ? c + half : c - half];
+            const float2 t = cs[first ? c : c - half];
+            const float x = y[i] * t.x, z = b * t.y;
+            y[i] = first ? x - z : x + z;
+        }
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void store8(typename T::one* p, const float y[8]) {
+    u32x4 w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = pack2<T>(y[2 * i], y[2 * i + 1]);
+    *reinterpret_cast<u32x4*>(p) = w;
+}
+
+__device__ __forceinline__ bool finite(float x) { return __builtin_fabsf(x) < __builtin_inff(); }
+
+// y / s as 8 e4m3 values.  Where s is a power of two (every scale this kernel
+// sets) the quotient is a shift of the exponent; another writer's scale
+// takes the division.
+__device__ __forceinline__ u32x2 held8(const float y[8], float s) {
+    float h[8];
+    const uint32_t bits = __builtin_bit_cast(uint32_t, s);
+    if ((bits & 0x007fffffu) == 0 && bits != 0) {
+        const int e = 127 - (int)(bits >> 23);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[i] = __builtin_amdgcn_ldexpf(y[i], e);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[i] = y[i] / s;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = finite(h[i]) ? h[i] : __builtin_nanf("");
+    u32x2 w;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        int v = __builtin_amdgcn_cvt_pk_fp8_f32(h[4 * i], h[4 * i + 1], 0, false);
+        w[i] = __builtin_amdgcn_cvt_pk_fp8_f32(h[4 * i + 2], h[4 * i + 3], v, true);
+    }
+    return w;
+}
+
+// The least power of two that brings amax to 448 = 0.875 * 2^9 or under.
+__device__ __forceinline__ float scale_of(float amax) {
+    const float part = __builtin_amdgcn_frexp_mantf(amax);
+    int e = __builtin_amdgcn_frexp_expf(amax);
+    e = e - 9 + (part > 0.875f ? 1 : 0);
+    e = amax == 0.0f ? -126 : (e < -126 ? -126 : (e > 127 ? 127 : e));
+    return __builtin_amdgcn_ldexpf(1.0f, e);
+}
+
+template <typename T, bool HELD8>
+__global__ void __launch_bounds__(256) k_append(AppendArgs p) {
+    typedef typename T::one one;
+    extern __shared__ float2 table[];
+    const tpl_kv_cache& c = p.c;
+    const tpl_kv_batch& g = p.g;
+    const tpl_kv_new& a = p.a;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int id = blockIdx.x, unit = p.unit;
+
+    // The sequence of this group, by counting those that begin at or before
+    // it: 64 at a time, one load's latency for each 64.
+    int before = 0;
+    for (int b0 = 0; b0 < g.batch; b0 += 64) {
+        const int b = b0 + lane;
+        bool there = false;
+        if (b < g.batch) {
+            const int r = g.starts[b];
+            there = p.by_token ? (r <= id && r < g.starts[b + 1]) : (r / unit + 2 * b <= id);
+            // by token, sequences without rows are passed over below
+        }
+        const uint64_t m = __ballot(there);
+        if (p.by_token) {
+            if (m) before = b0 + 64 - __builtin_clzll(m);
+        } else {
+            before += __builtin_popcountll(m);
+        }
+    }
+    if (before == 0) return;
+    const int b = __builtin_amdgcn_readfirstlane(before - 1);
+    const Seq s = read_seq(g, b);
+    if (s.n == 0) return;
+    const int first = s.length - s.n;   // index of the sequence's first new token
+    int i0, i1;                         // indexes of the group's tokens
+    if (p.by_token) {
+        i0 = first + id - s.row0;
+        if (id >= s.row0 + s.n || (id != s.row0 && i0 % unit != 0)) return;
+    } else {
+        const int64_t blk = first / unit + (int64_t)id - (s.row0 / unit + 2 * b);
+        const int64_t x = blk * unit;
+        if (x >= s.length) return;
+        i0 = x > first ? (int)x : first;
+    }
+    const int had = i0 % unit;
+    i1 = (s.length - i0 > unit - had) ? i0 + unit - had : s.length;
+    const int count = i1 - i0;
+    const int row0 = s.row0 + i0 - first;
+
+    const int pairs = a.inv_freq ? a.rot >> 1 : 0;
+    if (pairs) {
+        for (int i = threadIdx.x; i < count * pairs; i += 256) {
+            const int t = i / pairs, f = i - t * pairs;
+            int pos = i0 + t;
+            if (a.positions) {
+                int axis = 0;
+#pragma unroll
+                for (int k = 0; k < TPL_KV_MAX_AXES - 1; ++k) axis += (k + 1 < a.axes && f >= p.sec_end[k]) ? 1 : 0;
+                pos = a.positions[axis * a.positions_row + row0 + t];
+            }
+            table[i] = cos_sin((double)pos * (double)a.inv_freq[f]);
+        }
+        __syncthreads();
+    }
+    const float2* cs = pairs ? table : nullptr;
+
+    const int cpr = c.dim >> 3, rpw = 64 / cpr;
+    const int lr = lane / cpr, ch = (lane - lr * cpr) * 8;
+    const bool mine = lr < rpw;
+    const int pg = i0 / c.page, slot = i0 - pg * c.page;
+    const int where = pg < g.width ? g.table[b * g.table_row + pg] : -1;
+    const bool page_ok = where >= 0 && where < c.pages;
+
+    const int kv_tasks = page_ok ? 2 * c.kv_heads : 0;
+    for (int task = blockIdx.y * 4 + wave; task < kv_tasks; task += gridDim.y * 4) {
+        const bool key = task < c.kv_heads;
+        const int h = key ? task : task - c.kv_heads;
+        const one* x = key ? (const one*)a.k + row0 * a.k_token + h * a.k_head
+                           : (const one*)a.v + row0 * a.v_token + h * a.v_head;
+        const int64_t xs = key ? a.k_token : a.v_token;
+        const int64_t to = key ? where * c.k_page + slot * c.k_token + h * c.k_head
+                               : where * c.v_page + slot * c.v_token + h * c.v_head;
+        const int64_t ts = key ? c.k_token : c.v_token;
+        const float2* t2 = key ? cs : nullptr;
+        float y[8];
+        if constexpr (!HELD8) {
+            one* d = (one*)(key ? c.k : c.v) + to;
+            for (int t = lr; t < count; t += rpw) {
+                if (!mine) break;
+                load_rotated<T>(x + t * xs, ch, a.rot, a.interleaved, t2 + (key ? t * pairs : 0), y);
+                store8<T>(d + t * ts + ch, y);
+            }
+        } else {
+            float amax = 0.0f;
+            for (int t = lr; t < count; t += rpw) {
+                if (!mine) break;
+                load_rotated<T>(x + t * xs, ch, a.rot, a.interleaved, t2 ? t2 + t * pairs : nullptr, y);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) amax = finite(y[i]) ? fmaxf(amax, __builtin_fabsf(y[i])) : amax;
+            }
+#pragma unroll
+            for (int m = 32; m; m >>= 1) amax = fmaxf(amax, __shfl_xor(amax, m));
+            float sc = scale_of(amax);
+            float* at = key ? c.k_scale + where * c.ks_page + h * c.ks_head + (slot / c.block) * c.ks_block
+                            : c.v_scale + where * c.vs_page + h * c.vs_head + (slot / c.block) * c.vs_block;
+            uint8_t* d = (uint8_t*)(key ? c.k : c.v) + to;
+            if (had) {
+                const float old = *at;
+                const float grown = fmaxf(old, sc);
+                if (grown != old) {   // the tokens that the block holds, under the larger scale
+                    const float ratio = old / grown;
+                    for (int t = lr - had; t < 0; t += rpw) {
+                        if (!mine) break;
+                        u32x2* w = reinterpret_cast<u32x2*>(d + t * ts + ch);
+                        const u32x2 o = *w;
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            y[4 * i] = __builtin_amdgcn_cvt_f32_fp8(o[i], 0) * ratio;
+                            y[4 * i + 1] = __builtin_amdgcn_cvt_f32_fp8(o[i], 1) * ratio;
+                            y[4 * i + 2] = __builtin_amdgcn_cvt_f32_fp8(o[i], 2) * ratio;
+                            y[4 * i + 3] = __builtin_amdgcn_cvt_f32_fp8(o[i], 3) * ratio;
+                        }
+                        *w = held8(y, 1.0f);
+                    }
+                }
+                sc = grown;
+            }
+            for (int t = lr; t < count; t += rpw) {
+                if (!mine) break;
+                load_rotated<T>(x + t * xs, ch, a.rot, a.interleaved, t2 ? t2 + t * pairs : nullptr, y);
+                *reinterpret_cast<u32x2*>(d + t * ts + ch) = held8(y, sc);
+            }
+            if (lane == 0) *at = sc;
+        }
+    }
+
+    // The queries: rows of (token, head).  A row is read and written by one
+    // wave in one step, reads first, so q_out may be q itself.
+    if (a.q) {
+        const int rows = count * a.heads;
+        for (int r0 = (blockIdx.y * 4 + wave) * rpw; r0 < rows; r0 += gridDim.y * 4 * rpw) {
+            const int r = r0 + lr;
+            if (!mine || r >= rows) continue;
+            const int t = r / a.heads, h = r - t * a.heads;
+            float y[8];
+            load_rotated<T>((const one*)a.q + (row0 + t) * a.q_token + h * a.q_head, ch, a.rot, a.interleaved,
+                            cs ? cs + t * pairs : nullptr, y);
+            store8<T>((one*)a.q_out + (row0 + t) * a.o_token + h * a.o_head + ch, y);
+        }
+    }
+}
+
+template <typename T>
+static hipError_t launch_append(const AppendArgs& p, dim3 grid, size_t lds, hipStream_t st) {
+    if (p.c.type == TPL_KV_E4M3)
+        k_append<T, true><<<grid, 256, lds, st>>>(p);
+    else
+        k_append<T, false><<<grid, 256, lds, st>>>(p);
+    return hipGetLastError();
+}
+
+const char* check_cache(const tpl_kv_cache* c);                                   // kv_attend.hip
+const char* check_batch(const tpl_kv_cache& c, const tpl_kv_batch* g);
+bool aligned16(const void* p, int64_t s0, int64_t s1, int bytes);
+
+static int append_impl(const tpl_kv_cache* c, const tpl_kv_batch* g, const tpl_kv_new* a, hipStream_t st) {
+    if (!c || !g || !a) return fail_status(TPL_E_ARG, "cache, batch and arguments must not be NULL");
+    if (const char* why = check_cache(c)) return fail_status(TPL_E_ARG, why);
+    if (const char* why = check_batch(*c, g)) return fail_status(TPL_E_ARG, why);
+    if (a->type != TPL_KV_BF16 && a->type != TPL_KV_FP16)
+        return fail_status(TPL_E_DTYPE, "keys, values and queries must be bf16 or fp16");
+    if (c->type != TPL_KV_E4M3 && c->type != a->type)
+        return fail_status(TPL_E_DTYPE, "a 16-bit cache holds the type of its keys and values");
+    if (a->inv_freq) {
+        if (a->rot < 2 || a->rot > c->dim || (a->rot & 1))
+            return fail_status(TPL_E_ARG, "rotated channels must be an even number, 2 .. dim");
+        if (a->axes < 1 || a->axes > TPL_KV_MAX_AXES) return fail_status(TPL_E_ARG, "positions must have 1 .. 4 axes");
+        if (a->axes > 1) {
+            if (!a->positions) return fail_status(TPL_E_ARG, "sections need positions");
+            int64_t sum = 0;
+            for (int i = 0; i < a->axes; ++i) {
+                if (a->sections[i] < 0) return fail_status(TPL_E_ARG, "sections must be >= 0");
+                sum += a->sections[i];
+            }
+            if (sum != a->rot / 2) return fail_status(TPL_E_ARG, "sections must add up to the rotated pairs");
+        }
+    }
+    if (a->q && a->heads < 1) return fail_status(TPL_E_ARG, "heads must be >= 1");
+    if (g->batch == 0 || g->tokens == 0) return TPL_OK;
+    if (!a->k || !a->v) return fail_status(TPL_E_ARG, "k and v must not be NULL");
+    if (a->q && !a->q_out) return fail_status(TPL_E_ARG, "q needs q_out");
+    if (!aligned16(a->k, a->k_token, a->k_head, 2) || !aligned16(a->v, a->v_token, a->v_head, 2) ||
+        (a->q && (!aligned16(a->q, a->q_token, a->q_head, 2) || !aligned16(a->q_out, a->o_token, a->o_head, 2))))
+        return fail_status(TPL_E_LAYOUT, "k, v, q and q_out must start, and their rows and heads lie, on 16 bytes");
+
+    AppendArgs p;
+    p.c = *c;
+    p.g = *g;
+    p.a = *a;
+    if (!a->inv_freq) p.a.rot = 0;
+    p.unit = c->type == TPL_KV_E4M3 ? c->block : kGroup;
+    int end = 0;
+    for (int i = 0; i < TPL_KV_MAX_AXES; ++i) {
+        end += (a->inv_freq && a->axes > 1 && i < a->axes) ? a->sections[i] : 0;
+        p.sec_end[i] = end;
+    }
+    // A sequence's groups are numbered from starts / unit + 2 b on, which
+    // leaves room for the two that its ends may cut; where there are more
+    // such numbers than rows (single tokens), each row asks whether it
+    // begins a group.
+    const int64_t numbered = g->tokens / p.unit + 2 * (int64_t)g->batch;
+    p.by_token = g->tokens <= numbered ? 1 : 0;
+    const int64_t gx = p.by_token ? g->tokens : numbered;
+    // About two workgroups a CU; more would take the same angles again.
+    int64_t tasks = 2 * (int64_t)c->kv_heads + (a->q ? a->heads : 0);
+    int64_t gy = (512 + gx - 1) / gx, most = (tasks + 3) / 4;
+    if (gy > most) gy = most;
+    if (gy < 1) gy = 1;
+    const size_t lds = a->inv_freq ? (size_t)p.unit * (a->rot / 2) * sizeof(float2) : 0;
+    if (lds > 64 * 1024) return fail_status(TPL_E_ARG, "block * rotated channels must be at most 16384");
+    const dim3 grid((unsigned)gx, (unsigned)gy);
+    const hipError_t e = a->type == TPL_KV_BF16 ? launch_append<Bf16>(p, grid, lds, st) : launch_append<Fp16>(p, grid, lds, st);
+    if (e != hipSuccess) return fail_status(TPL_E_HIP, std::string("HIP launch failed: ") + hipGetErrorString(e));
+    return TPL_OK;
+}
+
+}  // namespace kv
+}  // namespace tpl
+
+extern "C" int tpl_kv_append(const tpl_kv_cache* cache, const tpl_kv_batch* batch, const tpl_kv_new* args,
+                             hipStream_t stream) {
+    try {
+        return tpl::kv::append_impl(cache, batch, args, stream);
+    } catch (...) {
+        return TPL_E_ARG;
+    }
+}

@@ -1,0 +1,191 @@
+// kv_attend.hip -- attention to a paged key/value cache: checks of arguments,
+// choice of the kernels, C entry points.
+#include <climits>
+
+#include "kv_attend.hpp"
+
+namespace tpl {
+namespace kv {
+
+bool aligned16(const void* p, int64_t s0, int64_t s1, int bytes) {
+    return ((uintptr_t)p & 15) == 0 && (s0 * bytes) % 16 == 0 && (s1 * bytes) % 16 == 0;
+}
+
+const char* check_cache(const tpl_kv_cache* c) {
+    if (c->type != TPL_KV_BF16 && c->type != TPL_KV_FP16 && c->type != TPL_KV_E4M3)
+        return "a cache holds bf16, fp16 or e4m3";
+    if (!c->k || !c->v) return "cache pools must not be NULL";
+    if (c->pages < 1 || c->pages > INT_MAX) return "a cache must have at least one page";
+    if (c->dim < 16 || c->dim > 256 || c->dim % 16) return "dim must be a multiple of 16, at most 256";
+    if (c->kv_heads < 1 || c->kv_heads > 65535) return "kv_heads must be 1 .. 65535";
+    if (c->page < 16 || c->page % 16) return "page must be a multiple of 16 tokens";
+    const int w = c->type == TPL_KV_E4M3 ? 1 : 2;
+    if (c->type == TPL_KV_E4M3) {
+        if (!c->k_scale || !c->v_scale) return "an e4m3 cache needs its scales";
+        if (c->block < 16 || c->block % 16 || c->page % c->block)
+            return "block must be a multiple of 16 tokens and divide the page";
+    }
+    if (!aligned16(c->k, c->k_token, c->k_head, w) || !aligned16(c->v, c->v_token, c->v_head, w) ||
+        (c->k_page * w) % 16 || (c->v_page * w) % 16)
+        return "cache pools must start, and their pages, tokens and heads lie, on 16 bytes";
+    return nullptr;
+}
+
+const char* check_batch(const tpl_kv_cache& c, const tpl_kv_batch* g) {
+    if (g->batch < 0 || g->tokens < 0 || g->width < 0) return "batch, tokens and width must be >= 0";
+    if (g->batch > (1 << 20)) return "batch must be at most 2^20";
+    if (g->tokens > (1 << 28)) return "tokens must be at most 2^28";
+    if ((int64_t)g->width * c.page > kMaxLength) return "a table row must not name more than 2^30 tokens";
+    if (g->batch && (!g->starts || !g->lengths || (g->width && !g->table)))
+        return "table, starts and lengths must not be NULL";
+    return nullptr;
+}
+
+constexpr int kCUs = 256;
+
+struct Choice {
+    bool few, tile;
+    int dc, mr, dk;
+    int64_t few_bytes, tile_bytes;
+    bool join;
+};
+
+static const char* choose(const tpl_kv_cache* c, const tpl_kv_batch* g, const tpl_kv_query* a, AttendArgs& p, Choice& q,
+                          int* status) {
+    *status = TPL_E_ARG;
+    if (!c || !g || !a) return "cache, batch and arguments must not be NULL";
+    if (const char* why = check_cache(c)) return why;
+    if (const char* why = check_batch(*c, g)) return why;
+    if (a->type != TPL_KV_BF16 && a->type != TPL_KV_FP16) {
+        *status = TPL_E_DTYPE;
+        return "queries must be bf16 or fp16";
+    }
+    if (c->type != TPL_KV_E4M3 && c->type != a->type) {
+        *status = TPL_E_DTYPE;
+        return "a 16-bit cache holds the type of its queries";
+    }
+    if (a->heads < 1 || a->heads % c->kv_heads) return "heads must be a multiple of the cache's";
+    if (!(a->scale > 0.0f) || !(a->scale < __builtin_inff())) return "scale must be a finite number over zero";
+    if (a->window < 0 || a->sinks < 0) return "window and sinks must be >= 0";
+    if (a->window > kMaxLength || a->sinks > kMaxLength) return "window and sinks must be at most 2^30";
+    p.c = *c;
+    p.g = *g;
+    p.a = *a;
+    if (c->type != TPL_KV_E4M3) p.c.block = c->page;
+    if (a->window == 0) p.a.sinks = 0;
+    p.parts = p.tile_parts = nullptr;
+    p.group = a->heads / c->kv_heads;
+    p.cap = g->width * c->page;
+    p.factor = a->scale * kLog2e;
+    p.div_page = make_fastdiv((uint32_t)c->page);
+    p.div_block = make_fastdiv((uint32_t)p.c.block);
+    p.div_group = make_fastdiv((uint32_t)p.group);
+    q.few = q.tile = false;
+    q.few_bytes = q.tile_bytes = 0;
+    if (g->batch == 0 || g->tokens == 0) return nullptr;
+    const int64_t rows = (int64_t)g->tokens * p.group;   // no sequence has more
+    if (rows > INT_MAX) return "tokens * heads / kv_heads must be under 2^31";
+
+    // Which kernel takes a sequence goes by its rows, which only the device
+    // knows; the host leaves a kernel out where no sequence can need it, and
+    // where there are no more rows than sequences (decoding) or only one
+    // sequence lets one kernel take whatever there is.
+    const int limit = 64;
+    if (p.group > kTileRows || rows <= limit || (g->batch > 1 && g->tokens <= g->batch)) {
+        q.few = true;
+        p.few = INT_MAX;
+    } else if (g->batch == 1) {
+        q.tile = true;
+        p.few = 0;
+    } else {
+        q.few = q.tile = true;
+        p.few = limit;
+    }
+    if (q.few) {
+        q.dc = c->dim <= 64 ? 4 : c->dim <= 128 ? 8 : c->dim % 12 == 0 ? 12 : 16;
+        // Rows of a tile: those of an average sequence, or of a decoding one
+        // where the average is a prompt's.
+        int64_t mean = (rows + g->batch - 1) / g->batch;
+        if (mean > limit) mean = p.group;
+        q.mr = mean <= 16 ? 1 : mean <= 32 || q.dc > 8 ? 2 : 4;
+        const int64_t tiles = (rows + q.mr * 16 - 1) / (q.mr * 16) + g->batch;
+        int64_t steps = ((int64_t)p.cap + 127) / 128 + 1;
+        q.join = steps > 2;
+        const int64_t most = tiles * c->kv_heads * steps;
+        p.workers = kCUs * (q.mr * q.dc <= 8 ? 4 : 2);
+        if (p.workers > most) p.workers = (int)most;
+        if ((int64_t)g->batch * c->kv_heads > INT_MAX) return "batch * kv_heads must be under 2^31";
+        q.few_bytes = (int64_t)p.workers * 2 * (q.mr * 16 * (16 * q.dc + 2)) * 4;
+    }
+    if (q.tile) {
+        q.dk = c->dim <= 64 ? 64 : c->dim <= 96 ? 96 : c->dim <= 128 ? 128 : c->dim <= 192 ? 192 : 256;
+        p.tile_tokens = kTileRows / p.group;
+        const int64_t tiles = (int64_t)g->tokens / p.tile_tokens + g->batch;
+        const int64_t units = tiles * c->kv_heads;
+        int64_t most = p.cap;
+        if (a->window && (int64_t)a->window + a->sinks + p.tile_tokens < most) most = (int64_t)a->window + a->sinks + p.tile_tokens;
+        most = (most + 511) / 512;
+        int64_t splits = 2 * kCUs / units;
+        if (splits > most) splits = most;
+        if (splits > 32) splits = 32;
+        if (splits < 1) splits = 1;
+        p.tiles = (int)tiles;
+        p.splits = (int)splits;
+        if (units * splits > INT_MAX) return "too many row tiles";
+        if (splits > 1) q.tile_bytes = units * splits * tile_part_floats(q.dk) * 4;
+    }
+    return nullptr;
+}
+
+static int attend_impl(const tpl_kv_cache* c, const tpl_kv_batch* g, const tpl_kv_query* a, void* ws, int64_t ws_bytes,
+                       hipStream_t st) {
+    AttendArgs p;
+    Choice q;
+    int status;
+    if (const char* why = choose(c, g, a, p, q, &status)) return fail_status(status, why);
+    if (!q.few && !q.tile) return TPL_OK;
+    if (!a->q || !a->out) return fail_status(TPL_E_ARG, "q and out must not be NULL");
+    if (!aligned16(a->q, a->q_token, a->q_head, 2) || !aligned16(a->out, a->o_token, a->o_head, 2))
+        return fail_status(TPL_E_LAYOUT, "q and out must start, and their rows and heads lie, on 16 bytes");
+    if (q.few_bytes + q.tile_bytes > 0 && (!ws || ((uintptr_t)ws & 15))) return fail_status(TPL_E_ARG, "workspace must lie on 16 bytes");
+    if (ws_bytes < q.few_bytes + q.tile_bytes) return fail_status(TPL_E_ARG, "workspace is too small");
+    p.parts = (float*)ws;
+    p.tile_parts = (float*)((char*)ws + q.few_bytes);
+    hipError_t e = hipSuccess;
+    if (q.tile) e = launch_tile(p, q.dk, false, st);
+    if (e == hipSuccess && q.few) e = launch_few(p, q.dc, q.mr, q.join, st);
+    if (e == hipSuccess && q.tile && p.splits > 1) e = launch_tile(p, q.dk, true, st);
+    if (e != hipSuccess) return fail_status(TPL_E_HIP, std::string("HIP launch failed: ") + hipGetErrorString(e));
+    return TPL_OK;
+}
+
+}  // namespace kv
+}  // namespace tpl
+
+extern "C" {
+
+int tpl_kv_attend(const tpl_kv_cache* cache, const tpl_kv_batch* batch, const tpl_kv_query* args, void* workspace,
+                  int64_t workspace_bytes, hipStream_t stream) {
+    try {
+        return tpl::kv::attend_impl(cache, batch, args, workspace, workspace_bytes, stream);
+    } catch (...) {
+        return TPL_E_ARG;
+    }
+}
+
+int64_t tpl_kv_attend_workspace(const tpl_kv_cache* cache, const tpl_kv_batch* batch, const tpl_kv_query* args) {
+    try {
+        tpl::kv::AttendArgs p;
+        tpl::kv::Choice q;
+        int status;
+        if (const char* why = tpl::kv::choose(cache, batch, args, p, q, &status)) {
+            tpl::fail_status(status, why);
+            return -1;
+        }
+        return q.few_bytes + q.tile_bytes;
+    } catch (...) {
+        return -1;
+    }
+}
+
+}  // extern "C"

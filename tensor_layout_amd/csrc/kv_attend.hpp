@@ -1,0 +1,183 @@
+// kv_attend.hpp -- argument block and tile arithmetic of the attention kernels.
+#pragma once
+
+#include "common.hpp"
+#include "kv.hpp"
+
+namespace tpl {
+namespace kv {
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+// A row's reference for its exponentials moves only when a score exceeds it
+// by this many powers of two, so that most tiles leave the accumulators as
+// they are; weights reach 2^8 then, far from any type's end.
+constexpr float kSlack = 8.0f;
+
+struct AttendArgs {
+    tpl_kv_cache c;
+    tpl_kv_batch g;
+    tpl_kv_query a;
+    float* parts;      // workspace: partial results
+    FastDiv div_page, div_block, div_group;
+    float factor;      // scale * log2 e
+    int32_t group;     // query heads that share one of the cache
+    int32_t cap;       // tokens that a table row can hold
+    // Split kernel (few rows a sequence)
+    int32_t few;       // it takes sequences of at most this many rows (new tokens * group)
+    int32_t workers;   // its workgroups
+    // Tile kernel (many rows a sequence)
+    int32_t tile_tokens;   // new tokens of a row tile
+    int32_t tiles;         // bound on the row tiles, grid order
+    int32_t splits;        // parts of each tile's tokens
+    float* tile_parts;
+};
+
+// The tokens that a range of rows sees, as groups of 16 consecutive tokens:
+// first `na` groups from token 0 (the sinks, where they lie before the
+// window), then groups from `lo` on.
+struct Span {
+    int na, lo, n;
+    __device__ __forceinline__ int base(int t) const { return t < na ? t * 16 : lo + (t - na) * 16; }
+};
+
+__device__ __forceinline__ Span span_of(const AttendArgs& p, int first_pos, int last_pos) {
+    Span s;
+    s.na = 0;
+    s.lo = 0;
+    int hi = last_pos + 1;
+    hi = hi < p.cap ? hi : p.cap;
+    if (p.a.window > 0 && first_pos >= p.a.window) {
+        const int lo = first_pos - p.a.window + 1;
+        const int sink = p.a.sinks < lo ? p.a.sinks : lo;
+        const int na = (sink + 15) >> 4, from = lo >> 4;
+        if (na < from) {
+            s.na = na;
+            s.lo = from * 16;
+        }
+    }
+    const int end = (hi + 15) >> 4, from = s.lo >> 4;
+    // Pages beyond the table's width are not there: the sinks end at hi too.
+    if (s.na > end) s.na = end;
+    s.n = s.na + (end > from ? end - from : 0);
+    return s;
+}
+
+__device__ __forceinline__ bool sees(const AttendArgs& p, int pos, int j) {
+    return j <= pos && (p.a.window == 0 || pos - j < p.a.window || j < p.a.sinks);
+}
+
+__device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
+__device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
+
+// Maximum and sum of a value over lanes that differ in bit 4 or 5.
+__device__ __forceinline__ float2 swap32(float x) {
+    const uint32_t u = __builtin_bit_cast(uint32_t, x);
+    const u32x2 r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    const uint32_t a = r[0], b = r[1];   // a bit cast of a vector's element itself reads its first
+    return make_float2(__builtin_bit_cast(float, a), __builtin_bit_cast(float, b));
+}
+__device__ __forceinline__ float2 swap16(float x) {
+    const uint32_t u = __builtin_bit_cast(uint32_t, x);
+    const u32x2 r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    const uint32_t a = r[0], b = r[1];
+    return make_float2(__builtin_bit_cast(float, a), __builtin_bit_cast(float, b));
+}
+__device__ __forceinline__ float max32(float x) { const float2 r = swap32(x); return fmaxf(r.x, r.y); }
+__device__ __forceinline__ float max16(float x) { const float2 r = swap16(x); return fmaxf(r.x, r.y); }
+__device__ __forceinline__ float sum32(float x) { const float2 r = swap32(x); return r.x + r.y; }
+__device__ __forceinline__ float sum16(float x) { const float2 r = swap16(x); return r.x + r.y; }
+
+// The split kernel's rows of a tile and tokens of a step: 4 waves of 32.
+constexpr int kStepGroups = 8;
+
+struct FewSeq {
+    Seq s;
+    Span span;
+    int tiles;      // row tiles
+    int steps;      // steps of one row tile of one head, at least 1
+    __device__ __forceinline__ uint64_t all(const AttendArgs& p) const {
+        return (uint64_t)tiles * (uint32_t)p.c.kv_heads * (uint32_t)steps;
+    }
+};
+
+template <int ROWS>
+__device__ __forceinline__ FewSeq few_seq(const AttendArgs& p, int b) {
+    FewSeq f;
+    f.s = read_seq(p.g, b);
+    const int64_t rows = (int64_t)f.s.n * p.group;
+    if (rows > p.few) f.s.n = 0;
+    f.tiles = f.s.n ? (int)((rows + ROWS - 1) / ROWS) : 0;
+    f.span = span_of(p, f.s.length - f.s.n, f.s.length - 1);
+    f.steps = (f.span.n + kStepGroups - 1) / kStepGroups;
+    if (f.steps < 1) f.steps = 1;
+    return f;
+}
+
+// Rows before each sequence in the order of steps: every workgroup sums the
+// batch for itself (one load's latency for up to 256 sequences).  Afterwards
+// `total` is the sum over the batch, and the sequence that holds step `c`
+// has its number and its own first step in *at_b and *at_step.
+template <int ROWS>
+__device__ __forceinline__ uint64_t locate(const AttendArgs& p, bool by_seq, int want_b, int* at_b, uint64_t* at_step,
+                                           uint64_t* chunk) {
+    __shared__ uint64_t sums[5];
+    __shared__ uint64_t found_step;
+    __shared__ int found_b;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int per = (p.g.batch + 255) / 256;
+    uint64_t mine = 0;
+    for (int i = 0; i < per; ++i) {
+        const int b = tid * per + i;
+        if (b < p.g.batch) mine += few_seq<ROWS>(p, b).all(p);
+    }
+    uint64_t run = mine;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const uint64_t o = __shfl_up(run, d);
+        if (lane >= d) run += o;
+    }
+    if (lane == 63) sums[wave] = run;
+    if (tid == 0) found_b = -1;
+    __syncthreads();
+    uint64_t total = 0, before = 0;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        if (w < wave) before += sums[w];
+        total += sums[w];
+    }
+    before += run - mine;
+    // Equal shares of the steps.
+    *chunk = (total + p.workers - 1) / (uint32_t)p.workers;
+    const uint64_t c = (uint64_t)blockIdx.x * *chunk;
+    if (by_seq ? (tid * per <= want_b && want_b < (tid + 1) * per) : (mine && before <= c && c < before + mine)) {
+        for (int i = 0; i < per; ++i) {
+            const int b = tid * per + i;
+            const uint64_t n = b < p.g.batch ? few_seq<ROWS>(p, b).all(p) : 0;
+            if (by_seq ? b == want_b : c < before + n) {
+                found_b = b;
+                found_step = before;
+                break;
+            }
+            before += n;
+        }
+    }
+    __syncthreads();
+    *at_b = found_b;
+    *at_step = found_step;
+    return total;
+}
+
+// Part of a row tile that one workgroup of the split kernel leaves: rows of
+// 16 * DC sums, then the rows' references, then their sums of weights.
+template <int DC, int MR>
+constexpr int few_part_floats() { return MR * 16 * (16 * DC + 2); }
+
+hipError_t launch_few(const AttendArgs& p, int dc, int mr, int join, hipStream_t st);
+hipError_t launch_tile(const AttendArgs& p, int dk, bool join, hipStream_t st);
+
+constexpr int kTileRows = 128;
+constexpr int tile_part_floats(int dk) { return kTileRows * (dk + 2); }
+
+}  // namespace kv
+}  // namespace tpl
