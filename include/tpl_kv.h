@@ -9,7 +9,8 @@
  * lengths[b] - (starts[b+1] - starts[b]) + i.
  *
  * Values are held in the tensors' own 16-bit type, or in e4m3 with one fp32
- * scale for each block of `block` tokens and head: value = e4m3 * scale.
+ * scale, over zero, for each block of `block` tokens and head: value = e4m3 *
+ * scale.  (Scales under 2^-126 count as 2^-126.)
  *
  * starts, lengths and table are read on the device only, so both calls can be
  * captured into a graph and replayed on new lengths.  Rows and pages that they

@@ -59,6 +59,18 @@ struct Fp16 {
     }
 };
 
+// e4m3 times a scale's power of two, as bf16: nothing is rounded while the
+// product stays a normal number.  scale_rest is what the power of two leaves
+// of a normal scale over zero: 1 to under 2, and 1 for every scale that
+// tpl_kv_append sets.
+template <bool HI>
+__device__ __forceinline__ uint32_t bf16_from_e4m3(uint32_t w, float scale) {
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, scale, HI));
+}
+__device__ __forceinline__ float scale_rest(float scale) {
+    return __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, scale) & 0x007fffffu) | 0x3f800000u);
+}
+
 template <typename T>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
     typename T::x2 r;

@@ -1,6 +1,7 @@
 // kv_attend.hip -- attention to a paged key/value cache: checks of arguments,
 // choice of the kernels, C entry points.
 #include <climits>
+#include <cstdlib>
 
 #include "kv_attend.hpp"
 
@@ -28,6 +29,8 @@ const char* check_cache(const tpl_kv_cache* c) {
     if (!aligned16(c->k, c->k_token, c->k_head, w) || !aligned16(c->v, c->v_token, c->v_head, w) ||
         (c->k_page * w) % 16 || (c->v_page * w) % 16)
         return "cache pools must start, and their pages, tokens and heads lie, on 16 bytes";
+    if (c->k_token < 0 || c->v_token < 0 || c->k_token > (1 << 24) || c->v_token > (1 << 24))
+        return "tokens of a page must lie at most 2^24 elements apart";
     return nullptr;
 }
 
@@ -91,7 +94,7 @@ static const char* choose(const tpl_kv_cache* c, const tpl_kv_batch* g, const tp
     // where there are no more rows than sequences (decoding) or only one
     // sequence lets one kernel take whatever there is.
     const int limit = 64;
-    if (p.group > kTileRows || rows <= limit || (g->batch > 1 && g->tokens <= g->batch)) {
+    if (p.group > 128 || rows <= limit || (g->batch > 1 && g->tokens <= g->batch)) {
         q.few = true;
         p.few = INT_MAX;
     } else if (g->batch == 1) {
@@ -119,7 +122,8 @@ static const char* choose(const tpl_kv_cache* c, const tpl_kv_batch* g, const tp
     }
     if (q.tile) {
         q.dk = c->dim <= 64 ? 64 : c->dim <= 96 ? 96 : c->dim <= 128 ? 128 : c->dim <= 192 ? 192 : 256;
-        p.tile_tokens = kTileRows / p.group;
+        p.tile_rows = getenv("R8") ? 256 : 128;
+        p.tile_tokens = p.tile_rows / p.group;
         const int64_t tiles = (int64_t)g->tokens / p.tile_tokens + g->batch;
         const int64_t units = tiles * c->kv_heads;
         int64_t most = p.cap;
@@ -132,7 +136,7 @@ static const char* choose(const tpl_kv_cache* c, const tpl_kv_batch* g, const tp
         p.tiles = (int)tiles;
         p.splits = (int)splits;
         if (units * splits > INT_MAX) return "too many row tiles";
-        if (splits > 1) q.tile_bytes = units * splits * tile_part_floats(q.dk) * 4;
+        if (splits > 1) q.tile_bytes = units * splits * tile_part_floats(q.dk, p.tile_rows) * 4;
     }
     return nullptr;
 }

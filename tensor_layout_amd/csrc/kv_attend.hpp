@@ -27,6 +27,7 @@ struct AttendArgs {
     int32_t few;       // it takes sequences of at most this many rows (new tokens * group)
     int32_t workers;   // its workgroups
     // Tile kernel (many rows a sequence)
+    int32_t tile_rows;     // 128 or 256
     int32_t tile_tokens;   // new tokens of a row tile
     int32_t tiles;         // bound on the row tiles, grid order
     int32_t splits;        // parts of each tile's tokens
@@ -176,8 +177,7 @@ constexpr int few_part_floats() { return MR * 16 * (16 * DC + 2); }
 hipError_t launch_few(const AttendArgs& p, int dc, int mr, int join, hipStream_t st);
 hipError_t launch_tile(const AttendArgs& p, int dk, bool join, hipStream_t st);
 
-constexpr int kTileRows = 128;
-constexpr int tile_part_floats(int dk) { return kTileRows * (dk + 2); }
+TPL_HD int tile_part_floats(int dk, int rows) { return rows * (dk + 2); }
 
 }  // namespace kv
 }  // namespace tpl

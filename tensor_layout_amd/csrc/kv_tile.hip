@@ -19,14 +19,17 @@
 // halves, and rescaling is a product with a lane's own number.
 #include "kv_attend.hpp"
 
+#ifndef PHASE_END
+#define PHASE_END __builtin_amdgcn_sched_barrier(0);
+#endif
 namespace tpl {
 namespace kv {
 
 constexpr int kTokens = 64;    // tokens of a step
-constexpr int kInfo = 256;     // 16-token groups whose pages are looked up at a time
+constexpr int kInfo = 128;     // 16-token groups whose pages are looked up at a time
 
-template <typename T, bool HELD8, int D>
-__global__ void __launch_bounds__(256) k_tile(AttendArgs p) {
+template <typename T, bool HELD8, int D, int WAVES>
+__global__ void __launch_bounds__(WAVES * 64, D <= 128 ? 2 : 1) k_tile(AttendArgs p) {
     typedef typename T::one one;
     typedef typename T::x8 x8;
     typedef typename std::conditional<HELD8, Bf16, T>::type V;   // as in kv_few.hip
@@ -34,12 +37,23 @@ __global__ void __launch_bounds__(256) k_tile(AttendArgs p) {
     constexpr int W = HELD8 ? 1 : 2;
     constexpr int KS = D / 16, NT = D / 32;
     // Rows of K padded by 16 bytes: an odd number of 16-byte units, so that
-    // 16 lanes reading a column of it reach all banks.
-    constexpr int KP = D * 2 + 16;
-    __shared__ __attribute__((aligned(16))) uint8_t ldsk[kTokens * KP];
-    __shared__ __attribute__((aligned(16))) uint8_t ldsv[D * kTokens * 2];
-    __shared__ int gpage[kInfo], gbase[kInfo];
-    __shared__ float gks[kInfo], gvs[kInfo];
+    // 16 lanes reading a column of it reach all banks.  Rows of V^T are 128
+    // bytes, their 16-byte units exchanged by the row's number: both the
+    // reads (rows next to each other, one unit) and the writes (rows 8 apart)
+    // then spread over the banks.
+    constexpr int KP = D * 2 + 16, KB = kTokens * KP, VB = D * kTokens * 2;
+    constexpr int THREADS = WAVES * 64;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[2 * (KB + VB)];   // two steps' keys, then values
+    // Two halves, looked up in turn.
+    __shared__ const uint8_t *gk[2 * kInfo], *gv[2 * kInfo];
+    __shared__ int gbase[2 * kInfo];
+    // Of a key's scale its product with the scores' factor.  Of a value's
+    // scale the power of two goes in where the values are converted; what is
+    // left of it, 1 to under 2, multiplies the weights: its logarithm is
+    // added in the exponent, and its reciprocal brings the weights' sum back.
+    __shared__ __attribute__((aligned(16))) float gks[2 * kInfo], gvs[2 * kInfo], glg[2 * kInfo], grv[2 * kInfo];
+    // A bit a group: all of it is seen by all of the tile's rows.
+    __shared__ uint64_t gfull[2 * kInfo / 64];
 
     const int tid = threadIdx.x, lane = tid & 63, r = lane & 31, hh = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -68,6 +82,7 @@ __global__ void __launch_bounds__(256) k_tile(AttendArgs p) {
     const int pmin = s.length - s.n + t0, pmax = pmin + tn - 1;
     const Span span = span_of(p, pmin, pmax);
     const int32_t* pages = p.g.table + b * p.g.table_row;
+    const int win = p.a.window ? p.a.window : 0x7fffffff;
 
     const int row = wave * 32 + r;
     const bool there = row < rows;
@@ -104,73 +119,95 @@ __global__ void __launch_bounds__(256) k_tile(AttendArgs p) {
 
     // What a thread brings: KN 16-byte pieces of keys; VN units of 4 tokens by
     // 8 channels of values.
-    constexpr int PIECES = D * W / 16, KN = (kTokens * PIECES + 255) / 256;
-    constexpr int CH8 = D / 8, VN = (kTokens / 4 * CH8 + 255) / 256;
-    u32x4 kreg[KN];
+    constexpr int PIECES = D * W / 16, KN = (kTokens * PIECES + THREADS - 1) / THREADS;
+    constexpr int CH8 = D / 8, VN = (kTokens / 4 * CH8 + THREADS - 1) / THREADS;
     typedef typename std::conditional<HELD8, u32x2, u32x4>::type VPiece;
+    u32x4 kreg[KN];
     VPiece vreg[VN][4];
+#pragma unroll
+    for (int i = 0; i < KN; ++i) kreg[i] = u32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < VN; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) vreg[i][e] = VPiece{};
 
-    auto look_up = [&](int group0) {   // pages, first tokens and scales of the next groups
-        const int t = group0 + tid;
-        int where = -1, base = 0;
+    // Where the next groups lie, their first tokens and scales.  A group
+    // whose page is not there stands beyond every position; its loads go to
+    // page 0.
+    auto look_up = [&](int group0) {
+        const int t = group0 + tid, to = t & (2 * kInfo - 1);
+        if (tid >= kInfo) return;
+        int where = -1, base = 0, slot = 0;
         float ks = 0.0f, vs = 0.0f;
         if (t < span.n) {
             base = span.base(t);
             const int pg = (int)fdiv((uint32_t)base, p.div_page);
             where = pages[pg];
             if (where >= p.c.pages) where = -1;
+            if (where >= 0) slot = base - pg * p.c.page;
             if (HELD8 && where >= 0) {
-                const int blk = (int)fdiv((uint32_t)(base - pg * p.c.page), p.div_block);
+                const int blk = (int)fdiv((uint32_t)slot, p.div_block);
                 ks = p.c.k_scale[where * p.c.ks_page + h * p.c.ks_head + blk * p.c.ks_block];
                 vs = p.c.v_scale[where * p.c.vs_page + h * p.c.vs_head + blk * p.c.vs_block];
             }
         }
-        gpage[tid] = where;
-        gbase[tid] = where < 0 ? 0x7fffff00 : base;
-        gks[tid] = HELD8 ? ks * p.factor : p.factor;
-        gvs[tid] = vs;
+        base = where < 0 ? 0x7fffff00 : base;
+        gbase[to] = base;
+        const uint64_t seen = __ballot((base <= pmin - 15) & ((pmax - base < win) | (base + 15 < p.a.sinks)));
+        if (lane == 0) gfull[to >> 6] = seen;
+        where = where < 0 ? 0 : where;
+        gk[to] = (const uint8_t*)p.c.k + (where * p.c.k_page + slot * p.c.k_token + h * p.c.k_head) * W;
+        gv[to] = (const uint8_t*)p.c.v + (where * p.c.v_page + slot * p.c.v_token + h * p.c.v_head) * W;
+        // A masked score is minus infinity times this: it must not be zero.
+        gks[to] = HELD8 ? fmaxf(ks * p.factor, 1.17549435e-38f) : p.factor;
+        if constexpr (HELD8) {
+            vs = vs < 1.17549435e-38f ? 1.17549435e-38f : vs;
+            const float rest = scale_rest(vs);
+            gvs[to] = vs;
+            glg[to] = rest == 1.0f ? 0.0f : __builtin_log2f(rest);
+            grv[to] = 1.0f / rest;
+        }
     };
-    auto fetch = [&](int step) {
-        const int g0 = (step * 4) & (kInfo - 1);
+    // Lanes beyond the head's channels read its first ones: those of keys are
+    // cleared before they meet the queries' zeros, those of values only reach
+    // sums that nothing stores.
+    auto all_see = [&](int step) {
+        const uint64_t m = gfull[(step >> 4) & (2 * kInfo / 64 - 1)];
+        const uint32_t half = (step & 8) ? (uint32_t)(m >> 32) : (uint32_t)m;
+        return ((__builtin_amdgcn_readfirstlane(half) >> ((step & 7) * 4)) & 15) == 15;
+    };
+    auto fetch_k = [&](int step) {
+        const int g0 = (step * 4) & (2 * kInfo - 1);
 #pragma unroll
         for (int i = 0; i < KN; ++i) {
-            const int id = i * 256 + tid, tok = id / PIECES, ch = (id - tok * PIECES) * (16 / W);
-            kreg[i] = u32x4{0, 0, 0, 0};
-            if (id < kTokens * PIECES && ch < p.c.dim) {
-                const int g = g0 + (tok >> 4), where = gpage[g];
-                if (where >= 0) {
-                    const int base = gbase[g];
-                    const int slot = base - (int)fdiv((uint32_t)base, p.div_page) * p.c.page + (tok & 15);
-                    kreg[i] = *reinterpret_cast<const u32x4*>(
-                        (const uint8_t*)p.c.k + (where * p.c.k_page + slot * p.c.k_token + h * p.c.k_head + ch) * W);
-                }
-            }
+            const int id = i * THREADS + tid, tok = id / PIECES, ch = (id - tok * PIECES) * (16 / W);
+            if (KN * THREADS == kTokens * PIECES || id < kTokens * PIECES)
+                kreg[i] = *reinterpret_cast<const u32x4*>(gk[g0 + (tok >> 4)] + ((tok & 15) * (int)p.c.k_token + (ch < p.c.dim ? ch : 0)) * W);
         }
+    };
+    auto fetch_v = [&](int step) {
+        const int g0 = (step * 4) & (2 * kInfo - 1);
 #pragma unroll
         for (int i = 0; i < VN; ++i) {
-            const int id = i * 256 + tid, quad = id / CH8, ch = (id - quad * CH8) * 8;
+            const int id = i * THREADS + tid, quad = id / CH8, ch = (id - quad * CH8) * 8;
+            if (VN * THREADS == kTokens / 4 * CH8 || id < kTokens / 4 * CH8) {
+                const uint8_t* v = gv[g0 + (quad >> 2)] + ((quad & 3) * 4 * (int)p.c.v_token + (ch < p.c.dim ? ch : 0)) * W;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) vreg[i][e] = VPiece{};
-            if (id < kTokens / 4 * CH8 && ch < p.c.dim) {
-                const int g = g0 + (quad >> 2), where = gpage[g];
-                if (where >= 0) {
-                    const int base = gbase[g];
-                    const int slot = base - (int)fdiv((uint32_t)base, p.div_page) * p.c.page + (quad & 3) * 4;
-                    const uint8_t* v = (const uint8_t*)p.c.v + (where * p.c.v_page + slot * p.c.v_token + h * p.c.v_head + ch) * W;
-                    const int j = base + (quad & 3) * 4;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)   // a token that no row sees weighs nothing, whatever its place holds
-                        if (j + e <= pmax && (p.a.window == 0 || pmin - (j + e) < p.a.window || j + e < p.a.sinks))
-                            vreg[i][e] = *reinterpret_cast<const VPiece*>(v + e * p.c.v_token * W);
-                }
+                for (int e = 0; e < 4; ++e) vreg[i][e] = *reinterpret_cast<const VPiece*>(v + e * (int)p.c.v_token * W);
             }
         }
     };
-    auto put = [&]() {
+    // Addresses in LDS are built from the step's buffer, so that they are
+    // computed where they are used instead of held in registers throughout.
+    auto put_k = [&](int at) {
+        if (p.c.dim < D)
+#pragma unroll
+            for (int i = 0; i < KN; ++i)
+                if ((i * THREADS + tid) % PIECES * (16 / W) >= p.c.dim) kreg[i] = u32x4{0, 0, 0, 0};
 #pragma unroll
         for (int i = 0; i < KN; ++i) {
-            const int id = i * 256 + tid, tok = id / PIECES, pc = id - tok * PIECES;
-            if (id < kTokens * PIECES) {
+            const int id = i * THREADS + tid, tok = id / PIECES, pc = id - tok * PIECES;
+            if (KN * THREADS == kTokens * PIECES || id < kTokens * PIECES) {
                 if constexpr (HELD8) {
                     u32x4 a, d;
 #pragma unroll
@@ -180,100 +217,181 @@ __global__ void __launch_bounds__(256) k_tile(AttendArgs p) {
                         d[2 * k] = T::template from_e4m3<false>(kreg[i][k + 2]);
                         d[2 * k + 1] = T::template from_e4m3<true>(kreg[i][k + 2]);
                     }
-                    *reinterpret_cast<u32x4*>(ldsk + tok * KP + pc * 32) = a;
-                    *reinterpret_cast<u32x4*>(ldsk + tok * KP + pc * 32 + 16) = d;
+                    *reinterpret_cast<u32x4*>(lds + at + tok * KP + pc * 32) = a;
+                    *reinterpret_cast<u32x4*>(lds + at + tok * KP + pc * 32 + 16) = d;
                 } else {
-                    *reinterpret_cast<u32x4*>(ldsk + tok * KP + pc * 16) = kreg[i];
+                    *reinterpret_cast<u32x4*>(lds + at + tok * KP + pc * 16) = kreg[i];
                 }
+            }
+        }
+    };
+    auto put_v = [&](int step, int buf) {
+        const int g0 = (step * 4) & (2 * kInfo - 1);
+        if (!all_see(step)) {   // a token that no row sees weighs nothing, whatever its place holds
+#pragma unroll
+            for (int i = 0; i < VN; ++i) {
+                const int quad = (i * THREADS + tid) / CH8 % (kTokens / 4);
+                const int j = gbase[g0 + (quad >> 2)] + (quad & 3) * 4;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (!((j + e <= pmax) & ((pmin - (j + e) < win) | (j + e < p.a.sinks)))) vreg[i][e] = VPiece{};
             }
         }
 #pragma unroll
         for (int i = 0; i < VN; ++i) {
-            const int id = i * 256 + tid, quad = id / CH8, c8 = id - quad * CH8;
-            if (id < kTokens / 4 * CH8) {
+            const int id = i * THREADS + tid, quad = id / CH8, c8 = id - quad * CH8;
+            if (VN * THREADS == kTokens / 4 * CH8 || id < kTokens / 4 * CH8) {
                 // Of each 16 tokens: pair 0 holds quads 0 and 2, pair 1 quads 1 and 3.
                 const int pair = (quad >> 2) * 2 + (quad & 1), half = (quad >> 1) & 1;
+                // The scale's power of two goes in with the conversion.
+                const float vs = HELD8 ? gvs[g0 + (quad >> 2)] : 1.0f;
+                const int at = buf + c8 * 1024 + half * 8 + ((pair ^ ((c8 & 1) * 4) ^ (c8 & 7)) << 4);
 #pragma unroll
                 for (int t = 0; t < 8; ++t) {
                     uint32_t w[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         if constexpr (HELD8)
-                            w[e] = (t & 2) ? V::template from_e4m3<true>(vreg[i][e][t >> 2]) : V::template from_e4m3<false>(vreg[i][e][t >> 2]);
+                            w[e] = (t & 2) ? bf16_from_e4m3<true>(vreg[i][e][t >> 2], vs) : bf16_from_e4m3<false>(vreg[i][e][t >> 2], vs);
                         else
                             w[e] = vreg[i][e][t >> 1];
                     }
                     const uint32_t sel = (t & 1) ? 0x07060302u : 0x05040100u;
-                    const int d = c8 * 8 + t, col = pair ^ (((d >> 1) ^ (d >> 3)) & 7);
-                    *reinterpret_cast<u32x2*>(ldsv + d * 128 + col * 16 + half * 8) =
+                    *reinterpret_cast<u32x2*>(lds + (at ^ ((t >> 1) << 4)) + t * 128) =
                         u32x2{__builtin_amdgcn_perm(w[1], w[0], sel), __builtin_amdgcn_perm(w[3], w[2], sel)};
                 }
             }
         }
     };
-
-    if (st0 < st1) {
-        look_up((st0 * 4) & ~(kInfo - 1));
-        __syncthreads();
-        fetch(st0);
-    }
-    for (int st = st0; st < st1; ++st) {
-        put();
-        const int gi = (st * 4) & (kInfo - 1);
-        // This step's groups, before the next ones may replace them.
-        int base[4];
-        float f2[4], vs[4];
+    f32x16 sc[2];
+    f32x16 sn[2];
+    // The products go in groups of NT: four groups of key products (32 tokens,
+    // half of the channels), four of value products (16 tokens).  A group's
+    // operands are read while the one before it is multiplied.
+    struct Part {
+        u32x4 w[NT];
+    };
+    auto read_k = [&](Part& f, int at, int g) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            base[i] = __builtin_amdgcn_readfirstlane(gbase[gi + i]);
-            f2[i] = gks[gi + i];
-            vs[i] = gvs[gi + i];
-        }
-        __syncthreads();
-        if (st + 1 < st1) {
-            if (((st + 1) * 4 & (kInfo - 1)) == 0) {
-                look_up((st + 1) * 4);
-                __syncthreads();
+        for (int i = 0; i < NT; ++i)
+            f.w[i] = *reinterpret_cast<const u32x4*>(lds + at + ((g >> 1) * 32 + r) * KP + ((g & 1) * NT + i) * 32 + hh * 16);
+    };
+    auto mul_k = [&](const Part& f, int g) {
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            const u32x4 w = f.w[i];
+            if ((g & 1) == 0 && i == 0) {
+                f32x16 zero;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) zero[e] = 0.0f;
+                sn[g >> 1] = T::mfma32(__builtin_bit_cast(x8, w), q[0], zero);
+            } else {
+                sn[g >> 1] = T::mfma32(__builtin_bit_cast(x8, w), q[(g & 1) * NT + i], sn[g >> 1]);
             }
-            fetch(st + 1);
         }
-        bool full = true, any = false;
+    };
+    auto read_v = [&](Part& f, int vat, int z) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) f.w[t] = *reinterpret_cast<const u32x4*>(lds + (vat ^ (((z * 2) ^ ((t & 1) * 4)) << 4)) + t * 4096);
+    };
+    // Whether a step is seen by all of the wave's rows whole, by none at all.
+    auto sight = [&](int step, bool& full, bool& any) {
+        const int g0 = (step * 4) & (2 * kInfo - 1);
+        full = true, any = false;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            full = full && base[i] <= wmin - 15 && (p.a.window == 0 || wmax - base[i] < p.a.window || base[i] + 15 < p.a.sinks);
-            any = any || (base[i] <= wmax && (p.a.window == 0 || wmin - base[i] - 15 < p.a.window || base[i] < p.a.sinks));
+            const int base = __builtin_amdgcn_readfirstlane(gbase[g0 + i]);
+            full = full & (base <= wmin - 15) & ((wmax - base < win) | (base + 15 < p.a.sinks));
+            any = any | ((base <= wmax) & ((wmin - base - 15 < win) | (base < p.a.sinks)));
         }
-        if (any) {
-            f32x16 sc[2];
+    };
+    auto mask = [&](int step) {
+        const int g0 = (step * 4) & (2 * kInfo - 1);
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
+        for (int z = 0; z < 4; ++z) {   // 16 tokens; `d` tokens back from the row lies the lane's first
+            const int base = __builtin_amdgcn_readfirstlane(gbase[g0 + z]);
+            const int d = pos - base - hh * 4;
+            const uint32_t w = (uint32_t)win;
+            const int sk = p.a.sinks - base - hh * 4;
+            if (base < p.a.sinks) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) sc[u][i] = 0.0f;
-#pragma unroll
-                for (int k = 0; k < KS; ++k) {
-                    const x8 kk = *reinterpret_cast<const x8*>(ldsk + (u * 32 + r) * KP + k * 32 + hh * 16);
-                    sc[u] = T::mfma32(kk, q[k], sc[u]);
+                for (int i = 0; i < 8; ++i) {
+                    const int t = (i >> 2) * 8 + (i & 3);
+                    if (!(((uint32_t)(d - t) < w) | ((t < sk) & (t <= d)))) sc[z >> 1][(z & 1) * 8 + i] = neg_inf();
                 }
-            }
-            if (full) {
-#pragma unroll
-                for (int u = 0; u < 2; ++u)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) sc[u][i] *= f2[u * 2 + (i >> 3)];
             } else {
 #pragma unroll
-                for (int u = 0; u < 2; ++u)
+                for (int i = 0; i < 8; ++i) {
+                    const int t = (i >> 2) * 8 + (i & 3);
+                    if (!((uint32_t)(d - t) < w)) sc[z >> 1][(z & 1) * 8 + i] = neg_inf();
+                }
+            }
+        }
+    };
+
+    // The steps' pipeline: while step st's weights are taken and multiplied
+    // with its values, step st + 1's scores are already under way (independent
+    // matrix products to fill the exponentials' time), its values and step
+    // st + 2's keys are brought into LDS, and what follows is being read.
+    bool any = false;
+    if (st0 < st1) {
+        look_up((st0 * 4) & ~(kInfo - 1));
+        if ((st0 * 4 & (kInfo - 1)) + 16 > kInfo) look_up((st0 * 4 & ~(kInfo - 1)) + kInfo);
+        __syncthreads();
+        fetch_k(st0);
+        fetch_v(st0);
+        put_k(0);
+        put_v(st0, 2 * KB);
+        if (st0 + 1 < st1) fetch_k(st0 + 1);
+        __syncthreads();
+        bool full;
+        sight(st0, full, any);
+        {
+            Part f;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const int j = base[u * 2 + (i >> 3)] + ((i >> 2) & 1) * 8 + hh * 4 + (i & 3);
-                        sc[u][i] = sees(p, pos, j) ? sc[u][i] * f2[u * 2 + (i >> 3)] : neg_inf();
-                    }
+            for (int g = 0; g < 4; ++g) {
+                read_k(f, 0, g);
+                mul_k(f, g);
+            }
+            sc[0] = sn[0];
+            sc[1] = sn[1];
+        }
+        if (!full) mask(st0);
+        if (st0 + 1 < st1) {
+            put_k(KB);
+            fetch_v(st0 + 1);
+            if (st0 + 2 < st1) fetch_k(st0 + 2);
+        }
+        __syncthreads();
+    }
+    for (int st = st0; st < st1; ++st) {
+        const int odd = (st - st0) & 1;
+        const int kat = odd ? 0 : KB;                     // step st + 1's keys
+        const int vat0 = 2 * KB + (odd ? VB : 0);         // step st's values
+        const int vat = vat0 + r * 128 + ((hh ^ (((r >> 1) ^ (r >> 3)) & 7)) << 4);
+        const int gi = (st * 4) & (2 * kInfo - 1);
+        const bool more = st + 1 < st1;
+        bool full = true, next = more;
+        if (more && !all_see(st + 1)) sight(st + 1, full, next);
+        if (any | next) {
+            Part fa, fb;
+            read_k(fa, kat, 0);
+            f32x4 f2, lg, rv;
+            if constexpr (HELD8) {
+                f2 = *reinterpret_cast<const f32x4*>(gks + gi);
+                lg = *reinterpret_cast<const f32x4*>(glg + gi);
+                rv = *reinterpret_cast<const f32x4*>(grv + gi);
+            } else {
+                f2 = f32x4{p.factor, p.factor, p.factor, p.factor};
             }
             float top = neg_inf();
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
+            for (int z = 0; z < 4; ++z) {
+                float t = neg_inf();
 #pragma unroll
-                for (int i = 0; i < 16; ++i) top = fmaxf(top, sc[u][i]);
+                for (int i = 0; i < 8; ++i) t = fmaxf(t, sc[z >> 1][(z & 1) * 8 + i]);
+                top = fmaxf(top, t * f2[z]);
+            }
             if (__any(top > m + kSlack)) {
                 top = max32(fmaxf(top, m));
                 const float a = top == neg_inf() ? 1.0f : exp2_(m - top);
@@ -285,32 +403,62 @@ __global__ void __launch_bounds__(256) k_tile(AttendArgs p) {
                     for (int i = 0; i < 16; ++i) o[t][i] *= a;
             }
             const float ref = m == neg_inf() ? 0.0f : m;
+            u32x4 w[4], w2[4];
+            // Weights of 4 of a lane's 8 tokens of 16.
+            auto weigh = [&](int z, int half) {
+                float e[4];
+                const float c = HELD8 ? lg[z] - ref : -ref;
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
+                for (int i = 0; i < 4; ++i) e[i] = exp2_(__builtin_fmaf(sc[z >> 1][(z & 1) * 8 + half * 4 + i], f2[z], c));
+                const float s4 = (e[0] + e[1]) + (e[2] + e[3]);
+                if constexpr (HELD8)
+                    l = __builtin_fmaf(s4, rv[z], l);
+                else
+                    l += s4;
 #pragma unroll
-                for (int z = 0; z < 2; ++z) {   // 16 tokens
-                    float e[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        e[i] = exp2_(sc[u][z * 8 + i] - ref);
-                        l += e[i];
-                        if constexpr (HELD8) e[i] *= vs[u * 2 + z];
-                    }
-                    u32x4 w, w2;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        w[i] = pack2<V>(e[2 * i], e[2 * i + 1]);
-                        if constexpr (kTwo) w2[i] = pack2<V>(e[2 * i] - lo16<V>(w[i]), e[2 * i + 1] - hi16<V>(w[i]));
-                    }
-#pragma unroll
-                    for (int t = 0; t < NT; ++t) {
-                        const int d = t * 32 + r, pair = (u * 2 + z) * 2 + hh;
-                        const auto vv = *reinterpret_cast<const typename V::x8*>(
-                            ldsv + d * 128 + ((pair ^ (((d >> 1) ^ (d >> 3)) & 7)) * 16));
-                        o[t] = V::mfma32(vv, __builtin_bit_cast(typename V::x8, w), o[t]);
-                        if constexpr (kTwo) o[t] = V::mfma32(vv, __builtin_bit_cast(typename V::x8, w2), o[t]);
-                    }
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t x = pack2<V>(e[2 * i], e[2 * i + 1]);
+                    w[z][half * 2 + i] = x;
+                    if constexpr (kTwo) w2[z][half * 2 + i] = pack2<V>(e[2 * i] - lo16<V>(x), e[2 * i + 1] - hi16<V>(x));
                 }
+            };
+            auto mul_v = [&](const Part& f, int z) {
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    const u32x4 x = f.w[t];
+                    o[t] = V::mfma32(__builtin_bit_cast(typename V::x8, x), __builtin_bit_cast(typename V::x8, w[z]), o[t]);
+                    if constexpr (kTwo) o[t] = V::mfma32(__builtin_bit_cast(typename V::x8, x), __builtin_bit_cast(typename V::x8, w2[z]), o[t]);
+                }
+            };
+            PHASE_END
+            read_k(fb, kat, 1), mul_k(fa, 0), weigh(0, 0);
+            PHASE_END
+            read_k(fa, kat, 2), mul_k(fb, 1), weigh(0, 1);
+            PHASE_END
+            read_v(fb, vat, 0), mul_k(fa, 2), weigh(1, 0);
+            PHASE_END
+            read_k(fa, kat, 3), mul_v(fb, 0), weigh(1, 1);
+            PHASE_END
+            read_v(fb, vat, 1), mul_k(fa, 3), weigh(2, 0);
+            PHASE_END
+            read_v(fa, vat, 2), mul_v(fb, 1), weigh(2, 1);
+            PHASE_END
+            read_v(fb, vat, 3), mul_v(fa, 2), weigh(3, 0), weigh(3, 1);
+            PHASE_END
+            mul_v(fb, 3);
+            sc[0] = sn[0];
+            sc[1] = sn[1];
+            if (!full) mask(st + 1);
+        }
+        any = next;
+        if (more) {
+            put_v(st + 1, 2 * KB + (odd ? 0 : VB));
+            if (st + 2 < st1) {
+                put_k(odd ? KB : 0);
+                fetch_v(st + 2);
+                if (st + 3 < st1) fetch_k(st + 3);
+            }
+            if (((st + 4) * 4 & (kInfo - 1)) == 0 && st + 4 < st1) look_up((st + 4) * 4);
         }
         __syncthreads();
     }
@@ -318,7 +466,7 @@ __global__ void __launch_bounds__(256) k_tile(AttendArgs p) {
     l = sum32(l);
     if (!there) return;
     if (p.splits > 1) {
-        float* part = p.tile_parts + ((uint64_t)(x * p.c.kv_heads + h) * p.splits + split) * tile_part_floats(D);
+        float* part = p.tile_parts + ((uint64_t)(x * p.c.kv_heads + h) * p.splits + split) * tile_part_floats(D, p.tile_rows);
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -326,8 +474,8 @@ __global__ void __launch_bounds__(256) k_tile(AttendArgs p) {
                 *reinterpret_cast<f32x4*>(part + row * D + t * 32 + i * 2 + hh * 4) =
                     m == neg_inf() ? f32x4{0, 0, 0, 0} : f32x4{o[t][i], o[t][i + 1], o[t][i + 2], o[t][i + 3]};
         if (hh == 0) {
-            part[kTileRows * D + row] = m;
-            part[kTileRows * D + kTileRows + row] = l;
+            part[p.tile_rows * D + row] = m;
+            part[p.tile_rows * D + p.tile_rows + row] = l;
         }
         return;
     }
@@ -366,19 +514,19 @@ __global__ void __launch_bounds__(256) k_tile_join(AttendArgs p) {
     const int t0 = (x - s.row0 / p.tile_tokens - b) * p.tile_tokens;
     if (t0 < 0 || t0 >= s.n) return;
     const int tn = s.n - t0 < p.tile_tokens ? s.n - t0 : p.tile_tokens;
-    const float* base = p.tile_parts + (uint64_t)(x * p.c.kv_heads + h) * p.splits * tile_part_floats(D);
+    const float* base = p.tile_parts + (uint64_t)(x * p.c.kv_heads + h) * p.splits * tile_part_floats(D, p.tile_rows);
     for (int row = blockIdx.y * 4 + wave; row < tn * p.group; row += gridDim.y * 4) {
         float top = neg_inf();
-        for (int i = 0; i < p.splits; ++i) top = fmaxf(top, base[i * tile_part_floats(D) + kTileRows * D + row]);
+        for (int i = 0; i < p.splits; ++i) top = fmaxf(top, base[i * tile_part_floats(D, p.tile_rows) + p.tile_rows * D + row]);
         float sum = 0.0f, y[D / 64 + 1];
 #pragma unroll
         for (int k = 0; k < D / 64 + 1; ++k) y[k] = 0.0f;
         for (int i = 0; i < p.splits; ++i) {
-            const float* part = base + i * tile_part_floats(D);
-            const float mp = part[kTileRows * D + row];
+            const float* part = base + i * tile_part_floats(D, p.tile_rows);
+            const float mp = part[p.tile_rows * D + row];
             if (mp == neg_inf()) continue;
             const float a = exp2_(mp - top);
-            sum += part[kTileRows * D + kTileRows + row] * a;
+            sum += part[p.tile_rows * D + p.tile_rows + row] * a;
 #pragma unroll
             for (int k = 0; k < D / 64 + 1; ++k)
                 if (k * 64 + lane < D) y[k] += part[row * D + k * 64 + lane] * a;
@@ -398,8 +546,10 @@ template <typename T, bool HELD8, int D>
 static hipError_t go(const AttendArgs& p, bool join, hipStream_t st) {
     if (join)
         k_tile_join<T, D><<<dim3((unsigned)(p.tiles * p.c.kv_heads), 4), 256, 0, st>>>(p);
+    else if (p.tile_rows == 256)
+        k_tile<T, HELD8, D, 8><<<(unsigned)(p.tiles * p.c.kv_heads * p.splits), 512, 0, st>>>(p);
     else
-        k_tile<T, HELD8, D><<<(unsigned)(p.tiles * p.c.kv_heads * p.splits), 256, 0, st>>>(p);
+        k_tile<T, HELD8, D, 4><<<(unsigned)(p.tiles * p.c.kv_heads * p.splits), 256, 0, st>>>(p);
     return hipGetLastError();
 }
 
