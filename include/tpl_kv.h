@@ -9,8 +9,8 @@
  * lengths[b] - (starts[b+1] - starts[b]) + i.
  *
  * Values are held in the tensors' own 16-bit type, or in e4m3 with one fp32
- * scale, over zero, for each block of `block` tokens and head: value = e4m3 *
- * scale.  (Scales under 2^-126 count as 2^-126.)
+ * scale over zero for each block of `block` tokens and head: value = e4m3 *
+ * scale.  (Scales under 2^-126 may count as 2^-126.)
  *
  * starts, lengths and table are read on the device only, so both calls can be
  * captured into a graph and replayed on new lengths.  Rows and pages that they
@@ -115,9 +115,12 @@ int tpl_kv_append(const tpl_kv_cache *cache, const tpl_kv_batch *batch,
  * an lse of minus infinity.
  *
  * `workspace` is device memory of at least tpl_kv_attend_workspace() bytes,
- * 16-byte aligned, not shared with work on another stream until this call's
- * work has ended; it needs no initial values and keeps none.
+ * 16-byte aligned.  Its first TPL_KV_COUNTERS bytes (or all of it, if it is
+ * smaller) must be zero before the first call that it is given to; every call
+ * leaves them zero, so that one workspace serves any number of calls on one
+ * stream.  Calls that may run at the same time need one each.
  */
+#define TPL_KV_COUNTERS 4096
 int tpl_kv_attend(const tpl_kv_cache *cache, const tpl_kv_batch *batch,
                   const tpl_kv_query *args, void *workspace, int64_t workspace_bytes,
                   hipStream_t stream);

@@ -1,12 +1,14 @@
 // kv_attend.hip -- attention to a paged key/value cache: checks of arguments,
 // choice of the kernels, C entry points.
 #include <climits>
-#include <cstdlib>
 
 #include "kv_attend.hpp"
 
 namespace tpl {
 namespace kv {
+
+constexpr int kCUs = 256;
+constexpr int kCounters = TPL_KV_COUNTERS / 4;   // at least the split kernel's workgroups
 
 bool aligned16(const void* p, int64_t s0, int64_t s1, int bytes) {
     return ((uintptr_t)p & 15) == 0 && (s0 * bytes) % 16 == 0 && (s1 * bytes) % 16 == 0;
@@ -18,9 +20,11 @@ const char* check_cache(const tpl_kv_cache* c) {
     if (!c->k || !c->v) return "cache pools must not be NULL";
     if (c->pages < 1 || c->pages > INT_MAX) return "a cache must have at least one page";
     if (c->dim < 16 || c->dim > 256 || c->dim % 16) return "dim must be a multiple of 16, at most 256";
-    if (c->kv_heads < 1 || c->kv_heads > 65535) return "kv_heads must be 1 .. 65535";
-    if (c->page < 16 || c->page % 16) return "page must be a multiple of 16 tokens";
+    if (c->kv_heads < 1 || c->kv_heads > kCounters) return "kv_heads must be 1 .. 1024";
+    if (c->page < 16 || c->page % 16 || c->page > (1 << 20)) return "page must be a multiple of 16 tokens, at most 2^20";
     const int w = c->type == TPL_KV_E4M3 ? 1 : 2;
+    for (int64_t x : {c->k_token, c->v_token, c->k_page, c->v_page, c->ks_page, c->vs_page, c->ks_block, c->vs_block})
+        if (x > ((int64_t)1 << 40) || x < -((int64_t)1 << 40)) return "strides must be under 2^40";
     if (c->type == TPL_KV_E4M3) {
         if (!c->k_scale || !c->v_scale) return "an e4m3 cache needs its scales";
         if (c->block < 16 || c->block % 16 || c->page % c->block)
@@ -29,8 +33,18 @@ const char* check_cache(const tpl_kv_cache* c) {
     if (!aligned16(c->k, c->k_token, c->k_head, w) || !aligned16(c->v, c->v_token, c->v_head, w) ||
         (c->k_page * w) % 16 || (c->v_page * w) % 16)
         return "cache pools must start, and their pages, tokens and heads lie, on 16 bytes";
-    if (c->k_token < 0 || c->v_token < 0 || c->k_token > (1 << 24) || c->v_token > (1 << 24))
-        return "tokens of a page must lie at most 2^24 elements apart";
+    // Offsets inside a page, and its size, are 32-bit numbers in the kernels.
+    const int64_t in_page[] = {c->k_token * w * c->page, c->v_token * w * c->page, c->k_token, c->v_token};
+    for (int64_t x : in_page)
+        if (x < 0 || x > INT_MAX) return "a page's tokens must lie within 2^31 bytes";
+    const int64_t page_of[] = {c->k_page * w, c->v_page * w};
+    for (int64_t x : page_of)
+        if (x < 0 || x > UINT32_MAX) return "pages must lie at most 2^32 bytes apart";
+    if (c->type == TPL_KV_E4M3) {
+        const int64_t s[] = {c->ks_page, c->vs_page, c->ks_block * c->page, c->vs_block * c->page};
+        for (int64_t x : s)
+            if (x < 0 || x > INT_MAX) return "a page's scales must lie within 2^31 elements";
+    }
     return nullptr;
 }
 
@@ -44,13 +58,10 @@ const char* check_batch(const tpl_kv_cache& c, const tpl_kv_batch* g) {
     return nullptr;
 }
 
-constexpr int kCUs = 256;
-
 struct Choice {
     bool few, tile;
     int dc, mr, dk;
     int64_t few_bytes, tile_bytes;
-    bool join;
 };
 
 static const char* choose(const tpl_kv_cache* c, const tpl_kv_batch* g, const tpl_kv_query* a, AttendArgs& p, Choice& q,
@@ -76,6 +87,7 @@ static const char* choose(const tpl_kv_cache* c, const tpl_kv_batch* g, const tp
     p.a = *a;
     if (c->type != TPL_KV_E4M3) p.c.block = c->page;
     if (a->window == 0) p.a.sinks = 0;
+    p.counters = nullptr;
     p.parts = p.tile_parts = nullptr;
     p.group = a->heads / c->kv_heads;
     p.cap = g->width * c->page;
@@ -111,18 +123,35 @@ static const char* choose(const tpl_kv_cache* c, const tpl_kv_batch* g, const tp
         int64_t mean = (rows + g->batch - 1) / g->batch;
         if (mean > limit) mean = p.group;
         q.mr = mean <= 16 ? 1 : mean <= 32 || q.dc > 8 ? 2 : 4;
+        // No more shares than steps there can be.
         const int64_t tiles = (rows + q.mr * 16 - 1) / (q.mr * 16) + g->batch;
-        int64_t steps = ((int64_t)p.cap + 127) / 128 + 1;
-        q.join = steps > 2;
-        const int64_t most = tiles * c->kv_heads * steps;
-        p.workers = kCUs * (q.mr * q.dc <= 8 ? 4 : 2);
-        if (p.workers > most) p.workers = (int)most;
-        if ((int64_t)g->batch * c->kv_heads > INT_MAX) return "batch * kv_heads must be under 2^31";
-        q.few_bytes = (int64_t)p.workers * 2 * (q.mr * 16 * (16 * q.dc + 2)) * 4;
+        const int64_t most = tiles * (((int64_t)p.cap + 31) / 32 + 1);
+        // Two heads a workgroup where they lie next to each other within 256
+        // bytes and a share is long: it then reads whole 256 bytes of a token.
+        // 64 sequences of up to 8192 tokens (64 steps a share at most): 157
+        // against 175 us; 32 of up to 4096 (16 steps), where the parts that
+        // are left weigh more: 55 against 50 us.
+        int64_t seen = p.cap;
+        if (a->window && (int64_t)a->window + a->sinks < seen) seen = (int64_t)a->window + a->sinks;
+        const int64_t blocks = kCUs * few_blocks(c->type == TPL_KV_E4M3, q.dc, q.mr);
+        const int w = c->type == TPL_KV_E4M3 ? 1 : 2;
+        p.heads_log = c->kv_heads % 2 == 0 && c->k_head * w < 256 && c->k_head < c->k_token && c->v_head < c->v_token &&
+                      g->batch * (seen / 128) * c->kv_heads >= 32 * blocks ? 1 : 0;
+        int64_t shares = blocks / (c->kv_heads >> p.heads_log);
+        if (shares > most) shares = most;
+        p.shares = shares < 1 ? 1 : (int)shares;
+        q.few_bytes = kCounters * 4 + (int64_t)p.shares * c->kv_heads * 2 * few_part_floats(q.dc, q.mr) * 4;
     }
     if (q.tile) {
         q.dk = c->dim <= 64 ? 64 : c->dim <= 96 ? 96 : c->dim <= 128 ? 128 : c->dim <= 192 ? 192 : 256;
-        p.tile_rows = getenv("R8") ? 256 : 128;
+        // Row tiles of 256 (8 waves that share a step's keys and values) where
+        // they still give every CU two, else of 128.  One prompt of 8192
+        // tokens, 32 heads of 128: 572 against 598 us; a chunk of 1024 tokens
+        // (128 tiles of 256): 169 against 139 us.  Under a window larger tiles
+        // see more that most of their rows do not (window 1024: 178 against
+        // 158 us), and longer heads do not fit 8 waves' registers.
+        const bool large = q.dk <= 128 && a->window == 0 && rows / 256 * c->kv_heads >= 2 * kCUs;
+        p.tile_rows = large ? 256 : 128;
         p.tile_tokens = p.tile_rows / p.group;
         const int64_t tiles = (int64_t)g->tokens / p.tile_tokens + g->batch;
         const int64_t units = tiles * c->kv_heads;
@@ -153,11 +182,12 @@ static int attend_impl(const tpl_kv_cache* c, const tpl_kv_batch* g, const tpl_k
         return fail_status(TPL_E_LAYOUT, "q and out must start, and their rows and heads lie, on 16 bytes");
     if (q.few_bytes + q.tile_bytes > 0 && (!ws || ((uintptr_t)ws & 15))) return fail_status(TPL_E_ARG, "workspace must lie on 16 bytes");
     if (ws_bytes < q.few_bytes + q.tile_bytes) return fail_status(TPL_E_ARG, "workspace is too small");
-    p.parts = (float*)ws;
+    p.counters = (int*)ws;
+    p.parts = (float*)((char*)ws + kCounters * 4);
     p.tile_parts = (float*)((char*)ws + q.few_bytes);
     hipError_t e = hipSuccess;
     if (q.tile) e = launch_tile(p, q.dk, false, st);
-    if (e == hipSuccess && q.few) e = launch_few(p, q.dc, q.mr, q.join, st);
+    if (e == hipSuccess && q.few) e = launch_few(p, q.dc, q.mr, st);
     if (e == hipSuccess && q.tile && p.splits > 1) e = launch_tile(p, q.dk, true, st);
     if (e != hipSuccess) return fail_status(TPL_E_HIP, std::string("HIP launch failed: ") + hipGetErrorString(e));
     return TPL_OK;

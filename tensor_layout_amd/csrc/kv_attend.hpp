@@ -18,6 +18,7 @@ struct AttendArgs {
     tpl_kv_cache c;
     tpl_kv_batch g;
     tpl_kv_query a;
+    int* counters;     // workspace: parts of a row tile that are there, zero between calls
     float* parts;      // workspace: partial results
     FastDiv div_page, div_block, div_group;
     float factor;      // scale * log2 e
@@ -25,7 +26,8 @@ struct AttendArgs {
     int32_t cap;       // tokens that a table row can hold
     // Split kernel (few rows a sequence)
     int32_t few;       // it takes sequences of at most this many rows (new tokens * group)
-    int32_t workers;   // its workgroups
+    int32_t shares;    // its workgroups for each set of heads
+    int32_t heads_log; // a workgroup takes 1 << heads_log of the cache's heads
     // Tile kernel (many rows a sequence)
     int32_t tile_rows;     // 128 or 256
     int32_t tile_tokens;   // new tokens of a row tile
@@ -33,6 +35,9 @@ struct AttendArgs {
     int32_t splits;        // parts of each tile's tokens
     float* tile_parts;
 };
+
+// Where a token stands that is not there: beyond every position.
+constexpr int kNowhere = 0x7fffff00;
 
 // The tokens that a range of rows sees, as groups of 16 consecutive tokens:
 // first `na` groups from token 0 (the sinks, where they lie before the
@@ -64,8 +69,11 @@ __device__ __forceinline__ Span span_of(const AttendArgs& p, int first_pos, int 
     return s;
 }
 
-__device__ __forceinline__ bool sees(const AttendArgs& p, int pos, int j) {
-    return j <= pos && (p.a.window == 0 || pos - j < p.a.window || j < p.a.sinks);
+// A number that no kernel of the call writes, at an address that is the same
+// in every lane: by the scalar path.
+template <typename X>
+__device__ __forceinline__ X scalar(const X* p) {
+    return *(const __attribute__((address_space(4))) X*)(uintptr_t)p;
 }
 
 __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
@@ -89,20 +97,26 @@ __device__ __forceinline__ float max16(float x) { const float2 r = swap16(x); re
 __device__ __forceinline__ float sum32(float x) { const float2 r = swap32(x); return r.x + r.y; }
 __device__ __forceinline__ float sum16(float x) { const float2 r = swap16(x); return r.x + r.y; }
 
-// The split kernel's rows of a tile and tokens of a step: 4 waves of 32.
+// A number that is the same in every lane, in a scalar register.
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ uint64_t uniform(uint64_t x) {
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)x), hi = __builtin_amdgcn_readfirstlane((uint32_t)(x >> 32));
+    return ((uint64_t)hi << 32) | lo;
+}
+
+// Groups of 16 tokens of a split kernel's step where its 4 waves, 2 groups
+// each, are on one head.
 constexpr int kStepGroups = 8;
 
 struct FewSeq {
     Seq s;
     Span span;
     int tiles;      // row tiles
-    int steps;      // steps of one row tile of one head, at least 1
-    __device__ __forceinline__ uint64_t all(const AttendArgs& p) const {
-        return (uint64_t)tiles * (uint32_t)p.c.kv_heads * (uint32_t)steps;
-    }
+    int steps;      // steps of one row tile, at least 1
+    __device__ __forceinline__ uint64_t all() const { return (uint64_t)tiles * (uint32_t)steps; }
 };
 
-template <int ROWS>
+template <int ROWS, bool UNIFORM>
 __device__ __forceinline__ FewSeq few_seq(const AttendArgs& p, int b) {
     FewSeq f;
     f.s = read_seq(p.g, b);
@@ -110,19 +124,29 @@ __device__ __forceinline__ FewSeq few_seq(const AttendArgs& p, int b) {
     if (rows > p.few) f.s.n = 0;
     f.tiles = f.s.n ? (int)((rows + ROWS - 1) / ROWS) : 0;
     f.span = span_of(p, f.s.length - f.s.n, f.s.length - 1);
-    f.steps = (f.span.n + kStepGroups - 1) / kStepGroups;
+    const int log = 3 - p.heads_log;   // kStepGroups a wave's share of them
+    f.steps = (f.span.n + (1 << log) - 1) >> log;
     if (f.steps < 1) f.steps = 1;
+    if constexpr (UNIFORM) {   // the same sequence in every lane
+        f.s.row0 = uniform(f.s.row0);
+        f.s.n = uniform(f.s.n);
+        f.s.length = uniform(f.s.length);
+        f.span.na = uniform(f.span.na);
+        f.span.lo = uniform(f.span.lo);
+        f.span.n = uniform(f.span.n);
+        f.tiles = uniform(f.tiles);
+        f.steps = uniform(f.steps);
+    }
     return f;
 }
 
-// Rows before each sequence in the order of steps: every workgroup sums the
-// batch for itself (one load's latency for up to 256 sequences).  Afterwards
-// `total` is the sum over the batch, and the sequence that holds step `c`
-// has its number and its own first step in *at_b and *at_step.
+// The batch's steps in order: every workgroup sums them for itself (one
+// load's latency for up to 256 sequences).  Gives the total, the size of a
+// share, and the sequence that this share begins in (-1: none) with that
+// sequence's own first step.
 template <int ROWS>
-__device__ __forceinline__ uint64_t locate(const AttendArgs& p, bool by_seq, int want_b, int* at_b, uint64_t* at_step,
-                                           uint64_t* chunk) {
-    __shared__ uint64_t sums[5];
+__device__ __forceinline__ uint64_t locate(const AttendArgs& p, int share, int* at_b, uint64_t* at_step, uint64_t* chunk) {
+    __shared__ uint64_t sums[4];
     __shared__ uint64_t found_step;
     __shared__ int found_b;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -130,7 +154,7 @@ __device__ __forceinline__ uint64_t locate(const AttendArgs& p, bool by_seq, int
     uint64_t mine = 0;
     for (int i = 0; i < per; ++i) {
         const int b = tid * per + i;
-        if (b < p.g.batch) mine += few_seq<ROWS>(p, b).all(p);
+        if (b < p.g.batch) mine += few_seq<ROWS, false>(p, b).all();
     }
     uint64_t run = mine;
 #pragma unroll
@@ -148,14 +172,13 @@ __device__ __forceinline__ uint64_t locate(const AttendArgs& p, bool by_seq, int
         total += sums[w];
     }
     before += run - mine;
-    // Equal shares of the steps.
-    *chunk = (total + p.workers - 1) / (uint32_t)p.workers;
-    const uint64_t c = (uint64_t)blockIdx.x * *chunk;
-    if (by_seq ? (tid * per <= want_b && want_b < (tid + 1) * per) : (mine && before <= c && c < before + mine)) {
+    *chunk = (total + p.shares - 1) / (uint32_t)p.shares;
+    const uint64_t c = (uint64_t)share * *chunk;
+    if (mine && before <= c && c < before + mine) {
         for (int i = 0; i < per; ++i) {
             const int b = tid * per + i;
-            const uint64_t n = b < p.g.batch ? few_seq<ROWS>(p, b).all(p) : 0;
-            if (by_seq ? b == want_b : c < before + n) {
+            const uint64_t n = b < p.g.batch ? few_seq<ROWS, false>(p, b).all() : 0;
+            if (c < before + n) {
                 found_b = b;
                 found_step = before;
                 break;
@@ -164,17 +187,28 @@ __device__ __forceinline__ uint64_t locate(const AttendArgs& p, bool by_seq, int
         }
     }
     __syncthreads();
-    *at_b = found_b;
-    *at_step = found_step;
-    return total;
+    // The same in every lane, which the compiler has to be told for what
+    // follows from them to stay in scalar registers.
+    *at_b = uniform(found_b);
+    *at_step = uniform(found_step);
+    *chunk = uniform(*chunk);
+    return uniform(total);
 }
 
 // Part of a row tile that one workgroup of the split kernel leaves: rows of
-// 16 * DC sums, then the rows' references, then their sums of weights.
-template <int DC, int MR>
-constexpr int few_part_floats() { return MR * 16 * (16 * DC + 2); }
+// 16 * dc sums, then each row's reference and sum of weights.
+TPL_HD constexpr int few_part_floats(int dc, int mr) { return mr * 16 * (16 * dc + 2); }
 
-hipError_t launch_few(const AttendArgs& p, int dc, int mr, int join, hipStream_t st);
+// The split kernel's workgroups that a CU holds at once: two of its waves a
+// SIMD as far as 256 registers allow, else one.  The grid is that many for
+// every CU, so that equal shares end together.  Three a CU measured 3 to 20 %
+// slower (more parts to join), and holding the next step's loads in registers
+// as well gained nothing: two waves a SIMD keep HBM busy.
+TPL_HD constexpr int few_blocks(bool held8, int dc, int mr) {
+    return 4 * dc * (held8 ? 1 : 2) + 6 * mr * dc <= 200 ? 2 : 1;
+}
+
+hipError_t launch_few(const AttendArgs& p, int dc, int mr, hipStream_t st);
 hipError_t launch_tile(const AttendArgs& p, int dk, bool join, hipStream_t st);
 
 TPL_HD int tile_part_floats(int dk, int rows) { return rows * (dk + 2); }

@@ -4,12 +4,15 @@
 // out = sum_j w_j v_j / sum_j w_j, w_j = 2^(x_j - m), x = scale log2(e) q k,
 // with one running reference m a row.
 //
-// Bound: HBM bytes of the cache, read once.  So the token axis is split: the
-// batch's work is counted in steps of 128 tokens of one (sequence, head, row
-// tile), and every workgroup takes an equal share of consecutive steps,
-// whatever the sequences' lengths are.  Of a step each of 4 waves takes 32
-// tokens straight from HBM into registers: nothing is staged in LDS, because
-// no other wave needs the same values.
+// Bound: HBM bytes of the cache, read once.  So the token axis is split: a
+// head's work is counted in steps of 128 tokens of one (sequence, row tile),
+// and every workgroup takes an equal share of consecutive steps of one head,
+// whatever the sequences' lengths are.  Workgroups next to each other take
+// the same share of different heads: where heads lie next to each other in a
+// token's row, they read those rows at about the same time (64 sequences of
+// up to 8192 tokens, 8 heads of 128 bytes: see below).  Of a step each of 4
+// waves takes 32 tokens straight from HBM into registers: nothing is staged
+// in LDS, because no other wave needs the same values.
 //
 // Layout.  S^T = K Q^T with 16 tokens as the rows of a 16x16x32 product:
 // lane (r = lane % 16, g = lane / 16) holds channels of token r, and its part
@@ -65,43 +68,55 @@ struct Tile {
     int base;     // first token, or a number beyond every position
 };
 
+// Where a group of 16 tokens lies: its page's table entry, its first token's
+// place in the page, and that token (beyond every position past the span).
+struct Place {
+    int entry, slot, base;
+};
+
+__device__ __forceinline__ Place place_of(const AttendArgs& p, const int32_t* pages, const Span& span, int t) {
+    Place x;
+    const int base = span.base(t < span.n ? t : span.n - 1);
+    const int pg = (int)fdiv((uint32_t)base, p.div_page);
+    x.entry = scalar(pages + pg);
+    x.slot = base - pg * p.c.page;
+    x.base = t < span.n ? base : kNowhere;
+    return x;
+}
+
+// One head's keys, values and scales.
+struct Head {
+    const uint8_t *k, *v;
+    const float *ks, *vs;
+};
+
+// Loads without a branch, so that they are in flight together: a group that
+// is not there reads page 0 and stands beyond every position; lanes beyond
+// the head's channels read its first ones.
 template <bool HELD8, int DC>
-__device__ __forceinline__ void load_tile(const AttendArgs& p, const int32_t* pages, const Span& span, int t, int h,
-                                          Tile<HELD8, DC>& x) {
+__device__ __forceinline__ void load_tile(const AttendArgs& p, const Head& h, Place at, Tile<HELD8, DC>& x) {
     constexpr int W = HELD8 ? 1 : 2;
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
-    x.base = 0x7fffff00;
-    x.ks = x.vs = 0.0f;
-#pragma unroll
-    for (int i = 0; i < x.KL; ++i) x.k[i] = u32x4{0, 0, 0, 0};
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-#pragma unroll
-        for (int i = 0; i < (int)(sizeof(x.v[e]) / 4); ++i) x.v[e].w[i] = 0;
-    if (t >= span.n) return;
-    const int base = span.base(t);
-    const int pg = (int)fdiv((uint32_t)base, p.div_page), slot = base - pg * p.c.page;
-    const int where = pages[pg];
-    if (where < 0 || where >= p.c.pages) return;
-    x.base = base;
-    const uint8_t* k = (const uint8_t*)p.c.k + (where * p.c.k_page + slot * p.c.k_token + h * p.c.k_head) * W;
-    const uint8_t* v = (const uint8_t*)p.c.v + (where * p.c.v_page + slot * p.c.v_token + h * p.c.v_head) * W;
+    const bool there = (uint32_t)at.entry < (uint32_t)p.c.pages;
+    const uint32_t where = there ? at.entry : 0, slot = at.slot;
+    x.base = there ? at.base : kNowhere;
+    const uint8_t* k = h.k + (uint64_t)where * (uint32_t)(p.c.k_page * W) + slot * (uint32_t)(p.c.k_token * W);
+    const uint8_t* v = h.v + (uint64_t)where * (uint32_t)(p.c.v_page * W) + slot * (uint32_t)(p.c.v_token * W);
+    x.ks = x.vs = 1.0f;
     if constexpr (HELD8) {
-        const int blk = (int)fdiv((uint32_t)slot, p.div_block);
-        x.ks = p.c.k_scale[where * p.c.ks_page + h * p.c.ks_head + blk * p.c.ks_block];
-        x.vs = p.c.v_scale[where * p.c.vs_page + h * p.c.vs_head + blk * p.c.vs_block];
+        const uint32_t blk = fdiv(slot, p.div_block);
+        x.ks = scalar(h.ks + (uint64_t)where * (uint32_t)p.c.ks_page + blk * (uint32_t)p.c.ks_block);
+        x.vs = scalar(h.vs + (uint64_t)where * (uint32_t)p.c.vs_page + blk * (uint32_t)p.c.vs_block);
     }
-    const uint8_t* kl = k + r * p.c.k_token * W;
+    const uint32_t kr = r * (uint32_t)(p.c.k_token * W);
 #pragma unroll
     for (int i = 0; i < x.KL; ++i) {
-        const int ch = HELD8 ? i * 64 + g * 16 : i * 32 + g * 8;
-        if (ch < p.c.dim) x.k[i] = *reinterpret_cast<const u32x4*>(kl + ch * W);
+        const uint32_t ch = HELD8 ? i * 64 + g * 16 : i * 32 + g * 8;
+        x.k[i] = *reinterpret_cast<const u32x4*>(k + (uint32_t)(kr + (ch < (uint32_t)p.c.dim ? ch : 0) * W));
     }
-    if (r * DC < p.c.dim) {
-        const uint8_t* vl = v + r * DC * W;
+    const uint32_t vc = (r * DC < p.c.dim ? r * DC : 0) * W;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x.v[e] = load_chunk<DC * W>(vl + (g * 4 + e) * p.c.v_token * W);
-    }
+    for (int e = 0; e < 4; ++e) x.v[e] = load_chunk<DC * W>(v + (uint32_t)(vc + (g * 4 + e) * (uint32_t)(p.c.v_token * W)));
 }
 
 // Channels t of 4 tokens as 2 words of two tokens each.
@@ -119,8 +134,19 @@ __device__ __forceinline__ u32x2 column(const Chunk<HELD8 ? DC : 2 * DC> (&v)[4]
     return u32x2{__builtin_amdgcn_perm(w[1], w[0], sel), __builtin_amdgcn_perm(w[3], w[2], sel)};
 }
 
+// Two numbers of a part, written through to where workgroups on other dies
+// see them, and read from there.
+__device__ __forceinline__ void leave2(float* p, float a, float b) {
+    const uint64_t w = (uint64_t)__builtin_bit_cast(uint32_t, b) << 32 | __builtin_bit_cast(uint32_t, a);
+    __hip_atomic_store(reinterpret_cast<uint64_t*>(p), w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ float2 take2(const float* p) {
+    const uint64_t w = __hip_atomic_load(reinterpret_cast<const uint64_t*>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    return make_float2(__builtin_bit_cast(float, (uint32_t)w), __builtin_bit_cast(float, (uint32_t)(w >> 32)));
+}
+
 template <typename T, bool HELD8, int DC, int MR>
-__global__ void __launch_bounds__(256) k_few(AttendArgs p) {
+__global__ void __launch_bounds__(256, few_blocks(HELD8, DC, MR)) k_few(AttendArgs p) {
     typedef typename T::one one;
     typedef typename T::x8 x8;
     // Weights and values are multiplied in the cache's type.  An e4m3 value's
@@ -133,34 +159,44 @@ __global__ void __launch_bounds__(256) k_few(AttendArgs p) {
     constexpr int HALVES = DC > 8 ? 2 : 1, DCH = DC / HALVES, PITCH = 16 * DCH + 4;
     __shared__ float obuf[4][16][PITCH];
     __shared__ float mbuf[4][ROWS], lbuf[4][ROWS];
+    __shared__ int arrived;
 
     const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     int b;
     uint64_t seq_step, chunk;
-    const uint64_t total = locate<ROWS>(p, false, 0, &b, &seq_step, &chunk);
-    uint64_t c = (uint64_t)blockIdx.x * chunk;
+    // Its heads, this wave's among them and its place among their waves.
+    const int hw = 1 << p.heads_log, sets = p.c.kv_heads >> p.heads_log;
+    // Workgroups are dealt to the 8 dies in turn: the same share of all heads
+    // goes to one die, one after the other.
+    const int by8 = blockIdx.x >> 3, share = by8 / sets * 8 + (blockIdx.x & 7), h0 = by8 % sets << p.heads_log;
+    const int id = share * sets + (h0 >> p.heads_log);
+    if (share >= p.shares) return;
+    const int wd = wave & (hw - 1), wt = wave >> p.heads_log, h = h0 + wd;
+    const uint64_t total = locate<ROWS>(p, share, &b, &seq_step, &chunk);
+    const int win = p.a.window ? p.a.window : 0x7fffffff;
+    uint64_t c = (uint64_t)share * chunk;
     uint64_t cend = c + chunk < total ? c + chunk : total;
     if (c >= cend || b < 0) return;
 
     while (c < cend) {
-        FewSeq f = few_seq<ROWS>(p, b);
-        const uint64_t off = c - seq_step, all = f.all(p);
+        FewSeq f = few_seq<ROWS, true>(p, b);
+        const uint64_t off = c - seq_step, all = f.all();
         if (off >= all) {
             seq_step += all;
             if (++b >= p.g.batch) return;
             continue;
         }
-        const int unit = (int)(off / (uint32_t)f.steps);
-        const int s0 = (int)(off - (uint64_t)unit * (uint32_t)f.steps);
-        const int s1 = (uint64_t)(f.steps - s0) < cend - c ? f.steps : s0 + (int)(cend - c);
-        const int rt = unit / p.c.kv_heads, h = unit - rt * p.c.kv_heads;
+        const int rt = uniform((int)(off / (uint32_t)f.steps));
+        const int s0 = uniform((int)(off - (uint64_t)rt * (uint32_t)f.steps));
+        const uint64_t tile_at = seq_step + (uint64_t)rt * (uint32_t)f.steps;
+        const int s1 = uniform((uint64_t)(f.steps - s0) < cend - c ? f.steps : s0 + (int)(cend - c));
         const int rows = f.s.n * p.group - rt * ROWS;   // of this tile, may exceed ROWS
         const int first = f.s.length - f.s.n;
         const int32_t* pages = p.g.table + b * p.g.table_row;
-        const int pmin = first + (int)fdiv((uint32_t)(rt * ROWS), p.div_group);
+        const int pmin = uniform(first + (int)fdiv((uint32_t)(rt * ROWS), p.div_group));
         const int lastrow = rt * ROWS + (rows < ROWS ? rows : ROWS) - 1;
-        const int pmax = first + (int)fdiv((uint32_t)lastrow, p.div_group);
+        const int pmax = uniform(first + (int)fdiv((uint32_t)lastrow, p.div_group));
 
         x8 q[MR][KS];
         int pos[MR];
@@ -187,14 +223,24 @@ __global__ void __launch_bounds__(256) k_few(AttendArgs p) {
             for (int t = 0; t < DC; ++t) o[mr][t] = f32x4{0, 0, 0, 0};
         }
 
-        for (int s = s0; s < s1; ++s) {
-            const int t0 = s * kStepGroups + wave * 2;
-            if (t0 >= f.span.n) break;
-            Tile<HELD8, DC> x[2];
-            load_tile<HELD8, DC>(p, pages, f.span, t0, h, x[0]);
-            load_tile<HELD8, DC>(p, pages, f.span, t0 + 1, h, x[1]);
-
+        constexpr int W = HELD8 ? 1 : 2;
+        const Head hd = {(const uint8_t*)p.c.k + h * p.c.k_head * W, (const uint8_t*)p.c.v + h * p.c.v_head * W,
+                         p.c.k_scale + h * p.c.ks_head, p.c.v_scale + h * p.c.vs_head};
+        auto places = [&](Place (&at)[2], int s) {
+            const int t = s * (kStepGroups >> p.heads_log) + wt * 2;
+            at[0] = place_of(p, pages, f.span, t);
+            at[1] = place_of(p, pages, f.span, t + 1);
+        };
+        auto step = [&](Tile<HELD8, DC> (&x)[2]) {
+            if (p.c.dim < 16 * DC) {   // what lanes read beyond the head's channels meets the queries' zeros
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int i = 0; i < x[u].KL; ++i)
+                        if ((HELD8 ? i * 64 + g * 16 : i * 32 + g * 8) >= p.c.dim) x[u].k[i] = u32x4{0, 0, 0, 0};
+            }
             f32x4 sc[MR][2];
+            float f2[2];
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
 #pragma unroll
@@ -214,23 +260,18 @@ __global__ void __launch_bounds__(256) k_few(AttendArgs p) {
                     for (int mr = 0; mr < MR; ++mr) sc[mr][u] = T::mfma16(kk, q[mr][k], sc[mr][u]);
                 }
                 const int base = x[u].base;
-                const float f2 = HELD8 ? p.factor * x[u].ks : p.factor;
-                const bool full = base <= pmin - 15 &&
-                                  (p.a.window == 0 || pmax - base < p.a.window || base + 15 < p.a.sinks);
-                if (full) {
-#pragma unroll
-                    for (int mr = 0; mr < MR; ++mr)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) sc[mr][u][i] *= f2;
-                } else {
+                // A masked score is minus infinity times this: it must not be zero.
+                f2[u] = HELD8 ? fmaxf(p.factor * x[u].ks, 1.17549435e-38f) : p.factor;
+                const bool full = (base <= pmin - 15) & ((pmax - base < win) | (base + 15 < p.a.sinks));
+                if (!full) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int j = base + g * 4 + i;
 #pragma unroll
                         for (int mr = 0; mr < MR; ++mr)
-                            sc[mr][u][i] = sees(p, pos[mr], j) ? sc[mr][u][i] * f2 : neg_inf();
+                            sc[mr][u][i] = ((j <= pos[mr]) & ((pos[mr] - j < win) | (j < p.a.sinks))) ? sc[mr][u][i] : neg_inf();
                         // A token that no row sees weighs nothing, whatever its place holds.
-                        if (!(j <= pmax && (p.a.window == 0 || pmin - j < p.a.window || j < p.a.sinks)))
+                        if (!((j <= pmax) & ((pmin - j < win) | (j < p.a.sinks))))
 #pragma unroll
                             for (int k = 0; k < (int)(sizeof(x[u].v[i]) / 4); ++k) x[u].v[i].w[k] = 0;
                     }
@@ -243,8 +284,7 @@ __global__ void __launch_bounds__(256) k_few(AttendArgs p) {
                 float top = neg_inf();
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) top = fmaxf(top, sc[mr][u][i]);
+                    top = fmaxf(top, f2[u] * fmaxf(fmaxf(sc[mr][u][0], sc[mr][u][1]), fmaxf(sc[mr][u][2], sc[mr][u][3])));
                 if (__any(top > m[mr] + kSlack)) {
                     top = max16(max32(fmaxf(top, m[mr])));
                     const float a = top == neg_inf() ? 1.0f : exp2_(m[mr] - top);
@@ -261,7 +301,7 @@ __global__ void __launch_bounds__(256) k_few(AttendArgs p) {
                     float e[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        e[i] = exp2_(sc[mr][u][i] - ref);
+                        e[i] = exp2_(__builtin_fmaf(sc[mr][u][i], f2[u], -ref));
                         l[mr] += e[i];
                         if constexpr (HELD8) e[i] *= x[u].vs;
                     }
@@ -283,9 +323,21 @@ __global__ void __launch_bounds__(256) k_few(AttendArgs p) {
                     if constexpr (kTwo) o[mr][t] = V::mfma16(vv, __builtin_bit_cast(typename V::x8, w2[mr]), o[mr][t]);
                 }
             }
+        };
+
+        if (s0 * (kStepGroups >> p.heads_log) + wt * 2 < f.span.n) {
+            Place at[2];
+            places(at, s0);
+            for (int s = s0; s < s1; ++s) {
+                Tile<HELD8, DC> x[2];
+                load_tile<HELD8, DC>(p, hd, at[0], x[0]);
+                load_tile<HELD8, DC>(p, hd, at[1], x[1]);
+                places(at, s + 1);   // the table's entries for the next step
+                step(x);
+            }
         }
 
-        // The four waves' sums join under the largest reference.
+        // The sums of a head's waves join under their largest reference.
 #pragma unroll
         for (int mr = 0; mr < MR; ++mr) {
             l[mr] = sum16(sum32(l[mr]));
@@ -296,24 +348,14 @@ __global__ void __launch_bounds__(256) k_few(AttendArgs p) {
         }
         __syncthreads();
         const bool whole = s0 == 0 && s1 == f.steps;
-        float* part = p.parts + ((uint64_t)blockIdx.x * 2 + (s0 ? 0 : 1)) * few_part_floats<DC, MR>();
 #pragma unroll
         for (int mr = 0; mr < MR; ++mr) {
-            const int row = mr * 16 + r;
             float top = neg_inf();
-#pragma unroll
-            for (int i = 0; i < 4; ++i) top = fmaxf(top, mbuf[i][row]);
+            for (int i = wd; i < 4; i += hw) top = fmaxf(top, mbuf[i][mr * 16 + r]);
             const float a = m[mr] == neg_inf() ? 0.0f : exp2_(m[mr] - top);
             const int orow = mr * 16 + (tid >> 4), oc = tid & 15;
-            float otop = neg_inf(), osum = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) otop = fmaxf(otop, mbuf[i][orow]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) osum += mbuf[i][orow] == neg_inf() ? 0.0f : lbuf[i][orow] * exp2_(mbuf[i][orow] - otop);
             const bool there = orow < rows;
             const int oi = (int)fdiv((uint32_t)(rt * ROWS + orow), p.div_group);
-            const int head = h * p.group + rt * ROWS + orow - oi * p.group;
-            const float inv = osum == 0.0f ? 0.0f : 1.0f / osum;
 #pragma unroll
             for (int half = 0; half < HALVES; ++half) {
                 if (mr + half) __syncthreads();
@@ -322,130 +364,142 @@ __global__ void __launch_bounds__(256) k_few(AttendArgs p) {
 #pragma unroll
                     for (int t = 0; t < DCH; ++t) obuf[wave][r][(g * 4 + i) * DCH + t] = m[mr] == neg_inf() ? 0.0f : o[mr][half * DCH + t][i] * a;
                 __syncthreads();
-                if (there && oc * DC < p.c.dim) {
-                    float y[DCH];
+                if (!there) continue;
+                for (int d = 0; d < hw; ++d) {
+                    float otop = neg_inf(), osum = 0.0f, y[DCH];
+                    for (int i = d; i < 4; i += hw) otop = fmaxf(otop, mbuf[i][orow]);
 #pragma unroll
-                    for (int t = 0; t < DCH; ++t) {
-                        y[t] = 0.0f;
+                    for (int t = 0; t < DCH; ++t) y[t] = 0.0f;
+                    for (int i = d; i < 4; i += hw) {
+                        osum += mbuf[i][orow] == neg_inf() ? 0.0f : lbuf[i][orow] * exp2_(mbuf[i][orow] - otop);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) y[t] += obuf[i][tid >> 4][oc * DCH + t];
+                        for (int t = 0; t < DCH; ++t) y[t] += obuf[i][tid >> 4][oc * DCH + t];
                     }
                     if (whole) {
+                        const int head = (h0 + d) * p.group + rt * ROWS + orow - oi * p.group;
+                        const float inv = osum == 0.0f ? 0.0f : 1.0f / osum;
                         one* out = (one*)p.a.out + (f.s.row0 + oi) * p.a.o_token + head * p.a.o_head + oc * DC + half * DCH;
+                        if (oc * DC < p.c.dim)
 #pragma unroll
-                        for (int t = 0; t < DCH; t += 2)
-                            *reinterpret_cast<uint32_t*>(out + t) = pack2<T>(osum == 0.0f ? 0.0f : y[t] * inv, osum == 0.0f ? 0.0f : y[t + 1] * inv);
-                    } else {
-                        float* out = part + orow * (16 * DC) + oc * DC + half * DCH;
-#pragma unroll
-                        for (int t = 0; t < DCH; ++t) out[t] = y[t];
-                    }
-                }
-                if (there && oc == 0 && half == 0) {
-                    if (whole) {
-                        if (p.a.lse)
+                            for (int t = 0; t < DCH; t += 2)
+                                *reinterpret_cast<uint32_t*>(out + t) = pack2<T>(osum == 0.0f ? 0.0f : y[t] * inv, osum == 0.0f ? 0.0f : y[t + 1] * inv);
+                        if (p.a.lse && oc == 0 && half == 0)
                             p.a.lse[(f.s.row0 + oi) * p.a.l_token + head * p.a.l_head] =
                                 osum == 0.0f ? neg_inf() : (otop + __builtin_log2f(osum)) * kLn2;
                     } else {
-                        part[ROWS * 16 * DC + orow] = otop;
-                        part[ROWS * 16 * DC + ROWS + orow] = osum;
+                        float* part = p.parts + (((uint64_t)(uint32_t)id * 2 + (s0 ? 0 : 1)) * hw + d) * few_part_floats(DC, MR);
+#pragma unroll
+                        for (int t = 0; t < DCH; t += 2) leave2(part + orow * (16 * DC) + oc * DC + half * DCH + t, y[t], y[t + 1]);
+                        if (oc == 0 && half == 0) leave2(part + ROWS * 16 * DC + orow * 2, otop, osum);
                     }
                 }
             }
         }
-        __syncthreads();
         c += s1 - s0;
-    }
-}
+        if (whole) {
+            __syncthreads();
+            continue;
+        }
 
-// Joins the parts of row tiles that more than one workgroup took: a wave a
-// row, 64 lanes over its channels, the parts in their order.
-template <typename T, int DC, int MR>
-__global__ void __launch_bounds__(256) k_few_join(AttendArgs p) {
-    typedef typename T::one one;
-    constexpr int ROWS = MR * 16, PER = DC / 4;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int bb = blockIdx.x / p.c.kv_heads, h = blockIdx.x - bb * p.c.kv_heads;
-    int b;
-    uint64_t seq_step, chunk;
-    locate<ROWS>(p, true, bb, &b, &seq_step, &chunk);
-    const FewSeq f = few_seq<ROWS>(p, bb);
-    const int row = blockIdx.y * 4 + wave;
-    for (int rt = 0; rt < f.tiles; ++rt) {
-        if (rt * ROWS + row >= f.s.n * p.group) break;
-        const uint64_t c0 = seq_step + ((uint64_t)rt * p.c.kv_heads + h) * (uint32_t)f.steps;
-        const uint64_t w0 = c0 / chunk, w1 = (c0 + f.steps - 1) / chunk;
-        if (w0 == w1) continue;
-        const int np = (int)(w1 - w0) + 1;
-        const float* base = p.parts + w0 * 2 * few_part_floats<DC, MR>();
-        float top = neg_inf();
-        for (int i = lane; i < np; i += 64) {
-            const float* part = base + ((uint64_t)i * 2 + (i ? 0 : 1)) * few_part_floats<DC, MR>();
-            top = fmaxf(top, part[ROWS * 16 * DC + row]);
-        }
+        // A part is left.  The workgroup that leaves the last one of its row
+        // tile joins them, in their order: whichever it is, the sum is the
+        // same.  Parts are counted at the tile's first workgroup, in a number
+        // that is zero again afterwards.
+        const int w0 = uniform((int)(tile_at / chunk));
+        const int np = uniform((int)((tile_at + f.steps - 1) / chunk)) - w0 + 1;
+        int* counter = p.counters + w0 * sets + (h0 >> p.heads_log);
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // this wave's part is out
+        __syncthreads();
+        if (tid == 0) arrived = __hip_atomic_fetch_add(counter, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __syncthreads();
+        if (uniform(arrived) != np - 1) continue;
+        if (tid == 0) __hip_atomic_store(counter, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        // 16 threads a row and head; the parts some at a time, so that their
+        // reads, which go past this die's L2, wait for one another once.
+        constexpr int AT_ONCE = DC <= 8 ? 8 : 4;
+        const int nrow = rows < ROWS ? rows : ROWS, oc = tid & 15;
+#pragma unroll 1
+        for (int z = tid >> 4; z < nrow * hw; z += 16) {
+            const int d = z / nrow, row = z - d * nrow;
+            float top = neg_inf(), sum = 0.0f, y[DC];
 #pragma unroll
-        for (int d = 32; d; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
-        float sum = 0.0f, y[PER];
+            for (int t = 0; t < DC; ++t) y[t] = 0.0f;
+#pragma unroll 1
+            for (int i0 = 0; i0 < np; i0 += AT_ONCE) {
+                float2 ml[AT_ONCE], v[AT_ONCE][DC / 2];
 #pragma unroll
-        for (int t = 0; t < PER; ++t) y[t] = 0.0f;
-#pragma unroll 4
-        for (int i = 0; i < np; ++i) {
-            const float* part = base + ((uint64_t)i * 2 + (i ? 0 : 1)) * few_part_floats<DC, MR>();
-            const float mp = part[ROWS * 16 * DC + row];
-            const float a = mp == neg_inf() ? 0.0f : exp2_(mp - top);
-            sum += part[ROWS * 16 * DC + ROWS + row] * a;
-            if (lane * PER < p.c.dim)
+                for (int k = 0; k < AT_ONCE; ++k) {
+                    const int i = i0 + k < np ? i0 + k : np - 1;
+                    const uint64_t w = (uint32_t)((w0 + i) * sets + (h0 >> p.heads_log));
+                    const float* part = p.parts + ((w * 2 + (i ? 0 : 1)) * hw + d) * few_part_floats(DC, MR);
+                    ml[k] = take2(part + ROWS * 16 * DC + row * 2);
 #pragma unroll
-                for (int t = 0; t < PER; ++t) {
-                    const float o = part[row * 16 * DC + lane * PER + t];
-                    y[t] += mp == neg_inf() ? 0.0f : o * a;
+                    for (int t = 0; t < DC / 2; ++t) v[k][t] = take2(part + row * 16 * DC + oc * DC + t * 2);
+                    if (i0 + k >= np) ml[k].x = neg_inf();
                 }
-        }
-        const int i = (int)fdiv((uint32_t)(rt * ROWS + row), p.div_group);
-        const int head = h * p.group + rt * ROWS + row - i * p.group;
-        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-        one* out = (one*)p.a.out + (f.s.row0 + i) * p.a.o_token + head * p.a.o_head + lane * PER;
-        if (lane * PER < p.c.dim)
+                float next = top;
 #pragma unroll
-            for (int t = 0; t < PER; ++t) out[t] = (one)(sum == 0.0f ? 0.0f : y[t] * inv);
-        if (p.a.lse && lane == 0)
-            p.a.lse[(f.s.row0 + i) * p.a.l_token + head * p.a.l_head] =
-                sum == 0.0f ? neg_inf() : (top + __builtin_log2f(sum)) * kLn2;
+                for (int k = 0; k < AT_ONCE; ++k) next = fmaxf(next, ml[k].x);
+                const float c0 = top == neg_inf() ? 0.0f : exp2_(top - next);
+                sum *= c0;
+#pragma unroll
+                for (int t = 0; t < DC; ++t) y[t] *= c0;
+#pragma unroll
+                for (int k = 0; k < AT_ONCE; ++k) {
+                    const float a = ml[k].x == neg_inf() ? 0.0f : exp2_(ml[k].x - next);
+                    sum += ml[k].x == neg_inf() ? 0.0f : ml[k].y * a;
+#pragma unroll
+                    for (int t = 0; t < DC / 2; ++t) {
+                        y[2 * t] += v[k][t].x * a;
+                        y[2 * t + 1] += v[k][t].y * a;
+                    }
+                }
+                top = next;
+            }
+            const int i = (int)fdiv((uint32_t)(rt * ROWS + row), p.div_group);
+            const int head = (h0 + d) * p.group + rt * ROWS + row - i * p.group;
+            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+            one* out = (one*)p.a.out + (f.s.row0 + i) * p.a.o_token + head * p.a.o_head + oc * DC;
+            if (oc * DC < p.c.dim)
+#pragma unroll
+                for (int t = 0; t < DC; t += 2)
+                    *reinterpret_cast<uint32_t*>(out + t) = pack2<T>(sum == 0.0f ? 0.0f : y[t] * inv, sum == 0.0f ? 0.0f : y[t + 1] * inv);
+            if (p.a.lse && oc == 0)
+                p.a.lse[(f.s.row0 + i) * p.a.l_token + head * p.a.l_head] =
+                    sum == 0.0f ? neg_inf() : (top + __builtin_log2f(sum)) * kLn2;
+        }
     }
 }
 
 template <typename T, bool HELD8, int DC, int MR>
-static hipError_t go(const AttendArgs& p, int join, hipStream_t st) {
-    k_few<T, HELD8, DC, MR><<<p.workers, 256, 0, st>>>(p);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || !join) return e;
-    k_few_join<T, DC, MR><<<dim3((unsigned)(p.g.batch * p.c.kv_heads), MR * 4), 256, 0, st>>>(p);
+static hipError_t go(const AttendArgs& p, hipStream_t st) {
+    k_few<T, HELD8, DC, MR><<<(unsigned)((p.shares + 7) / 8 * 8 * (p.c.kv_heads >> p.heads_log)), 256, 0, st>>>(p);
     return hipGetLastError();
 }
 
 template <typename T, bool HELD8, int DC>
-static hipError_t go_mr(const AttendArgs& p, int mr, int join, hipStream_t st) {
-    if (mr == 1) return go<T, HELD8, DC, 1>(p, join, st);
+static hipError_t go_mr(const AttendArgs& p, int mr, hipStream_t st) {
+    if (mr == 1) return go<T, HELD8, DC, 1>(p, st);
     if constexpr (DC <= 8) {   // 64 rows of longer heads would not fit a lane's registers
-        if (mr == 4) return go<T, HELD8, DC, 4>(p, join, st);
+        if (mr == 4) return go<T, HELD8, DC, 4>(p, st);
     }
-    return go<T, HELD8, DC, 2>(p, join, st);
+    return go<T, HELD8, DC, 2>(p, st);
 }
 
 template <typename T, bool HELD8>
-static hipError_t go_dc(const AttendArgs& p, int dc, int mr, int join, hipStream_t st) {
+static hipError_t go_dc(const AttendArgs& p, int dc, int mr, hipStream_t st) {
     switch (dc) {
-    case 4: return go_mr<T, HELD8, 4>(p, mr, join, st);
-    case 8: return go_mr<T, HELD8, 8>(p, mr, join, st);
-    case 12: return go_mr<T, HELD8, 12>(p, mr, join, st);
-    default: return go_mr<T, HELD8, 16>(p, mr, join, st);
+    case 4: return go_mr<T, HELD8, 4>(p, mr, st);
+    case 8: return go_mr<T, HELD8, 8>(p, mr, st);
+    case 12: return go_mr<T, HELD8, 12>(p, mr, st);
+    default: return go_mr<T, HELD8, 16>(p, mr, st);
     }
 }
 
-hipError_t launch_few(const AttendArgs& p, int dc, int mr, int join, hipStream_t st) {
+hipError_t launch_few(const AttendArgs& p, int dc, int mr, hipStream_t st) {
     const bool held8 = p.c.type == TPL_KV_E4M3;
-    if (p.a.type == TPL_KV_BF16) return held8 ? go_dc<Bf16, true>(p, dc, mr, join, st) : go_dc<Bf16, false>(p, dc, mr, join, st);
-    return held8 ? go_dc<Fp16, true>(p, dc, mr, join, st) : go_dc<Fp16, false>(p, dc, mr, join, st);
+    if (p.a.type == TPL_KV_BF16) return held8 ? go_dc<Bf16, true>(p, dc, mr, st) : go_dc<Bf16, false>(p, dc, mr, st);
+    return held8 ? go_dc<Fp16, true>(p, dc, mr, st) : go_dc<Fp16, false>(p, dc, mr, st);
 }
 
 }  // namespace kv

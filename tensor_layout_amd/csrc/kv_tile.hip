@@ -19,9 +19,6 @@
 // halves, and rescaling is a product with a lane's own number.
 #include "kv_attend.hpp"
 
-#ifndef PHASE_END
-#define PHASE_END __builtin_amdgcn_sched_barrier(0);
-#endif
 namespace tpl {
 namespace kv {
 
@@ -100,7 +97,11 @@ __global__ void __launch_bounds__(WAVES * 64, D <= 128 ? 2 : 1) k_tile(AttendArg
         const one* src = (const one*)p.a.q + (there ? (s.row0 + t0 + qi) * p.a.q_token + head * p.a.q_head : 0);
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
-            const int ch = k * 16 + hh * 8;
+            // The 8 channels that unit k * 2 + hh of a row of keys in LDS holds.
+            // Of e4m3 keys the first halves of every 16 channels lie before the
+            // second ones, so that lanes write units next to each other.
+            const int unit = k * 2 + hh;
+            const int ch = !HELD8 ? unit * 8 : unit < D / 16 ? unit * 16 : unit * 16 - D + 8;
             u32x4 w = {0, 0, 0, 0};
             if (there && ch < p.c.dim) w = *reinterpret_cast<const u32x4*>(src + ch);
             q[k] = __builtin_bit_cast(x8, w);
@@ -151,7 +152,7 @@ __global__ void __launch_bounds__(WAVES * 64, D <= 128 ? 2 : 1) k_tile(AttendArg
                 vs = p.c.v_scale[where * p.c.vs_page + h * p.c.vs_head + blk * p.c.vs_block];
             }
         }
-        base = where < 0 ? 0x7fffff00 : base;
+        base = where < 0 ? kNowhere : base;
         gbase[to] = base;
         const uint64_t seen = __ballot((base <= pmin - 15) & ((pmax - base < win) | (base + 15 < p.a.sinks)));
         if (lane == 0) gfull[to >> 6] = seen;
@@ -217,8 +218,8 @@ __global__ void __launch_bounds__(WAVES * 64, D <= 128 ? 2 : 1) k_tile(AttendArg
                         d[2 * k] = T::template from_e4m3<false>(kreg[i][k + 2]);
                         d[2 * k + 1] = T::template from_e4m3<true>(kreg[i][k + 2]);
                     }
-                    *reinterpret_cast<u32x4*>(lds + at + tok * KP + pc * 32) = a;
-                    *reinterpret_cast<u32x4*>(lds + at + tok * KP + pc * 32 + 16) = d;
+                    *reinterpret_cast<u32x4*>(lds + at + tok * KP + pc * 16) = a;
+                    *reinterpret_cast<u32x4*>(lds + at + tok * KP + D + pc * 16) = d;
                 } else {
                     *reinterpret_cast<u32x4*>(lds + at + tok * KP + pc * 16) = kreg[i];
                 }
@@ -430,21 +431,21 @@ __global__ void __launch_bounds__(WAVES * 64, D <= 128 ? 2 : 1) k_tile(AttendArg
                     if constexpr (kTwo) o[t] = V::mfma32(__builtin_bit_cast(typename V::x8, x), __builtin_bit_cast(typename V::x8, w2[z]), o[t]);
                 }
             };
-            PHASE_END
+            __builtin_amdgcn_sched_barrier(0);
             read_k(fb, kat, 1), mul_k(fa, 0), weigh(0, 0);
-            PHASE_END
+            __builtin_amdgcn_sched_barrier(0);
             read_k(fa, kat, 2), mul_k(fb, 1), weigh(0, 1);
-            PHASE_END
+            __builtin_amdgcn_sched_barrier(0);
             read_v(fb, vat, 0), mul_k(fa, 2), weigh(1, 0);
-            PHASE_END
+            __builtin_amdgcn_sched_barrier(0);
             read_k(fa, kat, 3), mul_v(fb, 0), weigh(1, 1);
-            PHASE_END
+            __builtin_amdgcn_sched_barrier(0);
             read_v(fb, vat, 1), mul_k(fa, 3), weigh(2, 0);
-            PHASE_END
+            __builtin_amdgcn_sched_barrier(0);
             read_v(fa, vat, 2), mul_v(fb, 1), weigh(2, 1);
-            PHASE_END
+            __builtin_amdgcn_sched_barrier(0);
             read_v(fb, vat, 3), mul_v(fa, 2), weigh(3, 0), weigh(3, 1);
-            PHASE_END
+            __builtin_amdgcn_sched_barrier(0);
             mul_v(fb, 3);
             sc[0] = sn[0];
             sc[1] = sn[1];
@@ -546,8 +547,8 @@ template <typename T, bool HELD8, int D>
 static hipError_t go(const AttendArgs& p, bool join, hipStream_t st) {
     if (join)
         k_tile_join<T, D><<<dim3((unsigned)(p.tiles * p.c.kv_heads), 4), 256, 0, st>>>(p);
-    else if (p.tile_rows == 256)
-        k_tile<T, HELD8, D, 8><<<(unsigned)(p.tiles * p.c.kv_heads * p.splits), 512, 0, st>>>(p);
+    else if (D <= 128 && p.tile_rows == 256)
+        k_tile<T, HELD8, D <= 128 ? D : 128, 8><<<(unsigned)(p.tiles * p.c.kv_heads * p.splits), 512, 0, st>>>(p);
     else
         k_tile<T, HELD8, D, 4><<<(unsigned)(p.tiles * p.c.kv_heads * p.splits), 256, 0, st>>>(p);
     return hipGetLastError();

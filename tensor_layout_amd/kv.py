@@ -18,7 +18,10 @@ points of include/tpl_kv.h, which every call ends in; a refused call raises
 from __future__ import annotations
 
 import ctypes
+import struct
 from typing import Optional, Sequence
+
+import torch
 
 from . import tpl
 from .tpl import TplError
@@ -57,7 +60,13 @@ class Query(ctypes.Structure):
                 + [("scale", ctypes.c_float)] + [(n, _I32) for n in ("type", "heads", "window", "sinks")])
 
 
+# The same layouts for packing a call's numbers in one go.
+_pack_batch = struct.Struct("3Pq3i4x").pack
+_pack_new = struct.Struct("6P9q5i4i4x").pack
+_pack_query = struct.Struct("3P6qf4i4x").pack
+
 _lib = None
+_calls = []   # append, attend, workspace
 
 
 def load():
@@ -65,27 +74,21 @@ def load():
     global _lib
     if _lib is None:
         lib = tpl.load()
-        c, b = ctypes.POINTER(Cache), ctypes.POINTER(Batch)
-        lib.tpl_kv_append.argtypes = [c, b, ctypes.POINTER(New), _P]
-        lib.tpl_kv_append.restype = ctypes.c_int
-        lib.tpl_kv_attend.argtypes = [c, b, ctypes.POINTER(Query), _P, _I64, _P]
-        lib.tpl_kv_attend.restype = ctypes.c_int
-        lib.tpl_kv_attend_workspace.argtypes = [c, b, ctypes.POINTER(Query)]
-        lib.tpl_kv_attend_workspace.restype = _I64
+        c, b, n, q = (ctypes.POINTER(x) for x in (Cache, Batch, New, Query))
+        for name, arg, rest, res in (("tpl_kv_append", n, [_P], ctypes.c_int),
+                                     ("tpl_kv_attend", q, [_P, _I64, _P], ctypes.c_int),
+                                     ("tpl_kv_attend_workspace", q, [], _I64)):
+            f = getattr(lib, name)
+            f.argtypes, f.restype = [c, b, arg] + rest, res
+            f = lib[name]   # a second handle, which takes packed bytes in the structures' places
+            f.argtypes, f.restype = [_P, _P, _P] + rest, res
+            _calls.append(f)
         _lib = lib
     return _lib
 
 
-_types = None
-
-
-def _type(t) -> int:
-    """The C type of a tensor's dtype, or -1."""
-    global _types
-    if _types is None:
-        import torch
-        _types = {torch.bfloat16: BF16, torch.float16: FP16, torch.float8_e4m3fn: E4M3}
-    return _types.get(t.dtype, -1)
+_TYPES = {torch.bfloat16: BF16, torch.float16: FP16, torch.float8_e4m3fn: E4M3}
+_INT32 = torch.int32
 
 
 def _need(ok: bool, message: str, status: int = tpl.TPL_E_ARG) -> None:
@@ -93,9 +96,22 @@ def _need(ok: bool, message: str, status: int = tpl.TPL_E_ARG) -> None:
         raise TplError(status, message)
 
 
+# The checks come in two forms: a call first asks whether everything is right
+# (_ints_ok, _heads_ok), and only for one that is not looks for what is wrong.
+
+
+def _ints_ok(t, index, *shape):
+    """Whether `t` is an array of 32-bit numbers on the device; None in `shape` is any size."""
+    s = t.shape
+    if t.dtype is not _INT32 or t.get_device() != index or len(s) != len(shape):
+        return False
+    for w, x in zip(shape, s):
+        if w is not None and w != x:
+            return False
+    return s[-1] < 2 or t.stride(-1) == 1
+
+
 def _ints(name, t, device, *shape):
-    """A device array of 32-bit numbers; None in `shape` is any size."""
-    import torch
     _need(t.dtype == torch.int32, f"{name} must be int32", tpl.TPL_E_DTYPE)
     s = t.shape
     _need(len(s) == len(shape) and all(w is None or w == x for w, x in zip(shape, s)),
@@ -104,12 +120,16 @@ def _ints(name, t, device, *shape):
     _need(s[-1] < 2 or t.stride(-1) == 1, f"{name} must be contiguous", tpl.TPL_E_LAYOUT)
 
 
-def _heads(name, t, like, tokens, heads, dim):
-    """A [tokens, heads, dim] tensor of `like`'s type whose channels are contiguous."""
-    _need(tuple(t.shape) == (tokens, heads, dim), f"{name} has shape {tuple(t.shape)}, not {(tokens, heads, dim)}",
+def _heads_ok(t, dtype, index, shape):
+    """Whether `t` is a [tokens, heads, dim] tensor of this type whose channels are contiguous."""
+    return t.dtype is dtype and t.get_device() == index and t.shape == shape and t.stride(2) == 1
+
+
+def _heads(name, t, dtype, device, shape):
+    _need(t.dim() == 3 and tuple(t.shape) == tuple(shape), f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}",
           tpl.TPL_E_EXTENT)
-    _need(t.dtype == like.dtype, f"{name} is {t.dtype}, not {like.dtype}", tpl.TPL_E_DTYPE)
-    _need(t.device == like.device, f"{name} must be on {like.device}")
+    _need(t.dtype == dtype, f"{name} is {t.dtype}, not {dtype}", tpl.TPL_E_DTYPE)
+    _need(t.device == device, f"{name} must be on {device}")
     _need(t.stride(2) == 1, f"{name}'s channels must be contiguous", tpl.TPL_E_LAYOUT)
 
 
@@ -120,13 +140,13 @@ class PagedCache:
     Any order in memory is taken as long as a head's channels are contiguous
     and pages, tokens and heads lie on 16 bytes: [pages, kv_heads, page, dim]
     storage goes in as its transposed view.  The object keeps the tensors and
-    their sizes and strides, nothing of their values."""
+    their sizes and strides, and workspaces for ``attend``, nothing of their
+    values."""
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
-        import torch
         _need(k.dim() == 4 and tuple(k.shape) == tuple(v.shape), "k and v must be [pages, page, kv_heads, dim]",
               tpl.TPL_E_EXTENT)
-        _need(_type(k) >= 0 and k.dtype == v.dtype, "a cache holds bf16, fp16 or e4m3", tpl.TPL_E_DTYPE)
+        _need(k.dtype in _TYPES and k.dtype == v.dtype, "a cache holds bf16, fp16 or e4m3", tpl.TPL_E_DTYPE)
         _need(k.device == v.device, "k and v must be on one device")
         _need(k.stride(3) == 1 and v.stride(3) == 1, "the channels of a head must be contiguous", tpl.TPL_E_LAYOUT)
         pages, page, kv_heads, dim = k.shape
@@ -147,36 +167,23 @@ class PagedCache:
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.device, self.kv_heads, self.dim, self.page, self.block = k.device, kv_heads, dim, page, block
         self._c = Cache(k.data_ptr(), v.data_ptr(), *ptr, pages, *k.stride()[:3], *v.stride()[:3], *strides,
-                        _type(k), page, block, kv_heads, dim)
-        self._ref = ctypes.byref(self._c)
+                        _TYPES[k.dtype], page, block, kv_heads, dim)
+        self._at = ctypes.addressof(self._c)
+        self._index = k.get_device()
+        self._sizes = {}   # workspace bytes by a call's sizes
+        self._work = {}    # workspaces by stream
 
 
 def _batch(cache, table, starts, lengths, tokens):
-    device = cache.device
-    _ints("table", table, device, None, None)
+    index = cache._index
+    if not (_ints_ok(table, index, None, None) and _ints_ok(starts, index, table.shape[0] + 1)
+            and _ints_ok(lengths, index, table.shape[0])):
+        device = cache.device
+        _ints("table", table, device, None, None)
+        _ints("starts", starts, device, table.shape[0] + 1)
+        _ints("lengths", lengths, device, table.shape[0])
     n, width = table.shape
-    _ints("starts", starts, device, n + 1)
-    _ints("lengths", lengths, device, n)
-    return Batch(table.data_ptr(), starts.data_ptr(), lengths.data_ptr(), table.stride(0), n, width, tokens)
-
-
-class _On:
-    """The device of a call made current, and its stream."""
-
-    def __init__(self, device, stream):
-        import torch
-        _need(device.type == "cuda", "tensors must live on the GPU")
-        self.stream = torch.cuda.current_stream(device).cuda_stream if stream is None else int(stream)
-        self.guard = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return self.stream
-
-    def __exit__(self, *a):
-        if self.guard is not None:
-            self.guard.__exit__(*a)
+    return n, width, _pack_batch(table.data_ptr(), starts.data_ptr(), lengths.data_ptr(), table.stride(0), n, width, tokens)
 
 
 def _raise(status):
@@ -195,53 +202,102 @@ def append(cache: PagedCache, k, v, table, starts, lengths, *, q=None, q_out=Non
     q_out         takes the rotated queries (default: a new tensor); may be ``q``.
 
     ``lengths`` counts the new tokens.  Returns ``q_out``."""
-    import torch
-    _need(k.dim() == 3, "k must be [tokens, kv_heads, dim]", tpl.TPL_E_EXTENT)
-    tokens, device = k.shape[0], cache.device
-    t = _type(k)
-    _need(t in (BF16, FP16), "k must be bf16 or fp16", tpl.TPL_E_DTYPE)
-    _need(k.device == device, f"k must be on {device}")
-    _heads("k", k, k, tokens, cache.kv_heads, cache.dim)
-    _heads("v", v, k, tokens, cache.kv_heads, cache.dim)
-    batch = _batch(cache, table, starts, lengths, tokens)
-    a = New(k.data_ptr(), v.data_ptr())
-    a.k_token, a.k_head, _ = k.stride()
-    a.v_token, a.v_head, _ = v.stride()
-    a.type, a.axes = t, 1
+    index, dtype = cache._index, k.dtype
+    tokens = k.shape[0] if k.dim() else 0
+    shape = (tokens, cache.kv_heads, cache.dim)
+    if not (dtype in _TYPES and dtype is not torch.float8_e4m3fn and _heads_ok(k, dtype, index, shape)
+            and _heads_ok(v, dtype, index, shape)):
+        _need(k.dim() == 3, "k must be [tokens, kv_heads, dim]", tpl.TPL_E_EXTENT)
+        _need(dtype in (torch.bfloat16, torch.float16), "k must be bf16 or fp16", tpl.TPL_E_DTYPE)
+        _heads("k", k, dtype, cache.device, shape)
+        _heads("v", v, dtype, cache.device, shape)
+    n, width, batch = _batch(cache, table, starts, lengths, tokens)
+    qp = op = qt = qh = ot = oh = heads = 0
     if q is not None:
-        _need(q.dim() == 3, "q must be [tokens, heads, dim]", tpl.TPL_E_EXTENT)
-        heads = q.shape[1]
-        _heads("q", q, k, tokens, heads, cache.dim)
         if q_out is None:
             q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
-        _heads("q_out", q_out, k, tokens, heads, cache.dim)
-        a.q, a.q_out, a.heads = q.data_ptr(), q_out.data_ptr(), heads
-        a.q_token, a.q_head, _ = q.stride()
-        a.o_token, a.o_head, _ = q_out.stride()
-    else:
-        _need(q_out is None, "q_out needs q")
+        heads = q.shape[1] if q.dim() == 3 else 0
+        shape = (tokens, heads, cache.dim)
+        if not (_heads_ok(q, dtype, index, shape) and _heads_ok(q_out, dtype, index, shape)):
+            _need(q.dim() == 3, "q must be [tokens, heads, dim]", tpl.TPL_E_EXTENT)
+            _heads("q", q, dtype, cache.device, shape)
+            _heads("q_out", q_out, dtype, cache.device, shape)
+        qp, op = q.data_ptr(), q_out.data_ptr()
+        qt, qh, _ = q.stride()
+        ot, oh, _ = q_out.stride()
+    elif q_out is not None:
+        _need(False, "q_out needs q")
+    fp = rot = 0
     if inv_freq is not None:
-        _need(inv_freq.dtype == torch.float32, "inv_freq must be fp32", tpl.TPL_E_DTYPE)
-        _need(inv_freq.device == device, f"inv_freq must be on {device}")
-        _need(inv_freq.dim() == 1 and inv_freq.is_contiguous(), "inv_freq must be one contiguous row", tpl.TPL_E_LAYOUT)
-        a.inv_freq, a.rot, a.interleaved = inv_freq.data_ptr(), 2 * inv_freq.shape[0], bool(interleaved)
+        rot = 2 * inv_freq.numel()
+        if not (inv_freq.dtype is torch.float32 and inv_freq.get_device() == index and inv_freq.dim() == 1
+                and (rot < 4 or inv_freq.stride(0) == 1)):
+            _need(inv_freq.dtype == torch.float32, "inv_freq must be fp32", tpl.TPL_E_DTYPE)
+            _need(inv_freq.device == cache.device, f"inv_freq must be on {cache.device}")
+            _need(False, "inv_freq must be one contiguous row", tpl.TPL_E_LAYOUT)
+        fp = inv_freq.data_ptr()
+    pp, row, axes, parts = 0, 0, 1, (0, 0, 0, 0)
     if positions is not None:
-        _ints("positions", positions, device, None, tokens)
-        a.positions, a.positions_row, axes = positions.data_ptr(), positions.stride(0), positions.shape[0]
-        _need(1 <= axes <= MAX_AXES, f"positions must have 1 .. {MAX_AXES} axes")
-        _need(axes == (len(sections) if sections is not None else 1), "sections must have one number for each axis")
-        a.axes = axes
+        if not _ints_ok(positions, index, None, tokens):
+            _ints("positions", positions, cache.device, None, tokens)
+        pp, row, axes = positions.data_ptr(), positions.stride(0), positions.shape[0]
+        _need(1 <= axes <= MAX_AXES, "positions must have 1 .. 4 axes")
+        _need(axes == (1 if sections is None else len(sections)), "sections must have one number for each axis")
     if sections is not None:
         _need(positions is not None, "sections need positions")
         _need(inv_freq is not None, "sections need inv_freq")
-        _need(sum(sections) * 2 == a.rot and all(x >= 0 for x in sections), "sections must add up to the rotated pairs")
-        for i, x in enumerate(sections):
-            a.sections[i] = x
-    with _On(device, stream) as s:
-        status = (_lib or load()).tpl_kv_append(cache._ref, ctypes.byref(batch), ctypes.byref(a), s)
+        _need(sum(sections) * 2 == rot and min(sections) >= 0, "sections must add up to the rotated pairs")
+        parts = (*sections, 0, 0, 0, 0)[:4]
+    kt, kh, _ = k.stride()
+    vt, vh, _ = v.stride()
+    args = _pack_new(k.data_ptr(), v.data_ptr(), qp, op, fp, pp, kt, kh, vt, vh, qt, qh, ot, oh, row,
+                     _TYPES[dtype], heads, rot, bool(interleaved), axes, *parts)
+    _need(index >= 0, "tensors must live on the GPU")
+    if _lib is None:
+        load()
+    if torch.cuda.current_device() == index:
+        s = torch.cuda.current_stream(index).cuda_stream if stream is None else int(stream)
+        status = _calls[0](cache._at, batch, args, s)
+    else:
+        with torch.cuda.device(index):
+            s = torch.cuda.current_stream(index).cuda_stream if stream is None else int(stream)
+            status = _calls[0](cache._at, batch, args, s)
     if status:
         _raise(status)
     return q_out
+
+
+def _workspace(cache, batch, args):
+    load()
+    size = _calls[2](cache._at, batch, args)
+    if size < 0:
+        raise TplError(tpl.TPL_E_ARG, tpl.tpl_last_error())
+    return size
+
+
+def _attend(cache, batch, args, size, stream):
+    """The call itself, with a workspace of the stream's own."""
+    index = cache._index
+    s = torch.cuda.current_stream(index).cuda_stream if stream is None else int(stream)
+    ws = cache._work.get(s)
+    if ws is None or ws[1] < size or torch.cuda.is_current_stream_capturing():
+        ws = _new_workspace(cache, size, s, stream is not None)
+    return _calls[1](cache._at, batch, args, ws[0], size, s)
+
+
+def _new_workspace(cache, size, s, named):
+    """(address, size, tensor), cleared once: every call leaves it as it needs to be.
+
+    Calls on one stream follow one another and share it.  A captured call has
+    one to itself, cleared in the graph: the graph may be replayed beside eager
+    calls on the stream it was captured on."""
+    with torch.cuda.stream(torch.cuda.ExternalStream(s, device=cache.device) if named else None):
+        capturing = torch.cuda.is_current_stream_capturing()
+        t = torch.zeros(size if capturing else max(size, 1 << 20), dtype=torch.uint8, device=cache.device)
+        ws = (t.data_ptr(), t.numel(), t)
+        if not capturing:
+            cache._work[s] = ws
+    return ws
 
 
 def attend(q, cache: PagedCache, table, starts, lengths, *, scale: Optional[float] = None, window: int = 0,
@@ -256,44 +312,44 @@ def attend(q, cache: PagedCache, table, starts, lengths, *, scale: Optional[floa
     lse     fp32 [tokens, heads]: takes the logarithm of each row's sum of exponentials.
 
     A row that sees nothing gets zeros and an lse of minus infinity.  Returns ``out``."""
-    import torch
-    _need(q.dim() == 3, "q must be [tokens, heads, dim]", tpl.TPL_E_EXTENT)
-    tokens, heads, dim = q.shape
-    device = cache.device
-    t = _type(q)
-    _need(t in (BF16, FP16), "q must be bf16 or fp16", tpl.TPL_E_DTYPE)
-    _need(q.device == device, f"q must be on {device}")
-    _heads("q", q, q, tokens, heads, cache.dim)
+    index, dtype = cache._index, q.dtype
+    shape = q.shape
+    if not (len(shape) == 3 and shape[2] == cache.dim and dtype in _TYPES and dtype is not torch.float8_e4m3fn
+            and _heads_ok(q, dtype, index, shape)):
+        _need(q.dim() == 3, "q must be [tokens, heads, dim]", tpl.TPL_E_EXTENT)
+        _need(dtype in (torch.bfloat16, torch.float16), "q must be bf16 or fp16", tpl.TPL_E_DTYPE)
+        _heads("q", q, dtype, cache.device, (shape[0], shape[1], cache.dim))
+    tokens, heads, dim = shape
     if out is None:
         out = torch.empty_like(q, memory_format=torch.contiguous_format)
-    else:
-        _heads("out", out, q, tokens, heads, dim)
-    batch = _batch(cache, table, starts, lengths, tokens)
-    a = Query(q.data_ptr(), out.data_ptr())
-    a.q_token, a.q_head, _ = q.stride()
-    a.o_token, a.o_head, _ = out.stride()
-    a.scale = dim ** -0.5 if scale is None else scale
-    a.type, a.heads, a.window, a.sinks = t, heads, window, sinks
+    elif not _heads_ok(out, dtype, index, shape):
+        _heads("out", out, dtype, cache.device, shape)
+    n, width, batch = _batch(cache, table, starts, lengths, tokens)
+    lp = lt = lh = 0
     if lse is not None:
-        _need(lse.dtype == torch.float32, "lse must be fp32", tpl.TPL_E_DTYPE)
-        _need(tuple(lse.shape) == (tokens, heads), f"lse has shape {tuple(lse.shape)}", tpl.TPL_E_EXTENT)
-        _need(lse.device == device, f"lse must be on {device}")
-        a.lse = lse.data_ptr()
-        a.l_token, a.l_head = lse.stride()
-    lib = _lib or load()
-    b, r = ctypes.byref(batch), ctypes.byref(a)
-    size = lib.tpl_kv_attend_workspace(cache._ref, b, r)
-    if size < 0:
-        raise TplError(tpl.TPL_E_ARG, tpl.tpl_last_error())
-    with _On(device, stream) as s:
-        # The workspace is the call's own: the allocator gives it to nobody
-        # else until this stream's work has passed.
-        if stream is None:
-            ws = torch.empty(size, dtype=torch.uint8, device=device)
-        else:
-            with torch.cuda.stream(torch.cuda.ExternalStream(s, device=device)):
-                ws = torch.empty(size, dtype=torch.uint8, device=device)
-        status = lib.tpl_kv_attend(cache._ref, b, r, ws.data_ptr(), size, s)
+        if not (lse.dtype is torch.float32 and lse.shape == (tokens, heads) and lse.get_device() == index):
+            _need(lse.dtype == torch.float32, "lse must be fp32", tpl.TPL_E_DTYPE)
+            _need(tuple(lse.shape) == (tokens, heads), f"lse has shape {tuple(lse.shape)}", tpl.TPL_E_EXTENT)
+            _need(False, f"lse must be on {cache.device}")
+        lp = lse.data_ptr()
+        lt, lh = lse.stride()
+    qt, qh, _ = q.stride()
+    ot, oh, _ = out.stride()
+    args = _pack_query(q.data_ptr(), out.data_ptr(), lp, qt, qh, ot, oh, lt, lh, dim ** -0.5 if scale is None else scale,
+                       _TYPES[dtype], heads, window, sinks)
+    # What the workspace's size depends on: sizes alone.
+    key = (tokens, heads, n, width, window, sinks, dtype)
+    size = cache._sizes.get(key)
+    if size is None:
+        if len(cache._sizes) > 1000:
+            cache._sizes.clear()
+        size = cache._sizes[key] = _workspace(cache, batch, args)
+    _need(index >= 0, "tensors must live on the GPU")
+    if torch.cuda.current_device() == index:
+        status = _attend(cache, batch, args, size, stream)
+    else:
+        with torch.cuda.device(index):
+            status = _attend(cache, batch, args, size, stream)
     if status:
         _raise(status)
     return out
