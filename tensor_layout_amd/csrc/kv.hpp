@@ -96,15 +96,13 @@ struct Seq {
     int length;  // tokens with them
 };
 
+__device__ __forceinline__ Seq ordered(int row0, int end, int length, int tokens) {
+    const bool ok = row0 >= 0 && end > row0 && end <= tokens && length >= end - row0 && length <= kMaxLength;
+    return ok ? Seq{row0, end - row0, length} : Seq{0, 0, 0};
+}
+
 __device__ __forceinline__ Seq read_seq(const tpl_kv_batch& g, int b) {
-    Seq s;
-    s.row0 = g.starts[b];
-    const int end = g.starts[b + 1];
-    s.length = g.lengths[b];
-    const bool ok = s.row0 >= 0 && end > s.row0 && end <= g.tokens && s.length >= end - s.row0 && s.length <= kMaxLength;
-    s.n = ok ? end - s.row0 : 0;
-    if (!ok) s.row0 = s.length = 0;
-    return s;
+    return ordered(g.starts[b], g.starts[b + 1], g.lengths[b], g.tokens);
 }
 
 }  // namespace kv

@@ -23,10 +23,14 @@ struct AppendArgs {
     tpl_kv_new a;
     int32_t unit;       // tokens of a group: the block, or kGroup where blocks bear no scale
     int32_t by_token;   // grid.x: 1 a group for each row that begins one, 0 numbered by sequence
+    // grid.y: ky workgroups for the keys, ky for the values, then the queries'
+    // qt ranges of q_tokens tokens, each in slices of its rows.
+    int32_t ky, qt, q_tokens, q_slices;
     int32_t sec_end[TPL_KV_MAX_AXES];
 };
 
 constexpr int kGroup = 16;
+constexpr int kQueryTokens = 8;   // of a workgroup on the queries of longer groups
 
 // cos and sin of an angle in 64 bits, rounded to 32.  The angle is brought
 // into [-pi/4, pi/4] with pi/2 in two parts (a product of up to 31 bits times
@@ -58,55 +62,87 @@ __device__ __forceinline__ float2 cos_sin(double angle) {
     return make_float2((float)((q == 1 || q == 2) ? -cc : cc), (float)((q & 2) ? -ss : ss));
 }
 
-// The 8 channels from `ch` of a row, rotated.  `cs`: the row's table of
-// (cos, sin), or NULL.  Products are rounded before they are added, as the
-// formula's plain evaluation does, so that a block's maximum does not depend
-// on which of the two products a fused multiply-add would keep whole.
-template <typename T>
-__device__ __forceinline__ void load_rotated(const typename T::one* row, int ch, int rot, bool interleaved,
-                                             const float2* cs, float y[8]) {
+// How channels turn: not at all; with the one half the rotated channels away,
+// where that half is a multiple of 4 (kQuads) or not (kSingles); with the
+// next one (kPairs).
+enum Mode { kStill, kQuads, kSingles, kPairs };
+
+// 8 channels of a row from `ch`, and for kQuads their partners, 4 at a time,
+// which lie on one side of the half.
+template <int MODE>
+struct Raw {
+    u32x4 own;
+    u32x2 other[MODE == kQuads ? 2 : 1];
+};
+
+template <typename T, int MODE>
+__device__ __forceinline__ Raw<MODE> load_raw(const typename T::one* row, int ch, int half) {
+    Raw<MODE> r;
+    r.own = *reinterpret_cast<const u32x4*>(row + ch);
+    if constexpr (MODE == kQuads) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int c = ch + 4 * j;
+            const int partner = c < half ? c + half : c < 2 * half ? c - half : c;
+            r.other[j] = *reinterpret_cast<const u32x2*>(row + partner);
+        }
+    }
+    return r;
+}
+
+// The channels, rotated.  `cs`: the row's table of (cos, sin).  Products are
+// rounded before they are added, as the formula's plain evaluation does, so
+// that a block's maximum does not depend on which of the two products a fused
+// multiply-add would keep whole.
+template <typename T, int MODE, int FROM>
+__device__ __forceinline__ void rotate(const Raw<FROM>& r, const typename T::one* row, int ch, int half, const float2* cs,
+                                       float (&y)[8]) {
 #pragma clang fp contract(off)
-    const u32x4 w = *reinterpret_cast<const u32x4*>(row + ch);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        y[2 * i] = lo16<T>(w[i]);
-        y[2 * i + 1] = hi16<T>(w[i]);
+        const uint32_t w = r.own[i];
+        y[2 * i] = lo16<T>(w);
+        y[2 * i + 1] = hi16<T>(w);
     }
-    if (!cs || ch >= rot) return;
-    const int half = rot >> 1;
-    if (interleaved) {
+    if constexpr (MODE == kPairs) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            if (ch + 2 * i < rot) {
+            if (ch + 2 * i < 2 * half) {
                 const float2 t = cs[(ch >> 1) + i];
                 const float a = y[2 * i], b = y[2 * i + 1];
                 y[2 * i] = a * t.x - b * t.y;
                 y[2 * i + 1] = b * t.x + a * t.y;
             }
         }
-        return;
-    }
-    if ((half & 7) == 0) {   // the partners are 8 aligned channels too
-        const bool first = ch < half;
-        const u32x4 p = *reinterpret_cast<const u32x4*>(row + (first ? ch + half : ch - half));
-        const float2* t = cs + (first ? ch : ch - half);
+    } else if constexpr (MODE == kQuads) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int c = ch + 4 * j;
+            if (c < 2 * half) {
+                const bool first = c < half;
+                const float2* t = cs + (first ? c : c - half);
+                const uint32_t sign = first ? 0x80000000u : 0u;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t w = r.other[j][i >> 1];
+                    const float b = (i & 1) ? hi16<T>(w) : lo16<T>(w);
+                    const float sn = t[i].y;
+                    const float x = y[4 * j + i] * t[i].x, z = b * __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, sn) ^ sign);
+                    y[4 * j + i] = x + z;
+                }
+            }
+        }
+    } else if constexpr (MODE == kSingles) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float b = (i & 1) ? hi16<T>(p[i >> 1]) : lo16<T>(p[i >> 1]);
-            const float x = y[i] * t[i].x, z = b * t[i].y;
-            y[i] = first ? x - z : x + z;
-        }
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int c = ch + i;
-        if (c < rot) {
-            const bool first = c < half;
-            const float b = (float)row[first ? c + half : c - half];
-            const float2 t = cs[first ? c : c - half];
-            const float x = y[i] * t.x, z = b * t.y;
-            y[i] = first ? x - z : x + z;
+            const int c = ch + i;
+            if (c < 2 * half) {
+                const bool first = c < half;
+                const float b = (float)row[first ? c + half : c - half];
+                const float2 t = cs[first ? c : c - half];
+                const float x = y[i] * t.x, z = b * t.y;
+                y[i] = first ? x - z : x + z;
+            }
         }
     }
 }
@@ -123,8 +159,9 @@ __device__ __forceinline__ bool finite(float x) { return __builtin_fabsf(x) < __
 
 // y / s as 8 e4m3 values.  Where s is a power of two (every scale this kernel
 // sets) the quotient is a shift of the exponent; another writer's scale
-// takes the division.
-__device__ __forceinline__ u32x2 held8(const float y[8], float s) {
+// takes the division.  The conversion gives NaN for NaN; infinities, which
+// are rare and known (`bad`), are made such.
+__device__ __forceinline__ u32x2 held8(const float y[8], float s, bool bad) {
     float h[8];
     const uint32_t bits = __builtin_bit_cast(uint32_t, s);
     if ((bits & 0x007fffffu) == 0 && bits != 0) {
@@ -135,8 +172,9 @@ __device__ __forceinline__ u32x2 held8(const float y[8], float s) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) h[i] = y[i] / s;
     }
+    if (bad)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] = finite(h[i]) ? h[i] : __builtin_nanf("");
+        for (int i = 0; i < 8; ++i) h[i] = finite(h[i]) ? h[i] : __builtin_nanf("");
     u32x2 w;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -155,9 +193,11 @@ __device__ __forceinline__ float scale_of(float amax) {
     return __builtin_amdgcn_ldexpf(1.0f, e);
 }
 
-template <typename T, bool HELD8>
-__global__ void __launch_bounds__(256) k_append(AppendArgs p) {
+// U: rows of a lane whose loads are under way at once.
+template <typename T, bool HELD8, int U, int MODE>
+__global__ void __launch_bounds__(256, 4) k_append(AppendArgs p) {
     typedef typename T::one one;
+    constexpr int WAVES = 4;
     extern __shared__ float2 table[];
     const tpl_kv_cache& c = p.c;
     const tpl_kv_batch& g = p.g;
@@ -165,30 +205,35 @@ __global__ void __launch_bounds__(256) k_append(AppendArgs p) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int id = blockIdx.x, unit = p.unit;
 
-    // The sequence of this group, by counting those that begin at or before
-    // it: 64 at a time, one load's latency for each 64.
-    int before = 0;
-    for (int b0 = 0; b0 < g.batch; b0 += 64) {
-        const int b = b0 + lane;
-        bool there = false;
-        if (b < g.batch) {
-            const int r = g.starts[b];
-            there = p.by_token ? (r <= id && r < g.starts[b + 1]) : (r / unit + 2 * b <= id);
-            // by token, sequences without rows are passed over below
-        }
+    // The sequence of this group: 64 are looked at together, with all that is
+    // needed of them, so that it is known after one load's latency.  A row's
+    // sequence is first looked for at the row's own number and before: most
+    // sequences of a batch of rows have one each.
+    int b = -1;
+    Seq s = {0, 0, 0};
+    auto look = [&](int b0) {
+        const int bb = b0 + lane < g.batch ? b0 + lane : g.batch - 1;
+        const int r = g.starts[bb], e = g.starts[bb + 1], n = g.lengths[bb];
+        const bool there = b0 + lane < g.batch && (p.by_token ? (r <= id && id < e) : (r / unit + 2 * bb <= id));
         const uint64_t m = __ballot(there);
-        if (p.by_token) {
-            if (m) before = b0 + 64 - __builtin_clzll(m);
-        } else {
-            before += __builtin_popcountll(m);
+        if (m) {   // the last of them
+            const int from = 63 - __builtin_clzll(m);
+            b = b0 + from;
+            s.row0 = __builtin_amdgcn_readlane(r, from);
+            s.n = __builtin_amdgcn_readlane(e, from);
+            s.length = __builtin_amdgcn_readlane(n, from);
         }
-    }
-    if (before == 0) return;
-    const int b = __builtin_amdgcn_readfirstlane(before - 1);
-    const Seq s = read_seq(g, b);
+        return m;
+    };
+    const int near = id < g.batch ? id : g.batch - 1;
+    if (!p.by_token || look(near > 63 ? near - 63 : 0) == 0)
+        for (int b0 = 0; b0 < g.batch; b0 += 64)
+            if (look(b0) != ~0ull && (b >= 0 || !p.by_token)) break;
+    if (b < 0) return;
+    s = ordered(s.row0, s.n, s.length, g.tokens);
     if (s.n == 0) return;
     const int first = s.length - s.n;   // index of the sequence's first new token
-    int i0, i1;                         // indexes of the group's tokens
+    int i0;                             // index of the group's first token
     if (p.by_token) {
         i0 = first + id - s.row0;
         if (id >= s.row0 + s.n || (id != s.row0 && i0 % unit != 0)) return;
@@ -199,14 +244,40 @@ __global__ void __launch_bounds__(256) k_append(AppendArgs p) {
         i0 = x > first ? (int)x : first;
     }
     const int had = i0 % unit;
-    i1 = (s.length - i0 > unit - had) ? i0 + unit - had : s.length;
-    const int count = i1 - i0;
+    const int count = s.length - i0 > unit - had ? unit - had : s.length - i0;
     const int row0 = s.row0 + i0 - first;
+    const int pg = i0 / c.page, slot = i0 - pg * c.page;
+    const int where = pg < g.width ? g.table[b * g.table_row + pg] : -1;
 
-    const int pairs = a.inv_freq ? a.rot >> 1 : 0;
-    if (pairs) {
-        for (int i = threadIdx.x; i < count * pairs; i += 256) {
-            const int t = i / pairs, f = i - t * pairs;
+    const int cpr = c.dim >> 3, rpw = 64 / cpr;
+    const int lr = lane / cpr, ch = (lane - lr * cpr) * 8;
+    const bool mine = lr < rpw;
+    const int pairs = MODE == kStill ? 0 : a.rot >> 1;
+
+    // A wave's task: a head's keys, or its values.  Rows t0 + lr, + rpw, ...
+    // are loaded together: past the last one, and in lanes that have no row,
+    // the last one again, so that nothing branches.  The first task's are on
+    // their way while the angles are taken.
+    const bool keys = (int)blockIdx.y < p.ky, queries = (int)blockIdx.y >= 2 * p.ky;
+    int h = (blockIdx.y - (keys ? 0 : p.ky)) * WAVES + wave;
+    const int qy = blockIdx.y - 2 * p.ky, slice = qy / p.qt, from = queries ? (qy - slice * p.qt) * p.q_tokens : 0;
+    const int to_ = queries && from + p.q_tokens < count ? from + p.q_tokens : count;   // tokens whose angles it needs
+    if (from >= count) return;
+    Raw<MODE> raw[U];
+    auto load = [&](int t0) __attribute__((always_inline)) {
+        const one* x = keys ? (const one*)a.k + row0 * a.k_token + h * a.k_head : (const one*)a.v + row0 * a.v_token + h * a.v_head;
+        const int64_t xs = keys ? a.k_token : a.v_token;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = t0 + u * rpw + lr;
+            raw[u] = load_raw<T, MODE>(x + (i < count ? i : count - 1) * xs, mine ? ch : 0, pairs);
+        }
+    };
+    if (!queries && h < c.kv_heads) load(0);
+
+    if (pairs && (keys || queries)) {
+        for (int i = threadIdx.x; i < (to_ - from) * pairs; i += 64 * WAVES) {
+            const int u = i / pairs, f = i - u * pairs, t = from + u;
             int pos = i0 + t;
             if (a.positions) {
                 int axis = 0;
@@ -218,50 +289,65 @@ __global__ void __launch_bounds__(256) k_append(AppendArgs p) {
         }
         __syncthreads();
     }
-    const float2* cs = pairs ? table : nullptr;
-
-    const int cpr = c.dim >> 3, rpw = 64 / cpr;
-    const int lr = lane / cpr, ch = (lane - lr * cpr) * 8;
-    const bool mine = lr < rpw;
-    const int pg = i0 / c.page, slot = i0 - pg * c.page;
-    const int where = pg < g.width ? g.table[b * g.table_row + pg] : -1;
-    const bool page_ok = where >= 0 && where < c.pages;
-
-    const int kv_tasks = page_ok ? 2 * c.kv_heads : 0;
-    for (int task = blockIdx.y * 4 + wave; task < kv_tasks; task += gridDim.y * 4) {
-        const bool key = task < c.kv_heads;
-        const int h = key ? task : task - c.kv_heads;
-        const one* x = key ? (const one*)a.k + row0 * a.k_token + h * a.k_head
-                           : (const one*)a.v + row0 * a.v_token + h * a.v_head;
+    auto write = [&](auto mode, auto is_key) __attribute__((always_inline)) {
+        constexpr int M = decltype(mode)::value;   // MODE for keys, kStill for values
+        constexpr bool key = decltype(is_key)::value;
+        const one* x = key ? (const one*)a.k + row0 * a.k_token + h * a.k_head : (const one*)a.v + row0 * a.v_token + h * a.v_head;
         const int64_t xs = key ? a.k_token : a.v_token;
         const int64_t to = key ? where * c.k_page + slot * c.k_token + h * c.k_head
                                : where * c.v_page + slot * c.v_token + h * c.v_head;
         const int64_t ts = key ? c.k_token : c.v_token;
-        const float2* t2 = key ? cs : nullptr;
-        float y[8];
+        float y[U][8];
+        auto turned = [&](int t0) __attribute__((always_inline)) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int i = t0 + u * rpw + lr, j = i < count ? i : count - 1;
+                rotate<T, M>(raw[u], x + j * xs, mine ? ch : 0, pairs, table + j * pairs, y[u]);
+            }
+        };
         if constexpr (!HELD8) {
             one* d = (one*)(key ? c.k : c.v) + to;
-            for (int t = lr; t < count; t += rpw) {
-                if (!mine) break;
-                load_rotated<T>(x + t * xs, ch, a.rot, a.interleaved, t2 + (key ? t * pairs : 0), y);
-                store8<T>(d + t * ts + ch, y);
+            for (int t0 = 0; t0 < count; t0 += U * rpw) {
+                if (t0) load(t0);
+                turned(t0);
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (mine && t0 + u * rpw + lr < count) store8<T>(d + (t0 + u * rpw + lr) * ts + ch, y[u]);
             }
         } else {
-            float amax = 0.0f;
-            for (int t = lr; t < count; t += rpw) {
-                if (!mine) break;
-                load_rotated<T>(x + t * xs, ch, a.rot, a.interleaved, t2 ? t2 + t * pairs : nullptr, y);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) amax = finite(y[i]) ? fmaxf(amax, __builtin_fabsf(y[i])) : amax;
-            }
-#pragma unroll
-            for (int m = 32; m; m >>= 1) amax = fmaxf(amax, __shfl_xor(amax, m));
-            float sc = scale_of(amax);
             float* at = key ? c.k_scale + where * c.ks_page + h * c.ks_head + (slot / c.block) * c.ks_block
                             : c.v_scale + where * c.vs_page + h * c.vs_head + (slot / c.block) * c.vs_block;
             uint8_t* d = (uint8_t*)(key ? c.k : c.v) + to;
+            float old = 0.0f;
+            if (had) old = *at;
+            // A maximum passes over NaN by itself.  An infinity shows in it,
+            // and has it taken again over the finite ones.
+            float amax = 0.0f;
+            for (int t0 = 0; t0 < count; t0 += U * rpw) {
+                if (t0) load(t0);
+                turned(t0);
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, __builtin_fabsf(y[u][i]));
+            }
+#pragma unroll
+            for (int m = 32; m; m >>= 1) amax = fmaxf(amax, __shfl_xor(amax, m));
+            const bool bad = !finite(amax);
+            if (bad) {
+                amax = 0.0f;
+                for (int t = lr; t < count; t += rpw) {
+                    if (!mine) break;
+                    float z[8];
+                    rotate<T, M>(load_raw<T, M>(x + t * xs, ch, pairs), x + t * xs, ch, pairs, table + t * pairs, z);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) amax = finite(z[i]) ? fmaxf(amax, __builtin_fabsf(z[i])) : amax;
+                }
+#pragma unroll
+                for (int m = 32; m; m >>= 1) amax = fmaxf(amax, __shfl_xor(amax, m));
+            }
+            float sc = scale_of(amax);
             if (had) {
-                const float old = *at;
                 const float grown = fmaxf(old, sc);
                 if (grown != old) {   // the tokens that the block holds, under the larger scale
                     const float ratio = old / grown;
@@ -269,50 +355,97 @@ __global__ void __launch_bounds__(256) k_append(AppendArgs p) {
                         if (!mine) break;
                         u32x2* w = reinterpret_cast<u32x2*>(d + t * ts + ch);
                         const u32x2 o = *w;
+                        float z[8];
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            y[4 * i] = __builtin_amdgcn_cvt_f32_fp8(o[i], 0) * ratio;
-                            y[4 * i + 1] = __builtin_amdgcn_cvt_f32_fp8(o[i], 1) * ratio;
-                            y[4 * i + 2] = __builtin_amdgcn_cvt_f32_fp8(o[i], 2) * ratio;
-                            y[4 * i + 3] = __builtin_amdgcn_cvt_f32_fp8(o[i], 3) * ratio;
+                            z[4 * i] = __builtin_amdgcn_cvt_f32_fp8(o[i], 0) * ratio;
+                            z[4 * i + 1] = __builtin_amdgcn_cvt_f32_fp8(o[i], 1) * ratio;
+                            z[4 * i + 2] = __builtin_amdgcn_cvt_f32_fp8(o[i], 2) * ratio;
+                            z[4 * i + 3] = __builtin_amdgcn_cvt_f32_fp8(o[i], 3) * ratio;
                         }
-                        *w = held8(y, 1.0f);
+                        *w = held8(z, 1.0f, false);
                     }
                 }
                 sc = grown;
             }
-            for (int t = lr; t < count; t += rpw) {
-                if (!mine) break;
-                load_rotated<T>(x + t * xs, ch, a.rot, a.interleaved, t2 ? t2 + t * pairs : nullptr, y);
-                *reinterpret_cast<u32x2*>(d + t * ts + ch) = held8(y, sc);
+            // Where one batch of loads holds the whole group (single tokens,
+            // most blocks of 16), its rows are still there; else they come
+            // again, out of the caches.
+            for (int t0 = 0; t0 < count; t0 += U * rpw) {
+                if (count > U * rpw) {
+                    load(t0);
+                    turned(t0);
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (mine && t0 + u * rpw + lr < count)
+                        *reinterpret_cast<u32x2*>(d + (t0 + u * rpw + lr) * ts + ch) = held8(y[u], sc, bad);
             }
             if (lane == 0) *at = sc;
         }
+    };
+    if (!queries) {
+        if (where < 0 || where >= c.pages) return;
+        for (bool begun = true; h < c.kv_heads; h += p.ky * WAVES, begun = false) {
+            if (!begun) load(0);
+            if (keys)
+                write(std::integral_constant<int, MODE>(), std::true_type());
+            else
+                write(std::integral_constant<int, kStill>(), std::false_type());
+        }
+        return;
     }
 
     // The queries: rows of (token, head).  A row is read and written by one
     // wave in one step, reads first, so q_out may be q itself.
-    if (a.q) {
-        const int rows = count * a.heads;
-        for (int r0 = (blockIdx.y * 4 + wave) * rpw; r0 < rows; r0 += gridDim.y * 4 * rpw) {
-            const int r = r0 + lr;
-            if (!mine || r >= rows) continue;
-            const int t = r / a.heads, h = r - t * a.heads;
-            float y[8];
-            load_rotated<T>((const one*)a.q + (row0 + t) * a.q_token + h * a.q_head, ch, a.rot, a.interleaved,
-                            cs ? cs + t * pairs : nullptr, y);
-            store8<T>((one*)a.q_out + (row0 + t) * a.o_token + h * a.o_head + ch, y);
+    const int rows = (to_ - from) * a.heads, stride = p.q_slices * WAVES * rpw;
+    for (int r0 = (slice * WAVES + wave) * rpw; r0 < rows; r0 += stride * U) {
+        Raw<MODE> w[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int r = r0 + u * stride + lr < rows ? r0 + u * stride + lr : rows - 1;
+            const int t = r / a.heads, hq = r - t * a.heads;
+            w[u] = load_raw<T, MODE>((const one*)a.q + (row0 + from + t) * a.q_token + hq * a.q_head, mine ? ch : 0, pairs);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int r = r0 + u * stride + lr;
+            if (mine && r < rows) {
+                const int t = r / a.heads, hq = r - t * a.heads;
+                float y[8];
+                rotate<T, MODE>(w[u], (const one*)a.q + (row0 + from + t) * a.q_token + hq * a.q_head, ch, pairs, table + t * pairs, y);
+                store8<T>((one*)a.q_out + (row0 + from + t) * a.o_token + hq * a.o_head + ch, y);
+            }
         }
     }
 }
 
-template <typename T>
-static hipError_t launch_append(const AppendArgs& p, dim3 grid, size_t lds, hipStream_t st) {
-    if (p.c.type == TPL_KV_E4M3)
-        k_append<T, true><<<grid, 256, lds, st>>>(p);
+template <typename T, bool HELD8, int MODE>
+static void launch_u(const AppendArgs& p, int u, dim3 grid, size_t lds, hipStream_t st) {
+    if (u == 1)
+        k_append<T, HELD8, 1, MODE><<<grid, 256, lds, st>>>(p);
+    else if (u == 2)
+        k_append<T, HELD8, 2, MODE><<<grid, 256, lds, st>>>(p);
     else
-        k_append<T, false><<<grid, 256, lds, st>>>(p);
+        k_append<T, HELD8, 4, MODE><<<grid, 256, lds, st>>>(p);
+}
+
+template <typename T, bool HELD8>
+static hipError_t launch_mode(const AppendArgs& p, int u, dim3 grid, size_t lds, hipStream_t st) {
+    if (!p.a.inv_freq)
+        launch_u<T, HELD8, kStill>(p, u, grid, lds, st);
+    else if (p.a.interleaved)
+        launch_u<T, HELD8, kPairs>(p, u, grid, lds, st);
+    else if (p.a.rot % 8 == 0)
+        launch_u<T, HELD8, kQuads>(p, u, grid, lds, st);
+    else
+        launch_u<T, HELD8, kSingles>(p, u, grid, lds, st);
     return hipGetLastError();
+}
+
+template <typename T>
+static hipError_t launch_append(const AppendArgs& p, int u, dim3 grid, size_t lds, hipStream_t st) {
+    return p.c.type == TPL_KV_E4M3 ? launch_mode<T, true>(p, u, grid, lds, st) : launch_mode<T, false>(p, u, grid, lds, st);
 }
 
 const char* check_cache(const tpl_kv_cache* c);                                   // kv_attend.hip
@@ -341,7 +474,7 @@ static int append_impl(const tpl_kv_cache* c, const tpl_kv_batch* g, const tpl_k
             if (sum != a->rot / 2) return fail_status(TPL_E_ARG, "sections must add up to the rotated pairs");
         }
     }
-    if (a->q && a->heads < 1) return fail_status(TPL_E_ARG, "heads must be >= 1");
+    if (a->q && (a->heads < 1 || a->heads > 65535)) return fail_status(TPL_E_ARG, "heads must be 1 .. 65535");
     if (g->batch == 0 || g->tokens == 0) return TPL_OK;
     if (!a->k || !a->v) return fail_status(TPL_E_ARG, "k and v must not be NULL");
     if (a->q && !a->q_out) return fail_status(TPL_E_ARG, "q needs q_out");
@@ -367,15 +500,21 @@ static int append_impl(const tpl_kv_cache* c, const tpl_kv_batch* g, const tpl_k
     const int64_t numbered = g->tokens / p.unit + 2 * (int64_t)g->batch;
     p.by_token = g->tokens <= numbered ? 1 : 0;
     const int64_t gx = p.by_token ? g->tokens : numbered;
-    // About two workgroups a CU; more would take the same angles again.
-    int64_t tasks = 2 * (int64_t)c->kv_heads + (a->q ? a->heads : 0);
-    int64_t gy = (512 + gx - 1) / gx, most = (tasks + 3) / 4;
-    if (gy > most) gy = most;
-    if (gy < 1) gy = 1;
+    // Rows under way at once: one where most groups are single tokens, else as
+    // many as a group's tokens fill.
+    const int rpw = 64 / (c->dim / 8);
+    const int u = p.by_token ? 1 : p.unit > 2 * rpw ? 4 : 2;
+    // A head a wave; the queries of single tokens in slices of a row a wave,
+    // those of longer groups by kQueryTokens tokens.
+    p.ky = (c->kv_heads + 3) / 4;
+    p.qt = 1, p.q_tokens = p.unit, p.q_slices = 0;
+    if (a->q && p.by_token) p.q_slices = (int)((a->heads + 4 * (int64_t)rpw - 1) / (4 * rpw));
+    if (a->q && !p.by_token) p.qt = p.unit / kQueryTokens, p.q_tokens = kQueryTokens, p.q_slices = 1;
+    const int64_t gy = 2 * p.ky + p.qt * p.q_slices;
     const size_t lds = a->inv_freq ? (size_t)p.unit * (a->rot / 2) * sizeof(float2) : 0;
     if (lds > 64 * 1024) return fail_status(TPL_E_ARG, "block * rotated channels must be at most 16384");
     const dim3 grid((unsigned)gx, (unsigned)gy);
-    const hipError_t e = a->type == TPL_KV_BF16 ? launch_append<Bf16>(p, grid, lds, st) : launch_append<Fp16>(p, grid, lds, st);
+    const hipError_t e = a->type == TPL_KV_BF16 ? launch_append<Bf16>(p, u, grid, lds, st) : launch_append<Fp16>(p, u, grid, lds, st);
     if (e != hipSuccess) return fail_status(TPL_E_HIP, std::string("HIP launch failed: ") + hipGetErrorString(e));
     return TPL_OK;
 }
