@@ -6,6 +6,7 @@
 
 #include <cmath>
 #include <string>
+#include <type_traits>
 
 #include "../../include/tpl_kv.h"
 
@@ -79,10 +80,34 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
     return __builtin_bit_cast(uint32_t, r);
 }
 
+// Clears the values of a word that are no finite numbers; whether there were
+// any.  An exponent of all ones (for e4m3, which has no infinities, the code
+// of all ones) carries into the sign's place when one is added to it.
+struct E4m3 {};
+template <typename H>
+__device__ __forceinline__ bool clear_bad(uint32_t& w) {
+    constexpr bool e4 = std::is_same<H, E4m3>::value, bf = std::is_same<H, Bf16>::value;
+    constexpr uint32_t ones = e4 ? 0x7f7f7f7fu : bf ? 0x7f807f80u : 0x7c007c00u, unit = e4 ? 0x01010101u : bf ? 0x00800080u : 0x04000400u;
+    const uint32_t top = e4 ? 0x80808080u : 0x80008000u;
+    const uint32_t bad = ((w & ones) + unit) & top;
+    if (bad) w &= ~((bad >> (e4 ? 7 : 15)) * (e4 ? 0xffu : 0xffffu));
+    return bad != 0;
+}
+
 template <typename T>
 __device__ __forceinline__ float lo16(uint32_t w) { return (float)__builtin_bit_cast(typename T::x2, w)[0]; }
 template <typename T>
 __device__ __forceinline__ float hi16(uint32_t w) { return (float)__builtin_bit_cast(typename T::x2, w)[1]; }
+
+// One value of a cache, for the rare cases that ask for it alone.
+template <typename H>
+__device__ __forceinline__ float value_at(const uint8_t* p) {
+    if constexpr (std::is_same<H, E4m3>::value) {
+        return __builtin_amdgcn_cvt_f32_fp8(*p, 0);
+    } else {
+        return lo16<H>(*reinterpret_cast<const uint16_t*>(p));
+    }
+}
 
 // Tokens of a sequence: far enough from 2^31 that sums of positions and tile
 // offsets stay 32-bit numbers.

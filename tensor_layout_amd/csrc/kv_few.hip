@@ -154,6 +154,7 @@ __global__ void __launch_bounds__(256, few_blocks(HELD8, DC, MR)) k_few(AttendAr
     // output keeps 11 bits the weight goes in as the sum of two bf16 numbers.
     typedef typename std::conditional<HELD8, Bf16, T>::type V;
     constexpr bool kTwo = HELD8 && std::is_same<T, Fp16>::value;
+    typedef typename std::conditional<HELD8, E4m3, T>::type H;   // what the cache holds
     constexpr int KS = DC / 2;           // key products of a row
     constexpr int ROWS = MR * 16;
     constexpr int HALVES = DC > 8 ? 2 : 1, DCH = DC / HALVES, PITCH = 16 * DCH + 4;
@@ -231,6 +232,7 @@ __global__ void __launch_bounds__(256, few_blocks(HELD8, DC, MR)) k_few(AttendAr
             at[0] = place_of(p, pages, f.span, t);
             at[1] = place_of(p, pages, f.span, t + 1);
         };
+        bool left_out = false;
         auto step = [&](Tile<HELD8, DC> (&x)[2]) {
             if (p.c.dim < 16 * DC) {   // what lanes read beyond the head's channels meets the queries' zeros
 #pragma unroll
@@ -264,6 +266,18 @@ __global__ void __launch_bounds__(256, few_blocks(HELD8, DC, MR)) k_few(AttendAr
                 f2[u] = HELD8 ? fmaxf(p.factor * x[u].ks, 1.17549435e-38f) : p.factor;
                 const bool full = (base <= pmin - 15) & ((pmax - base < win) | (base + 15 < p.a.sinks));
                 if (!full) {
+                    // Rows that do not see a token multiply its values with
+                    // zeros, which an infinity or NaN among them would show:
+                    // such values are left out here, and added at the end to
+                    // the rows that do see them.
+                    if (pmin != pmax) {
+                        bool some = false;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+#pragma unroll
+                            for (int k = 0; k < (int)(sizeof(x[u].v[i]) / 4); ++k) some |= clear_bad<H>(x[u].v[i].w[k]);
+                        if (some) left_out = true;
+                    }
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int j = base + g * 4 + i;
@@ -335,6 +349,38 @@ __global__ void __launch_bounds__(256, few_blocks(HELD8, DC, MR)) k_few(AttendAr
                 places(at, s + 1);   // the table's entries for the next step
                 step(x);
             }
+        }
+
+        if (__any(left_out)) {
+#pragma unroll 1
+            for (int s = s0; s < s1; ++s)
+#pragma unroll 1
+                for (int u = 0; u < 2; ++u) {
+                    const int t = s * (kStepGroups >> p.heads_log) + wt * 2 + u;
+                    if (t >= f.span.n) break;
+                    const Place x = place_of(p, pages, f.span, t);
+                    if ((uint32_t)x.entry >= (uint32_t)p.c.pages) continue;
+                    if ((x.base <= pmin - 15) & ((pmax - x.base < win) | (x.base + 15 < p.a.sinks))) continue;   // all see it
+#pragma unroll 1
+                    for (int j = 0; j < 16; ++j) {
+                        const uint8_t* from = hd.v + (uint64_t)(uint32_t)x.entry * (uint32_t)(p.c.v_page * W) +
+                                              (uint32_t)(x.slot + j) * (uint32_t)(p.c.v_token * W);
+                        const int tok = x.base + j;
+                        int g4 = g * 4, dim = p.c.dim;
+                        asm volatile("" : "+v"(g4), "+s"(dim));   // no comparison is to be held in registers throughout
+#pragma unroll
+                        for (int t2 = 0; t2 < DC; ++t2)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const int ch = (g4 + i) * DC + t2;
+                                const float v = ch < dim ? value_at<H>(from + ch * W) : 0.0f;
+                                if (!(__builtin_fabsf(v) < __builtin_inff()))
+#pragma unroll
+                                    for (int mr = 0; mr < MR; ++mr)
+                                        if ((tok <= pos[mr]) & ((pos[mr] - tok < win) | (tok < p.a.sinks))) o[mr][t2][i] += v;
+                            }
+                    }
+                }
         }
 
         // The sums of a head's waves join under their largest reference.
@@ -446,8 +492,9 @@ __global__ void __launch_bounds__(256, few_blocks(HELD8, DC, MR)) k_few(AttendAr
                 for (int t = 0; t < DC; ++t) y[t] *= c0;
 #pragma unroll
                 for (int k = 0; k < AT_ONCE; ++k) {
-                    const float a = ml[k].x == neg_inf() ? 0.0f : exp2_(ml[k].x - next);
-                    sum += ml[k].x == neg_inf() ? 0.0f : ml[k].y * a;
+                    if (ml[k].x == neg_inf()) continue;   // nothing in it: no product, which an infinity would show
+                    const float a = exp2_(ml[k].x - next);
+                    sum += ml[k].y * a;
 #pragma unroll
                     for (int t = 0; t < DC / 2; ++t) {
                         y[2 * t] += v[k][t].x * a;

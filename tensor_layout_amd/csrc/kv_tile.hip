@@ -32,6 +32,7 @@ __global__ void __launch_bounds__(WAVES * 64, D <= 128 ? 2 : 1) k_tile(AttendArg
     typedef typename std::conditional<HELD8, Bf16, T>::type V;   // as in kv_few.hip
     constexpr bool kTwo = HELD8 && std::is_same<T, Fp16>::value;
     constexpr int W = HELD8 ? 1 : 2;
+    typedef typename std::conditional<HELD8, E4m3, T>::type H;   // what the cache holds
     constexpr int KS = D / 16, NT = D / 32;
     // Rows of K padded by 16 bytes: an odd number of 16-byte units, so that
     // 16 lanes reading a column of it reach all banks.  Rows of V^T are 128
@@ -51,6 +52,7 @@ __global__ void __launch_bounds__(WAVES * 64, D <= 128 ? 2 : 1) k_tile(AttendArg
     __shared__ __attribute__((aligned(16))) float gks[2 * kInfo], gvs[2 * kInfo], glg[2 * kInfo], grv[2 * kInfo];
     // A bit a group: all of it is seen by all of the tile's rows.
     __shared__ uint64_t gfull[2 * kInfo / 64];
+    __shared__ int left_out;   // whether put_v left out values that are no finite numbers
 
     const int tid = threadIdx.x, lane = tid & 63, r = lane & 31, hh = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -236,6 +238,22 @@ __global__ void __launch_bounds__(WAVES * 64, D <= 128 ? 2 : 1) k_tile(AttendArg
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     if (!((j + e <= pmax) & ((pmin - (j + e) < win) | (j + e < p.a.sinks)))) vreg[i][e] = VPiece{};
+                // Rows that do not see a token multiply its values with zeros,
+                // which an infinity or NaN among them would show: such values
+                // are left out here, and added at the end to the rows that do
+                // see them.
+                const int gb = j - (quad & 3) * 4;
+                if ((gb <= pmin - 15) & ((pmax - gb < win) | (gb + 15 < p.a.sinks))) continue;   // all rows see these 16
+                bool some = false;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+#pragma unroll
+                    for (int k = 0; k < (int)(sizeof(VPiece) / 4); ++k) {
+                        uint32_t w = vreg[i][e][k];
+                        some |= clear_bad<H>(w);
+                        vreg[i][e][k] = w;
+                    }
+                if (some) left_out = 1;
             }
         }
 #pragma unroll
@@ -334,7 +352,8 @@ __global__ void __launch_bounds__(WAVES * 64, D <= 128 ? 2 : 1) k_tile(AttendArg
     // with its values, step st + 1's scores are already under way (independent
     // matrix products to fill the exponentials' time), its values and step
     // st + 2's keys are brought into LDS, and what follows is being read.
-    bool any = false;
+    bool any = false;   // of the step at hand
+    if (tid == 0) left_out = 0;
     if (st0 < st1) {
         look_up((st0 * 4) & ~(kInfo - 1));
         if ((st0 * 4 & (kInfo - 1)) + 16 > kInfo) look_up((st0 * 4 & ~(kInfo - 1)) + kInfo);
@@ -462,6 +481,31 @@ __global__ void __launch_bounds__(WAVES * 64, D <= 128 ? 2 : 1) k_tile(AttendArg
             if (((st + 4) * 4 & (kInfo - 1)) == 0 && st + 4 < st1) look_up((st + 4) * 4);
         }
         __syncthreads();
+    }
+
+    if (left_out) {
+#pragma unroll 1
+        for (int t = st0 * 4; t < st1 * 4 && t < span.n; ++t) {
+            const int base = span.base(t), pg = (int)fdiv((uint32_t)base, p.div_page);
+            const int where = pages[pg];
+            if (where < 0 || where >= p.c.pages) continue;
+            if ((base <= pmin - 15) & ((pmax - base < win) | (base + 15 < p.a.sinks))) continue;   // all see it: nothing left out
+#pragma unroll 1
+            for (int j = base; j < base + 16; ++j) {
+                if (!((j <= pos) & ((pos - j < win) | (j < p.a.sinks)))) continue;
+                const uint8_t* from = (const uint8_t*)p.c.v + (where * p.c.v_page + (j - pg * p.c.page) * p.c.v_token + h * p.c.v_head) * W;
+                int h4 = hh * 4, dim = p.c.dim;
+                asm volatile("" : "+v"(h4), "+s"(dim));   // no comparison is to be held in registers throughout
+#pragma unroll
+                for (int u = 0; u < NT; ++u)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const int ch = u * 32 + (i >> 2) * 8 + h4 + (i & 3);
+                        const float v = ch < dim ? value_at<H>(from + ch * W) : 0.0f;
+                        if (!(__builtin_fabsf(v) < __builtin_inff())) o[u][i] += v;
+                    }
+            }
+        }
     }
 
     l = sum32(l);

@@ -159,6 +159,40 @@ def test_values_that_are_no_numbers(value, n):
     check_attend(11, [n, n], [120, 150], heads=4, kv_heads=2, dim=64, dtype=torch.bfloat16, held8=False, tweak=put)
 
 
+@pytest.mark.parametrize("value", [math.inf, -math.inf, math.nan])
+@pytest.mark.parametrize("n", [5, 30, 90])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (20, 2)])
+@pytest.mark.parametrize("dtype,dim", [(torch.bfloat16, 80), (torch.float16, 128)])
+def test_values_that_are_no_numbers_beside_rows_that_do_not_see_them(value, n, window, sinks, dtype, dim):
+    """Tokens among the new ones: the rows before them, and those whose window has left them, stay as they are."""
+    def put(k, v, table, lengths, **_):
+        for b, back, h, c in ((0, 2, 0, 5), (0, n - 1, 1, dim - 1), (1, n // 2, 1, 0), (1, n // 2, 1, 17)):
+            j = lengths[b] - back
+            v[table[b][j // 32], j % 32, h, c] = value
+    check_attend(33, [n, n], [120, 150], heads=4, kv_heads=2, dim=dim, dtype=dtype, held8=False, tweak=put, window=window,
+                 sinks=sinks)
+    if math.isnan(value):
+        check_attend(34, [n, n], [120, 150], heads=4, kv_heads=2, dim=dim, dtype=dtype, held8=True, tweak=put, window=window,
+                     sinks=sinks)
+
+
+def test_scales_that_are_no_powers_of_two():
+    """Another writer's scales, among them one under the smallest normal number."""
+    from tensor_layout_amd import kv
+    g = torch.Generator().manual_seed(35)
+    for n in (1, 6, 90):
+        starts, lengths, table, pages = kv_cases.batch(g, [n, 1], [300, 75], 32)
+        k, ks, v, vs = kv_cases.pools(g, pages, 32, 2, 64, torch.float16, True, 16, False)
+        ks, vs = ks * (1 + torch.rand(ks.shape, generator=g)), vs * (1 + torch.rand(vs.shape, generator=g))
+        vs[table[0][1], 0, 0] = 2.0 ** -126
+        q = torch.randn((n + 1, 4, 64), generator=g).half()
+        want = kv_oracle.attend(q, k, v, ks, vs, table, starts, lengths, 0.125)
+        got, lse = torch.empty_like(q, device="cuda"), torch.empty((n + 1, 4), device="cuda")
+        kv.attend(dev(q), kv.PagedCache(on_gpu(k), on_gpu(v), dev(ks), dev(vs)), dev(table), dev(starts), dev(lengths),
+                  scale=0.125, out=got, lse=lse)
+        compare_attend(got.cpu(), lse.cpu(), *want, v, vs, torch.float16, True, 64, 300)
+
+
 def test_strides():
     """q and out as parts of wider tensors, lse by heads, a table row inside a wider table."""
     from tensor_layout_amd import kv
