@@ -34,6 +34,7 @@ __global__ void __launch_bounds__(WAVES * 64, D <= 128 ? 2 : 1) k_tile(AttendArg
     constexpr int W = HELD8 ? 1 : 2;
     typedef typename std::conditional<HELD8, E4m3, T>::type H;   // what the cache holds
     constexpr int KS = D / 16, NT = D / 32;
+    constexpr int AHEAD = 1;   // groups of products (see below) that operands are read ahead; 2 and 3 gained nothing
     // Rows of K padded by 16 bytes: an odd number of 16-byte units, so that
     // 16 lanes reading a column of it reach all banks.  Rows of V^T are 128
     // bytes, their 16-byte units exchanged by the row's number: both the
@@ -394,8 +395,21 @@ __global__ void __launch_bounds__(WAVES * 64, D <= 128 ? 2 : 1) k_tile(AttendArg
         bool full = true, next = more;
         if (more && !all_see(st + 1)) sight(st + 1, full, next);
         if (any | next) {
-            Part fa, fb;
-            read_k(fa, kat, 0);
+            Part f[AHEAD + 1];
+            // The order of the groups: weights of 16 tokens are ready before
+            // their values' products, and what is left of the weights goes
+            // beside each.
+            auto read = [&](int at) {
+                Part& x = f[at % (AHEAD + 1)];
+                switch (at) {
+                case 0: case 1: case 2: return read_k(x, kat, at);
+                case 4: return read_k(x, kat, 3);
+                case 3: return read_v(x, vat, 0);
+                default: return read_v(x, vat, at - 4);
+                }
+            };
+#pragma unroll
+            for (int at = 0; at < AHEAD; ++at) read(at);
             f32x4 f2, lg, rv;
             if constexpr (HELD8) {
                 f2 = *reinterpret_cast<const f32x4*>(gks + gi);
@@ -450,22 +464,18 @@ __global__ void __launch_bounds__(WAVES * 64, D <= 128 ? 2 : 1) k_tile(AttendArg
                     if constexpr (kTwo) o[t] = V::mfma32(__builtin_bit_cast(typename V::x8, x), __builtin_bit_cast(typename V::x8, w2[z]), o[t]);
                 }
             };
-            __builtin_amdgcn_sched_barrier(0);
-            read_k(fb, kat, 1), mul_k(fa, 0), weigh(0, 0);
-            __builtin_amdgcn_sched_barrier(0);
-            read_k(fa, kat, 2), mul_k(fb, 1), weigh(0, 1);
-            __builtin_amdgcn_sched_barrier(0);
-            read_v(fb, vat, 0), mul_k(fa, 2), weigh(1, 0);
-            __builtin_amdgcn_sched_barrier(0);
-            read_k(fa, kat, 3), mul_v(fb, 0), weigh(1, 1);
-            __builtin_amdgcn_sched_barrier(0);
-            read_v(fb, vat, 1), mul_k(fa, 3), weigh(2, 0);
-            __builtin_amdgcn_sched_barrier(0);
-            read_v(fa, vat, 2), mul_v(fb, 1), weigh(2, 1);
-            __builtin_amdgcn_sched_barrier(0);
-            read_v(fb, vat, 3), mul_v(fa, 2), weigh(3, 0), weigh(3, 1);
-            __builtin_amdgcn_sched_barrier(0);
-            mul_v(fb, 3);
+#pragma unroll
+            for (int at = 0; at < 8; ++at) {
+                const Part& x = f[at % (AHEAD + 1)];
+                __builtin_amdgcn_sched_barrier(0);
+                if (at + AHEAD < 8) read(at + AHEAD);
+                if (at < 3 || at == 4)
+                    mul_k(x, at < 3 ? at : 3);
+                else
+                    mul_v(x, at == 3 ? 0 : at - 4);
+                if (at < 6) weigh(at >> 1, at & 1);
+                if (at == 6) weigh(3, 0), weigh(3, 1);
+            }
             sc[0] = sn[0];
             sc[1] = sn[1];
             if (!full) mask(st + 1);
@@ -509,36 +519,41 @@ __global__ void __launch_bounds__(WAVES * 64, D <= 128 ? 2 : 1) k_tile(AttendArg
     }
 
     l = sum32(l);
-    if (!there) return;
+    // The row again, from the thread's number, rather than held throughout.
+    int again = threadIdx.x;
+    asm volatile("" : "+v"(again));
+    const int orow = (again >> 6) * 32 + (again & 31), oh = again >> 5 & 1;
+    if (orow >= rows) return;
+    const int oi = (int)fdiv((uint32_t)orow, p.div_group), ohead = h * p.group + orow - oi * p.group;
     if (p.splits > 1) {
         float* part = p.tile_parts + ((uint64_t)(x * p.c.kv_heads + h) * p.splits + split) * tile_part_floats(D, p.tile_rows);
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int i = 0; i < 16; i += 4)
-                *reinterpret_cast<f32x4*>(part + row * D + t * 32 + i * 2 + hh * 4) =
+                *reinterpret_cast<f32x4*>(part + orow * D + t * 32 + i * 2 + oh * 4) =
                     m == neg_inf() ? f32x4{0, 0, 0, 0} : f32x4{o[t][i], o[t][i + 1], o[t][i + 2], o[t][i + 3]};
-        if (hh == 0) {
-            part[p.tile_rows * D + row] = m;
-            part[p.tile_rows * D + p.tile_rows + row] = l;
+        if (oh == 0) {
+            part[p.tile_rows * D + orow] = m;
+            part[p.tile_rows * D + p.tile_rows + orow] = l;
         }
         return;
     }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    one* out = (one*)p.a.out + (s.row0 + t0 + qi) * p.a.o_token + head * p.a.o_head;
+    one* out = (one*)p.a.out + (s.row0 + t0 + oi) * p.a.o_token + ohead * p.a.o_head;
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int i = 0; i < 16; i += 4) {
-            const int ch = t * 32 + i * 2 + hh * 4;
+            const int ch = t * 32 + i * 2 + oh * 4;
             if (ch < p.c.dim) {
                 u32x2 w = {0, 0};
                 if (l != 0.0f) w = u32x2{pack2<T>(o[t][i] * inv, o[t][i + 1] * inv), pack2<T>(o[t][i + 2] * inv, o[t][i + 3] * inv)};
                 *reinterpret_cast<u32x2*>(out + ch) = w;
             }
         }
-    if (p.a.lse && hh == 0)
-        p.a.lse[(s.row0 + t0 + qi) * p.a.l_token + head * p.a.l_head] = l == 0.0f ? neg_inf() : (m + __builtin_log2f(l)) * kLn2;
+    if (p.a.lse && oh == 0)
+        p.a.lse[(s.row0 + t0 + oi) * p.a.l_token + ohead * p.a.l_head] = l == 0.0f ? neg_inf() : (m + __builtin_log2f(l)) * kLn2;
 }
 
 // Joins a row tile's parts, in their order: a wave a row at a time.
