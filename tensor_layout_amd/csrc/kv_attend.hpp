@@ -116,7 +116,7 @@ struct FewSeq {
     __device__ __forceinline__ uint64_t all() const { return (uint64_t)tiles * (uint32_t)steps; }
 };
 
-template <int ROWS, bool UNIFORM>
+template <int ROWS>
 __device__ __forceinline__ FewSeq few_seq(const AttendArgs& p, int b) {
     FewSeq f;
     f.s = read_seq(p.g, b);
@@ -127,16 +127,18 @@ __device__ __forceinline__ FewSeq few_seq(const AttendArgs& p, int b) {
     const int log = 3 - p.heads_log;   // kStepGroups a wave's share of them
     f.steps = (f.span.n + (1 << log) - 1) >> log;
     if (f.steps < 1) f.steps = 1;
-    if constexpr (UNIFORM) {   // the same sequence in every lane
-        f.s.row0 = uniform(f.s.row0);
-        f.s.n = uniform(f.s.n);
-        f.s.length = uniform(f.s.length);
-        f.span.na = uniform(f.span.na);
-        f.span.lo = uniform(f.span.lo);
-        f.span.n = uniform(f.span.n);
-        f.tiles = uniform(f.tiles);
-        f.steps = uniform(f.steps);
-    }
+    return f;
+}
+
+__device__ __forceinline__ FewSeq uniform(FewSeq f) {
+    f.s.row0 = uniform(f.s.row0);
+    f.s.n = uniform(f.s.n);
+    f.s.length = uniform(f.s.length);
+    f.span.na = uniform(f.span.na);
+    f.span.lo = uniform(f.span.lo);
+    f.span.n = uniform(f.span.n);
+    f.tiles = uniform(f.tiles);
+    f.steps = uniform(f.steps);
     return f;
 }
 
@@ -145,16 +147,22 @@ __device__ __forceinline__ FewSeq few_seq(const AttendArgs& p, int b) {
 // share, and the sequence that this share begins in (-1: none) with that
 // sequence's own first step.
 template <int ROWS>
-__device__ __forceinline__ uint64_t locate(const AttendArgs& p, int share, int* at_b, uint64_t* at_step, uint64_t* chunk) {
+__device__ __forceinline__ uint64_t locate(const AttendArgs& p, int share, int* at_b, FewSeq* at_seq, uint64_t* at_step,
+                                           uint64_t* chunk) {
     __shared__ uint64_t sums[4];
     __shared__ uint64_t found_step;
     __shared__ int found_b;
+    __shared__ FewSeq found;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int per = (p.g.batch + 255) / 256;
     uint64_t mine = 0;
+    FewSeq f;
     for (int i = 0; i < per; ++i) {
         const int b = tid * per + i;
-        if (b < p.g.batch) mine += few_seq<ROWS, false>(p, b).all();
+        if (b < p.g.batch) {
+            f = few_seq<ROWS>(p, b);
+            mine += f.all();
+        }
     }
     uint64_t run = mine;
 #pragma unroll
@@ -175,21 +183,23 @@ __device__ __forceinline__ uint64_t locate(const AttendArgs& p, int share, int* 
     *chunk = (total + p.shares - 1) / (uint32_t)p.shares;
     const uint64_t c = (uint64_t)share * *chunk;
     if (mine && before <= c && c < before + mine) {
-        for (int i = 0; i < per; ++i) {
-            const int b = tid * per + i;
-            const uint64_t n = b < p.g.batch ? few_seq<ROWS, false>(p, b).all() : 0;
-            if (c < before + n) {
-                found_b = b;
-                found_step = before;
-                break;
-            }
-            before += n;
+        int b = tid;
+        for (int i = 0; per > 1 && i < per; ++i) {
+            b = tid * per + i;
+            if (b >= p.g.batch) break;
+            f = few_seq<ROWS>(p, b);
+            if (c < before + f.all()) break;
+            before += f.all();
         }
+        found = f;
+        found_b = b;
+        found_step = before;
     }
     __syncthreads();
     // The same in every lane, which the compiler has to be told for what
     // follows from them to stay in scalar registers.
     *at_b = uniform(found_b);
+    *at_seq = uniform(found);
     *at_step = uniform(found_step);
     *chunk = uniform(*chunk);
     return uniform(total);

@@ -174,18 +174,19 @@ __global__ void __launch_bounds__(256, few_blocks(HELD8, DC, MR)) k_few(AttendAr
     const int id = share * sets + (h0 >> p.heads_log);
     if (share >= p.shares) return;
     const int wd = wave & (hw - 1), wt = wave >> p.heads_log, h = h0 + wd;
-    const uint64_t total = locate<ROWS>(p, share, &b, &seq_step, &chunk);
+    FewSeq f;
+    const uint64_t total = locate<ROWS>(p, share, &b, &f, &seq_step, &chunk);
     const int win = p.a.window ? p.a.window : 0x7fffffff;
     uint64_t c = (uint64_t)share * chunk;
     uint64_t cend = c + chunk < total ? c + chunk : total;
     if (c >= cend || b < 0) return;
 
     while (c < cend) {
-        FewSeq f = few_seq<ROWS, true>(p, b);
         const uint64_t off = c - seq_step, all = f.all();
         if (off >= all) {
             seq_step += all;
             if (++b >= p.g.batch) return;
+            f = uniform(few_seq<ROWS>(p, b));
             continue;
         }
         const int rt = uniform((int)(off / (uint32_t)f.steps));

@@ -87,6 +87,12 @@ def load():
     return _lib
 
 
+# The current device and a stream's handle without building the objects that
+# the public functions return (1 us a call) where this torch has them.
+_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_stream = (getattr(torch._C, "_cuda_getCurrentRawStream", None)
+           or (lambda index: torch.cuda.current_stream(index).cuda_stream))
+
 _TYPES = {torch.bfloat16: BF16, torch.float16: FP16, torch.float8_e4m3fn: E4M3}
 _INT32 = torch.int32
 
@@ -255,12 +261,12 @@ def append(cache: PagedCache, k, v, table, starts, lengths, *, q=None, q_out=Non
     _need(index >= 0, "tensors must live on the GPU")
     if _lib is None:
         load()
-    if torch.cuda.current_device() == index:
-        s = torch.cuda.current_stream(index).cuda_stream if stream is None else int(stream)
+    if _device() == index:
+        s = _stream(index) if stream is None else int(stream)
         status = _calls[0](cache._at, batch, args, s)
     else:
         with torch.cuda.device(index):
-            s = torch.cuda.current_stream(index).cuda_stream if stream is None else int(stream)
+            s = _stream(index) if stream is None else int(stream)
             status = _calls[0](cache._at, batch, args, s)
     if status:
         _raise(status)
@@ -278,7 +284,7 @@ def _workspace(cache, batch, args):
 def _attend(cache, batch, args, size, stream):
     """The call itself, with a workspace of the stream's own."""
     index = cache._index
-    s = torch.cuda.current_stream(index).cuda_stream if stream is None else int(stream)
+    s = _stream(index) if stream is None else int(stream)
     ws = cache._work.get(s)
     if ws is None or ws[1] < size or torch.cuda.is_current_stream_capturing():
         ws = _new_workspace(cache, size, s, stream is not None)
@@ -345,7 +351,7 @@ def attend(q, cache: PagedCache, table, starts, lengths, *, scale: Optional[floa
             cache._sizes.clear()
         size = cache._sizes[key] = _workspace(cache, batch, args)
     _need(index >= 0, "tensors must live on the GPU")
-    if torch.cuda.current_device() == index:
+    if _device() == index:
         status = _attend(cache, batch, args, size, stream)
     else:
         with torch.cuda.device(index):
