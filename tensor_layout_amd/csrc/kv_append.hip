@@ -7,11 +7,20 @@
 // max |y| <= 448 s, and y / s is rounded once.
 //
 // Bound: HBM bytes for prompts (each input read and each output written
-// once), the call's own latency for single tokens.  So one workgroup takes
-// the new tokens of one block (they share scales and angles: the angles'
-// cosines and sines are taken once, in LDS) and grid.y splits its heads where
-// blocks are few.  Within it a wave takes a head's keys or values at a time:
-// 8 channels a lane, so a wave reads 64 / (dim / 8) whole rows.
+// once), the call's own latency for single tokens.  Workgroups are told apart
+// by a group of tokens (those of one block: they share scales) and by what
+// they do: keys, where a wave takes a head at a time, values, which need no
+// angles, and queries, which need no scales and go 8 tokens at a time.  A
+// lane holds 8 channels, so a wave reads 64 / (dim / 8) whole rows; up to 4
+// such reads are under way at once.  A workgroup takes the cosines and sines
+// it needs once, in LDS, in 64 bits, while its first rows are on their way.
+//
+// Measured on an MI355X (HBM copies run at 5.1 to 5.2 TB/s): 65536 tokens of
+// 16 + 16 + 16 heads of 64 into a 16-bit cache 158 us, 5.1 TB/s; three prompts
+// of up to 4093 tokens, 28 + 4 + 4 heads of 128, e4m3 in blocks of 64: 55 us,
+// 3.2 TB/s (before keys, values and queries had workgroups of their own
+// 67 us, with one row under way at a time 82 us); one token, 32 + 8 + 8 heads
+// of 128: 5.5 us; 256 single tokens of the same heads: 9.2 us.
 #include "kv.hpp"
 
 namespace tpl {

@@ -4,15 +4,27 @@
 // out = sum_j w_j v_j / sum_j w_j, w_j = 2^(x_j - m), x = scale log2(e) q k,
 // with one running reference m a row.
 //
-// Bound: HBM bytes of the cache, read once.  So the token axis is split: a
-// head's work is counted in steps of 128 tokens of one (sequence, row tile),
-// and every workgroup takes an equal share of consecutive steps of one head,
-// whatever the sequences' lengths are.  Workgroups next to each other take
-// the same share of different heads: where heads lie next to each other in a
-// token's row, they read those rows at about the same time (64 sequences of
-// up to 8192 tokens, 8 heads of 128 bytes: see below).  Of a step each of 4
-// waves takes 32 tokens straight from HBM into registers: nothing is staged
-// in LDS, because no other wave needs the same values.
+// Bound: HBM bytes of the cache, read once; for short caches the chain of
+// dependent reads (lengths, table, keys, parts).  So the token axis is split:
+// a head's work is counted in steps of 128 tokens of one (sequence, row
+// tile), and every workgroup takes an equal share of consecutive steps of one
+// head, whatever the sequences' lengths are.  Of a step each of 4 waves takes
+// 32 tokens straight from HBM into registers: nothing is staged in LDS,
+// because no other wave needs the same values.  Row tiles that end inside a
+// share leave a part, and the last workgroup of a tile to do so joins its
+// parts: no second launch.
+//
+// Where heads lie next to each other in a token's row (128 bytes each), HBM
+// gives its rate only if a row's heads are read at about the same time from
+// one die: workgroups of one share's heads are dealt to one die in a row (64
+// windows of 1024 tokens 32 -> 23 us, drafts 65 -> 50 us), and where shares
+// are so long that these drift apart, a workgroup takes two heads (64
+// sequences of up to 8192 tokens 175 -> 160 us; with pages laid out by head
+// it takes 148 us).
+//
+// Measured on an MI355X: that batch at 4.3 TB/s, two sequences of 131009
+// tokens, 64 heads on 8, pages by head, at 4.4 TB/s (122 us); a batch of 64
+// even ones by head at 5.3 TB/s, which is what copies reach.
 //
 // Layout.  S^T = K Q^T with 16 tokens as the rows of a 16x16x32 product:
 // lane (r = lane % 16, g = lane / 16) holds channels of token r, and its part
