@@ -543,7 +543,7 @@ __global__ void __launch_bounds__(WAVES * 64, D <= 128 ? 2 : 1) k_tile(AttendArg
         for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int i = 0; i < 16; i += 4)
-                *reinterpret_cast<f32x4*>(part + orow * D + t * 32 + i * 2 + oh * 4) =
+                *reinterpret_cast<f32x4*>(part + ((t * 8 + i / 2 + oh) * p.tile_rows + orow) * 4) =
                     m == neg_inf() ? f32x4{0, 0, 0, 0} : f32x4{o[t][i], o[t][i + 1], o[t][i + 2], o[t][i + 3]};
         if (oh == 0) {
             part[p.tile_rows * D + orow] = m;
@@ -568,11 +568,15 @@ __global__ void __launch_bounds__(WAVES * 64, D <= 128 ? 2 : 1) k_tile(AttendArg
         p.a.lse[(s.row0 + t0 + oi) * p.a.l_token + ohead * p.a.l_head] = l == 0.0f ? neg_inf() : (m + __builtin_log2f(l)) * kLn2;
 }
 
-// Joins a row tile's parts, in their order: a wave a row at a time.
+// Joins a row tile's parts, in their order.  A part is kept by 4 channels,
+// then rows: threads next to each other write and read rows next to each
+// other.
+constexpr int kJoinBlocks = 8;   // of a row tile
+
 template <typename T, int D>
 __global__ void __launch_bounds__(256) k_tile_join(AttendArgs p) {
     typedef typename T::one one;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63;
     const int h = blockIdx.x % p.c.kv_heads, x = blockIdx.x / p.c.kv_heads;
     int before = 0;
     for (int b0 = 0; b0 < p.g.batch; b0 += 64) {
@@ -587,29 +591,43 @@ __global__ void __launch_bounds__(256) k_tile_join(AttendArgs p) {
     if (t0 < 0 || t0 >= s.n) return;
     const int tn = s.n - t0 < p.tile_tokens ? s.n - t0 : p.tile_tokens;
     const float* base = p.tile_parts + (uint64_t)(x * p.c.kv_heads + h) * p.splits * tile_part_floats(D, p.tile_rows);
-    for (int row = blockIdx.y * 4 + wave; row < tn * p.group; row += gridDim.y * 4) {
-        float top = neg_inf();
-        for (int i = 0; i < p.splits; ++i) top = fmaxf(top, base[i * tile_part_floats(D, p.tile_rows) + p.tile_rows * D + row]);
-        float sum = 0.0f, y[D / 64 + 1];
+    constexpr int AT_ONCE = 4;
+    const int rows = tn * p.group, quads = p.c.dim / 4;
+    for (int item = blockIdx.y * 256 + threadIdx.x; item < p.tile_rows * quads; item += kJoinBlocks * 256) {
+        const int q = item / p.tile_rows, row = item - q * p.tile_rows;
+        if (row >= rows) continue;
+        float top = neg_inf(), sum = 0.0f;
+        f32x4 y = {0, 0, 0, 0};
+        for (int i0 = 0; i0 < p.splits; i0 += AT_ONCE) {
+            float m[AT_ONCE], l[AT_ONCE], next = top;
+            f32x4 v[AT_ONCE];
 #pragma unroll
-        for (int k = 0; k < D / 64 + 1; ++k) y[k] = 0.0f;
-        for (int i = 0; i < p.splits; ++i) {
-            const float* part = base + i * tile_part_floats(D, p.tile_rows);
-            const float mp = part[p.tile_rows * D + row];
-            if (mp == neg_inf()) continue;
-            const float a = exp2_(mp - top);
-            sum += part[p.tile_rows * D + p.tile_rows + row] * a;
+            for (int k = 0; k < AT_ONCE; ++k) {
+                const float* part = base + (uint64_t)(i0 + k < p.splits ? i0 + k : p.splits - 1) * tile_part_floats(D, p.tile_rows);
+                m[k] = part[p.tile_rows * D + row];
+                l[k] = part[p.tile_rows * D + p.tile_rows + row];
+                v[k] = *reinterpret_cast<const f32x4*>(part + item * 4);
+                if (i0 + k >= p.splits) m[k] = neg_inf();
+                next = fmaxf(next, m[k]);
+            }
+            const float c0 = top == neg_inf() ? 0.0f : exp2_(top - next);
+            sum *= c0;
+            y *= c0;
 #pragma unroll
-            for (int k = 0; k < D / 64 + 1; ++k)
-                if (k * 64 + lane < D) y[k] += part[row * D + k * 64 + lane] * a;
+            for (int k = 0; k < AT_ONCE; ++k) {
+                if (m[k] == neg_inf()) continue;   // nothing in it: no product, which an infinity would show
+                const float a = exp2_(m[k] - next);
+                sum += l[k] * a;
+                y += v[k] * a;
+            }
+            top = next;
         }
         const int qi = (int)fdiv((uint32_t)row, p.div_group), head = h * p.group + row - qi * p.group;
-        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-        one* out = (one*)p.a.out + (s.row0 + t0 + qi) * p.a.o_token + head * p.a.o_head;
-#pragma unroll
-        for (int k = 0; k < D / 64 + 1; ++k)
-            if (k * 64 + lane < p.c.dim && k * 64 + lane < D) out[k * 64 + lane] = (one)(sum == 0.0f ? 0.0f : y[k] * inv);
-        if (p.a.lse && lane == 0)
+        const float inv = 1.0f / sum;
+        u32x2 w = {0, 0};
+        if (sum != 0.0f) w = u32x2{pack2<T>(y[0] * inv, y[1] * inv), pack2<T>(y[2] * inv, y[3] * inv)};
+        *reinterpret_cast<u32x2*>((one*)p.a.out + (s.row0 + t0 + qi) * p.a.o_token + head * p.a.o_head + q * 4) = w;
+        if (p.a.lse && q == 0)
             p.a.lse[(s.row0 + t0 + qi) * p.a.l_token + head * p.a.l_head] = sum == 0.0f ? neg_inf() : (top + __builtin_log2f(sum)) * kLn2;
     }
 }
@@ -617,7 +635,7 @@ __global__ void __launch_bounds__(256) k_tile_join(AttendArgs p) {
 template <typename T, bool HELD8, int D>
 static hipError_t go(const AttendArgs& p, bool join, hipStream_t st) {
     if (join)
-        k_tile_join<T, D><<<dim3((unsigned)(p.tiles * p.c.kv_heads), 4), 256, 0, st>>>(p);
+        k_tile_join<T, D><<<dim3((unsigned)(p.tiles * p.c.kv_heads), kJoinBlocks), 256, 0, st>>>(p);
     else if (D <= 128 && p.tile_rows == 256)
         k_tile<T, HELD8, D <= 128 ? D : 128, 8><<<(unsigned)(p.tiles * p.c.kv_heads * p.splits), 512, 0, st>>>(p);
     else
