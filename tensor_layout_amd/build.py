@@ -37,7 +37,7 @@ def _run(cmd, verbose):
     msgs = [l for l in (res.stdout + res.stderr).splitlines() if noise not in l and l.strip()]
     if res.returncode != 0:
         sys.stderr.write("\n".join(msgs) + "\n")
-        raise RuntimeError(f"hipcc failed ({res.returncode})")
+        raise RuntimeError(f"{cmd[0]} failed ({res.returncode})")
     if verbose and msgs:
         print("\n".join(msgs))
 
@@ -47,8 +47,26 @@ CLIENT_SRC = os.path.join(ROOT, "tests", "c_abi", "abi_client.cpp")
 CLIENT = os.path.join(ROOT, "tests", "c_abi", "abi_client")
 
 
+# The reading of torch tensors for kv.py: a Python extension (host code only).
+CALL_SRC = os.path.join(CSRC, "kv_binding.cpp")
+CALL = os.path.join(HERE, "_kv_call.so")
+
+
+def _call_command(out):
+    import sysconfig
+
+    import torch
+    base = os.path.dirname(torch.__file__)
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+            "-isystem", os.path.join(base, "include"), "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),
+            "-isystem", os.path.join(os.path.dirname(os.path.dirname(HIPCC)), "include"),
+            "-isystem", sysconfig.get_paths()["include"], CALL_SRC, "-o", out,
+            "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+
+
 def build(verbose: bool = False) -> str:
-    """Build libtpl.so and the C ABI test client (both in-tree).
+    """Build libtpl.so, the binding's extension and the C ABI test client (all in-tree).
 
     Every source is compiled to an object on its own (in parallel), then the
     objects are linked."""
@@ -56,7 +74,9 @@ def build(verbose: bool = False) -> str:
     objdir = tempfile.mkdtemp(prefix="tpl_build_")
     try:
         objs = [os.path.join(objdir, s + ".o") for s in SOURCES]
-        jobs = [[HIPCC] + compile_flags + ["-c", os.path.join(CSRC, s), "-o", o] for s, o in zip(SOURCES, objs)]
+        calltmp = CALL + ".tmp"
+        jobs = [_call_command(calltmp)]
+        jobs += [[HIPCC] + compile_flags + ["-c", os.path.join(CSRC, s), "-o", o] for s, o in zip(SOURCES, objs)]
         workers = max(1, min(len(jobs), os.cpu_count() or 1, 16))
         with cf.ThreadPoolExecutor(max_workers=workers) as ex:
             for f in [ex.submit(_run, j, verbose) for j in jobs]:
@@ -64,6 +84,7 @@ def build(verbose: bool = False) -> str:
         tmp = LIB + ".tmp"
         _run([HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC"] + objs + ["-o", tmp], verbose)
         os.replace(tmp, LIB)
+        os.replace(calltmp, CALL)
     finally:
         shutil.rmtree(objdir, ignore_errors=True)
     if os.path.exists(CLIENT_SRC):

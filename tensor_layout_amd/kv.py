@@ -67,11 +67,12 @@ _pack_query = struct.Struct("3P6qf4i4x").pack
 
 _lib = None
 _calls = []   # append, attend, workspace
+_append = _attend = None   # the extension's, which read the tensors too
 
 
 def load():
     """libtpl.so with this module's entry points declared."""
-    global _lib
+    global _lib, _append, _attend
     if _lib is None:
         lib = tpl.load()
         c, b, n, q = (ctypes.POINTER(x) for x in (Cache, Batch, New, Query))
@@ -83,6 +84,13 @@ def load():
             f = lib[name]   # a second handle, which takes packed bytes in the structures' places
             f.argtypes, f.restype = [_P, _P, _P] + rest, res
             _calls.append(f)
+        try:
+            from . import _kv_call
+        except ImportError as e:
+            raise RuntimeError("tensor_layout_amd/_kv_call.so is missing or was built for another torch: build it "
+                               "(python -c 'import __graft_entry__ as g; g.build()')") from e
+        _kv_call.bind(*(ctypes.cast(getattr(lib, n), _P).value for n in EXPORTED))
+        _append, _attend = _kv_call.append, _kv_call.attend
         _lib = lib
     return _lib
 
@@ -176,7 +184,6 @@ class PagedCache:
                         _TYPES[k.dtype], page, block, kv_heads, dim)
         self._at = ctypes.addressof(self._c)
         self._index = k.get_device()
-        self._sizes = {}   # workspace bytes by a call's sizes
         self._work = {}    # workspaces by stream
 
 
@@ -208,6 +215,23 @@ def append(cache: PagedCache, k, v, table, starts, lengths, *, q=None, q_out=Non
     q_out         takes the rotated queries (default: a new tensor); may be ``q``.
 
     ``lengths`` counts the new tokens.  Returns ``q_out``."""
+    if _lib is None:
+        load()
+    if q is not None and q_out is None:
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    index = cache._index
+    if index >= 0 and _device() == index:
+        status = _append(cache._at, index, k, v, table, starts, lengths, q, q_out, inv_freq, positions, sections, interleaved,
+                         _stream(index) if stream is None else int(stream))
+        if status == 0:
+            return q_out
+        if status > 0:
+            _raise(status)
+    return _append_checked(cache, k, v, table, starts, lengths, q, q_out, inv_freq, positions, sections, interleaved, stream)
+
+
+def _append_checked(cache, k, v, table, starts, lengths, q, q_out, inv_freq, positions, sections, interleaved, stream):
+    """The same, each argument by itself: says what is wrong, or makes the call."""
     index, dtype = cache._index, k.dtype
     tokens = k.shape[0] if k.dim() else 0
     shape = (tokens, cache.kv_heads, cache.dim)
@@ -220,8 +244,6 @@ def append(cache: PagedCache, k, v, table, starts, lengths, *, q=None, q_out=Non
     n, width, batch = _batch(cache, table, starts, lengths, tokens)
     qp = op = qt = qh = ot = oh = heads = 0
     if q is not None:
-        if q_out is None:
-            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
         heads = q.shape[1] if q.dim() == 3 else 0
         shape = (tokens, heads, cache.dim)
         if not (_heads_ok(q, dtype, index, shape) and _heads_ok(q_out, dtype, index, shape)):
@@ -259,8 +281,6 @@ def append(cache: PagedCache, k, v, table, starts, lengths, *, q=None, q_out=Non
     args = _pack_new(k.data_ptr(), v.data_ptr(), qp, op, fp, pp, kt, kh, vt, vh, qt, qh, ot, oh, row,
                      _TYPES[dtype], heads, rot, bool(interleaved), axes, *parts)
     _need(index >= 0, "tensors must live on the GPU")
-    if _lib is None:
-        load()
     if _device() == index:
         s = _stream(index) if stream is None else int(stream)
         status = _calls[0](cache._at, batch, args, s)
@@ -281,7 +301,7 @@ def _workspace(cache, batch, args):
     return size
 
 
-def _attend(cache, batch, args, size, stream):
+def _attend_packed(cache, batch, args, size, stream):
     """The call itself, with a workspace of the stream's own."""
     index = cache._index
     s = _stream(index) if stream is None else int(stream)
@@ -318,6 +338,25 @@ def attend(q, cache: PagedCache, table, starts, lengths, *, scale: Optional[floa
     lse     fp32 [tokens, heads]: takes the logarithm of each row's sum of exponentials.
 
     A row that sees nothing gets zeros and an lse of minus infinity.  Returns ``out``."""
+    if _lib is None:
+        load()
+    if out is None:
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    index = cache._index
+    if index >= 0 and _device() == index:
+        s = _stream(index) if stream is None else int(stream)
+        ws = cache._work.get(s)
+        if ws is not None and not torch.cuda.is_current_stream_capturing():
+            status = _attend(cache._at, index, q, table, starts, lengths, scale, window, sinks, out, lse, ws[0], ws[1], s)
+            if status == 0:
+                return out
+            if status > 0:
+                _raise(status)
+    return _attend_checked(q, cache, table, starts, lengths, scale, window, sinks, out, lse, stream)
+
+
+def _attend_checked(q, cache, table, starts, lengths, scale, window, sinks, out, lse, stream):
+    """The same, each argument by itself: says what is wrong, or makes the call, with a new workspace where it needs one."""
     index, dtype = cache._index, q.dtype
     shape = q.shape
     if not (len(shape) == 3 and shape[2] == cache.dim and dtype in _TYPES and dtype is not torch.float8_e4m3fn
@@ -326,9 +365,7 @@ def attend(q, cache: PagedCache, table, starts, lengths, *, scale: Optional[floa
         _need(dtype in (torch.bfloat16, torch.float16), "q must be bf16 or fp16", tpl.TPL_E_DTYPE)
         _heads("q", q, dtype, cache.device, (shape[0], shape[1], cache.dim))
     tokens, heads, dim = shape
-    if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
-    elif not _heads_ok(out, dtype, index, shape):
+    if not _heads_ok(out, dtype, index, shape):
         _heads("out", out, dtype, cache.device, shape)
     n, width, batch = _batch(cache, table, starts, lengths, tokens)
     lp = lt = lh = 0
@@ -343,19 +380,13 @@ def attend(q, cache: PagedCache, table, starts, lengths, *, scale: Optional[floa
     ot, oh, _ = out.stride()
     args = _pack_query(q.data_ptr(), out.data_ptr(), lp, qt, qh, ot, oh, lt, lh, dim ** -0.5 if scale is None else scale,
                        _TYPES[dtype], heads, window, sinks)
-    # What the workspace's size depends on: sizes alone.
-    key = (tokens, heads, n, width, window, sinks, dtype)
-    size = cache._sizes.get(key)
-    if size is None:
-        if len(cache._sizes) > 1000:
-            cache._sizes.clear()
-        size = cache._sizes[key] = _workspace(cache, batch, args)
+    size = _workspace(cache, batch, args)
     _need(index >= 0, "tensors must live on the GPU")
     if _device() == index:
-        status = _attend(cache, batch, args, size, stream)
+        status = _attend_packed(cache, batch, args, size, stream)
     else:
         with torch.cuda.device(index):
-            status = _attend(cache, batch, args, size, stream)
+            status = _attend_packed(cache, batch, args, size, stream)
     if status:
         _raise(status)
     return out
