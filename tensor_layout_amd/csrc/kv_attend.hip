@@ -138,6 +138,7 @@ static const char* choose(const tpl_kv_cache* c, const tpl_kv_batch* g, const tp
         p.heads_log = c->kv_heads % 2 == 0 && c->k_head * w < 256 && c->k_head < c->k_token && c->v_head < c->v_token &&
                       g->batch * (seen / 128) * c->kv_heads >= 32 * blocks ? 1 : 0;
         int64_t shares = blocks / (c->kv_heads >> p.heads_log);
+        if (most > INT_MAX) return "tokens and table are too large together";
         if (shares > most) shares = most;
         p.shares = shares < 1 ? 1 : (int)shares;
         q.few_bytes = kCounters * 4 + (int64_t)p.shares * c->kv_heads * 2 * few_part_floats(q.dc, q.mr) * 4;

@@ -142,23 +142,46 @@ __device__ __forceinline__ FewSeq uniform(FewSeq f) {
     return f;
 }
 
+__device__ __forceinline__ FewSeq from_lane(FewSeq f, int lane) {
+    f.s.row0 = __builtin_amdgcn_readlane(f.s.row0, lane);
+    f.s.n = __builtin_amdgcn_readlane(f.s.n, lane);
+    f.s.length = __builtin_amdgcn_readlane(f.s.length, lane);
+    f.span.na = __builtin_amdgcn_readlane(f.span.na, lane);
+    f.span.lo = __builtin_amdgcn_readlane(f.span.lo, lane);
+    f.span.n = __builtin_amdgcn_readlane(f.span.n, lane);
+    f.tiles = __builtin_amdgcn_readlane(f.tiles, lane);
+    f.steps = __builtin_amdgcn_readlane(f.steps, lane);
+    return f;
+}
+
+// Steps of a share: an equal part of them all, but no less than keeps the
+// joining of a tile's parts (8 at a time) short beside its steps.  An average
+// sequence of n steps takes about c + n / (8 c) of a step's time with c a
+// share, least at c = sqrt(n / 8).
+__device__ __forceinline__ int share_of(const AttendArgs& p, int total) {
+    const int equal = (int)(((uint32_t)total + (uint32_t)p.shares - 1) / (uint32_t)p.shares);
+    const int short_ = (int)__builtin_sqrtf((float)total / (float)(p.g.batch * 8)) + 1;
+    return equal > short_ ? equal : short_;
+}
+
 // The batch's steps in order: every workgroup sums them for itself (one
-// load's latency for up to 256 sequences).  Gives the total, the size of a
-// share, and the sequence that this share begins in (-1: none) with that
-// sequence's own first step.
+// load's latency for up to 256 sequences, and no barrier for up to 64).
+// Gives the total, the size of a share, and the sequence that this share
+// begins in (-1: none) with that sequence's own first step.  More steps than
+// 31 bits hold can only be counted for sequences that claim one another's
+// rows (the host refuses sizes that allow them otherwise): nothing is done.
 template <int ROWS>
-__device__ __forceinline__ uint64_t locate(const AttendArgs& p, int share, int* at_b, FewSeq* at_seq, uint64_t* at_step,
-                                           uint64_t* chunk) {
+__device__ __forceinline__ int locate(const AttendArgs& p, int share, int* at_b, FewSeq* at_seq, int* at_step, int* chunk) {
     __shared__ uint64_t sums[4];
-    __shared__ uint64_t found_step;
-    __shared__ int found_b;
+    __shared__ int found_step, found_b;
     __shared__ FewSeq found;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int per = (p.g.batch + 255) / 256;
+    const bool alone = p.g.batch <= 64;   // every wave counts them all
+    const int per = alone ? 1 : (p.g.batch + 255) / 256, me = alone ? lane : tid;
     uint64_t mine = 0;
-    FewSeq f;
+    FewSeq f = {};
     for (int i = 0; i < per; ++i) {
-        const int b = tid * per + i;
+        const int b = me * per + i;
         if (b < p.g.batch) {
             f = few_seq<ROWS>(p, b);
             mine += f.all();
@@ -170,19 +193,38 @@ __device__ __forceinline__ uint64_t locate(const AttendArgs& p, int share, int* 
         const uint64_t o = __shfl_up(run, d);
         if (lane >= d) run += o;
     }
-    if (lane == 63) sums[wave] = run;
-    if (tid == 0) found_b = -1;
-    __syncthreads();
-    uint64_t total = 0, before = 0;
+    uint64_t total, before = run - mine;
+    if (alone) {
+        total = __shfl(run, 63);
+    } else {
+        if (lane == 63) sums[wave] = run;
+        if (tid == 0) found_b = -1;
+        __syncthreads();
+        total = 0;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-        if (w < wave) before += sums[w];
-        total += sums[w];
+        for (int w = 0; w < 4; ++w) {
+            if (w < wave) before += sums[w];
+            total += sums[w];
+        }
     }
-    before += run - mine;
-    *chunk = (total + p.shares - 1) / (uint32_t)p.shares;
-    const uint64_t c = (uint64_t)share * *chunk;
-    if (mine && before <= c && c < before + mine) {
+    total = uniform(total);
+    *at_b = -1;
+    *at_step = *chunk = 0;
+    if (total == 0 || total > 0x7fffffffu) return 0;
+    *chunk = uniform(share_of(p, (int)total));
+    const uint64_t c = (uint64_t)share * (uint32_t)*chunk;
+    const bool here = mine && before <= c && c < before + mine;
+    if (alone) {
+        const uint64_t m = __ballot(here);
+        if (m) {
+            const int from = __builtin_ctzll(m);
+            *at_b = from;
+            *at_seq = from_lane(f, from);
+            *at_step = __builtin_amdgcn_readlane((int)before, from);
+        }
+        return (int)total;
+    }
+    if (here) {
         int b = tid;
         for (int i = 0; per > 1 && i < per; ++i) {
             b = tid * per + i;
@@ -193,7 +235,7 @@ __device__ __forceinline__ uint64_t locate(const AttendArgs& p, int share, int* 
         }
         found = f;
         found_b = b;
-        found_step = before;
+        found_step = (int)before;
     }
     __syncthreads();
     // The same in every lane, which the compiler has to be told for what
@@ -201,8 +243,7 @@ __device__ __forceinline__ uint64_t locate(const AttendArgs& p, int share, int* 
     *at_b = uniform(found_b);
     *at_seq = uniform(found);
     *at_step = uniform(found_step);
-    *chunk = uniform(*chunk);
-    return uniform(total);
+    return (int)total;
 }
 
 // Part of a row tile that one workgroup of the split kernel leaves: rows of

@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(256, few_blocks(HELD8, DC, MR)) k_few(AttendAr
     const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     int b;
-    uint64_t seq_step, chunk;
+    int seq_step, chunk;
     // Its heads, this wave's among them and its place among their waves.
     const int hw = 1 << p.heads_log, sets = p.c.kv_heads >> p.heads_log;
     // Workgroups are dealt to the 8 dies in turn: the same share of all heads
@@ -187,24 +187,24 @@ __global__ void __launch_bounds__(256, few_blocks(HELD8, DC, MR)) k_few(AttendAr
     if (share >= p.shares) return;
     const int wd = wave & (hw - 1), wt = wave >> p.heads_log, h = h0 + wd;
     FewSeq f;
-    const uint64_t total = locate<ROWS>(p, share, &b, &f, &seq_step, &chunk);
+    const int total = locate<ROWS>(p, share, &b, &f, &seq_step, &chunk);
     const int win = p.a.window ? p.a.window : 0x7fffffff;
-    uint64_t c = (uint64_t)share * chunk;
-    uint64_t cend = c + chunk < total ? c + chunk : total;
+    if (b < 0) return;
+    int c = share * chunk;
+    const int cend = chunk < total - c ? c + chunk : total;
     if (c >= cend || b < 0) return;
 
     while (c < cend) {
-        const uint64_t off = c - seq_step, all = f.all();
+        const int off = c - seq_step, all = (int)f.all();
         if (off >= all) {
             seq_step += all;
             if (++b >= p.g.batch) return;
             f = uniform(few_seq<ROWS>(p, b));
             continue;
         }
-        const int rt = uniform((int)(off / (uint32_t)f.steps));
-        const int s0 = uniform((int)(off - (uint64_t)rt * (uint32_t)f.steps));
-        const uint64_t tile_at = seq_step + (uint64_t)rt * (uint32_t)f.steps;
-        const int s1 = uniform((uint64_t)(f.steps - s0) < cend - c ? f.steps : s0 + (int)(cend - c));
+        const int rt = uniform((int)((uint32_t)off / (uint32_t)f.steps));
+        const int s0 = uniform(off - rt * f.steps), tile_at = seq_step + rt * f.steps;
+        const int s1 = uniform(f.steps - s0 < cend - c ? f.steps : s0 + (cend - c));
         const int rows = f.s.n * p.group - rt * ROWS;   // of this tile, may exceed ROWS
         const int first = f.s.length - f.s.n;
         const int32_t* pages = p.g.table + b * p.g.table_row;
@@ -464,8 +464,8 @@ __global__ void __launch_bounds__(256, few_blocks(HELD8, DC, MR)) k_few(AttendAr
         // tile joins them, in their order: whichever it is, the sum is the
         // same.  Parts are counted at the tile's first workgroup, in a number
         // that is zero again afterwards.
-        const int w0 = uniform((int)(tile_at / chunk));
-        const int np = uniform((int)((tile_at + f.steps - 1) / chunk)) - w0 + 1;
+        const int w0 = uniform((int)((uint32_t)tile_at / (uint32_t)chunk));
+        const int np = uniform((int)((uint32_t)(tile_at + f.steps - 1) / (uint32_t)chunk)) - w0 + 1;
         int* counter = p.counters + w0 * sets + (h0 >> p.heads_log);
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // this wave's part is out
         __syncthreads();
