@@ -20,12 +20,13 @@
 // halves, and rescaling is a product with a lane's own number.
 //
 // Measured on an MI355X (a matrix product of 8192^3 in bf16 runs at 1240
-// TFLOP/s): a prompt of 8192 tokens, 32 heads of 128 on 8 in e4m3, 571 us,
-// 963 TFLOP/s.  Steps there: two waves a SIMD instead of one 1400 -> 752 us;
+// TFLOP/s): a prompt of 8192 tokens, 32 heads of 128 on 8 in e4m3, 566 us,
+// 971 TFLOP/s.  Steps there: two waves a SIMD instead of one 1400 -> 752 us;
 // no short-circuit conditions, which had cost registers, 737; products in
 // groups whose operands are read one group ahead, the weights' arithmetic
 // beside them and the scores of the next step before the values of this one
-// 604; keys' halves apart in LDS 598; 8 waves that share a step 572.  What is
+// 604; keys' halves apart in LDS 598; 8 waves that share a step 572; their
+// products first 3 % less again.  What is
 // left is vector arithmetic: about 260 instructions a wave and step beside
 // 32 matrix products, 51 % of the vector units' time and 40 % of the matrix
 // units', which hardly overlap further with two waves a SIMD.
@@ -412,12 +413,12 @@ __global__ void __launch_bounds__(WAVES * 64, D <= 128 ? 2 : 1) k_tile(AttendArg
             // their values' products, and what is left of the weights goes
             // beside each.
             auto read = [&](int at) {
-                Part& x = f[at % (AHEAD + 1)];
+                Part& operand = f[at % (AHEAD + 1)];
                 switch (at) {
-                case 0: case 1: case 2: return read_k(x, kat, at);
-                case 4: return read_k(x, kat, 3);
-                case 3: return read_v(x, vat, 0);
-                default: return read_v(x, vat, at - 4);
+                case 0: case 1: case 2: return read_k(operand, kat, at);
+                case 4: return read_k(operand, kat, 3);
+                case 3: return read_v(operand, vat, 0);
+                default: return read_v(operand, vat, at - 4);
                 }
             };
 #pragma unroll
@@ -476,18 +477,22 @@ __global__ void __launch_bounds__(WAVES * 64, D <= 128 ? 2 : 1) k_tile(AttendArg
                     if constexpr (kTwo) o[t] = V::mfma32(__builtin_bit_cast(typename V::x8, x), __builtin_bit_cast(typename V::x8, w2[z]), o[t]);
                 }
             };
+            // Of two waves a SIMD the one in its products goes first: 583 -> 566 us
+            // for the prompt above; with 4 waves a workgroup it cost 1 %.
+            if constexpr (WAVES == 8) __builtin_amdgcn_s_setprio(3);
 #pragma unroll
             for (int at = 0; at < 8; ++at) {
-                const Part& x = f[at % (AHEAD + 1)];
+                const Part& operand = f[at % (AHEAD + 1)];
                 __builtin_amdgcn_sched_barrier(0);
                 if (at + AHEAD < 8) read(at + AHEAD);
                 if (at < 3 || at == 4)
-                    mul_k(x, at < 3 ? at : 3);
+                    mul_k(operand, at < 3 ? at : 3);
                 else
-                    mul_v(x, at == 3 ? 0 : at - 4);
+                    mul_v(operand, at == 3 ? 0 : at - 4);
                 if (at < 6) weigh(at >> 1, at & 1);
                 if (at == 6) weigh(3, 0), weigh(3, 1);
             }
+            if constexpr (WAVES == 8) __builtin_amdgcn_s_setprio(0);
             sc[0] = sn[0];
             sc[1] = sn[1];
             if (!full) mask(st + 1);
