@@ -22,8 +22,9 @@
 // sequences of up to 8192 tokens 175 -> 160 us; with pages laid out by head
 // it takes 148 us).
 //
-// Measured on an MI355X: that batch at 4.3 TB/s, two sequences of 131009
-// tokens, 64 heads on 8, pages by head, at 4.4 TB/s (122 us); a batch of 64
+// Measured on an MI355X: that batch in 152 us, 4.7 TB/s (the figures above
+// are with another 10 us for clearing the parts' memory, which is not needed), two sequences of 131009
+// tokens, 64 heads on 8, pages by head, at 4.7 TB/s (114 us); a batch of 64
 // even ones by head at 5.3 TB/s, which is what copies reach.
 //
 // Layout.  S^T = K Q^T with 16 tokens as the rows of a 16x16x32 product:

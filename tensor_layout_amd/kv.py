@@ -28,6 +28,7 @@ from .tpl import TplError
 
 BF16, FP16, E4M3 = 0, 1, 2
 MAX_AXES = 4
+COUNTERS = 4096   # TPL_KV_COUNTERS: the bytes of a workspace that a call finds zero and leaves zero
 
 EXPORTED = ("tpl_kv_append", "tpl_kv_attend", "tpl_kv_attend_workspace")
 
@@ -312,14 +313,15 @@ def _attend_packed(cache, batch, args, size, stream):
 
 
 def _new_workspace(cache, size, s, named):
-    """(address, size, tensor), cleared once: every call leaves it as it needs to be.
+    """(address, size, tensor), its counters cleared once: every call leaves them zero.
 
     Calls on one stream follow one another and share it.  A captured call has
-    one to itself, cleared in the graph: the graph may be replayed beside eager
+    one to itself, whose counters the graph clears: it may be replayed beside eager
     calls on the stream it was captured on."""
     with torch.cuda.stream(torch.cuda.ExternalStream(s, device=cache.device) if named else None):
         capturing = torch.cuda.is_current_stream_capturing()
-        t = torch.zeros(size if capturing else max(size, 1 << 20), dtype=torch.uint8, device=cache.device)
+        t = torch.empty(size if capturing else max(size, 1 << 20), dtype=torch.uint8, device=cache.device)
+        t[:COUNTERS].zero_()
         ws = (t.data_ptr(), t.numel(), t)
         if not capturing:
             cache._work[s] = ws
