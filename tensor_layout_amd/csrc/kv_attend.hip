@@ -128,15 +128,18 @@ static const char* choose(const tpl_kv_cache* c, const tpl_kv_batch* g, const tp
         const int64_t most = tiles * (((int64_t)p.cap + 31) / 32 + 1);
         // Two heads a workgroup where they lie next to each other within 256
         // bytes and a share is long: it then reads whole 256 bytes of a token.
-        // 64 sequences of up to 8192 tokens (64 steps a share at most): 157
-        // against 175 us; 32 of up to 4096 (16 steps), where the parts that
-        // are left weigh more: 55 against 50 us.
+        // 64 sequences of up to 8192 tokens (64 steps a share at most): 155
+        // against 174 us; 24 of them (24 steps): 65 against 72.  At 16 steps,
+        // where the parts that are left weigh more, it goes both ways: 8 of up
+        // to 16384 58 against 62, 2 of up to 65536 63 against 60, 32 of up to
+        // 4096 46 against 49 with a row each and 48 against 46 with four.
+        // Under a window of 1024, 64 of them (8 steps): 28 against 22 us.
         int64_t seen = p.cap;
         if (a->window && (int64_t)a->window + a->sinks < seen) seen = (int64_t)a->window + a->sinks;
         const int64_t blocks = kCUs * few_blocks(c->type == TPL_KV_E4M3, q.dc, q.mr);
         const int w = c->type == TPL_KV_E4M3 ? 1 : 2;
         p.heads_log = c->kv_heads % 2 == 0 && c->k_head * w < 256 && c->k_head < c->k_token && c->v_head < c->v_token &&
-                      g->batch * (seen / 128) * c->kv_heads >= 32 * blocks ? 1 : 0;
+                      g->batch * (seen / 128) * c->kv_heads >= 24 * blocks ? 1 : 0;
         int64_t shares = blocks / (c->kv_heads >> p.heads_log);
         if (most > INT_MAX) return "tokens and table are too large together";
         if (shares > most) shares = most;

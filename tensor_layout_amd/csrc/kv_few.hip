@@ -19,13 +19,12 @@
 // one die: workgroups of one share's heads are dealt to one die in a row (64
 // windows of 1024 tokens 32 -> 23 us, drafts 65 -> 50 us), and where shares
 // are so long that these drift apart, a workgroup takes two heads (64
-// sequences of up to 8192 tokens 175 -> 160 us; with pages laid out by head
-// it takes 148 us).
+// sequences of up to 8192 tokens 174 -> 155 us; with pages laid out by head
+// it takes 140 us).
 //
-// Measured on an MI355X: that batch in 152 us, 4.7 TB/s (the figures above
-// are with another 10 us for clearing the parts' memory, which is not needed), two sequences of 131009
+// Measured on an MI355X: that batch at 4.6 TB/s, two sequences of 131009
 // tokens, 64 heads on 8, pages by head, at 4.7 TB/s (114 us); a batch of 64
-// even ones by head at 5.3 TB/s, which is what copies reach.
+// even ones by head at 5.5 TB/s (a large copy: 5.2).
 //
 // Layout.  S^T = K Q^T with 16 tokens as the rows of a 16x16x32 product:
 // lane (r = lane % 16, g = lane / 16) holds channels of token r, and its part
