@@ -115,9 +115,9 @@ int tpl_kv_append(const tpl_kv_cache *cache, const tpl_kv_batch *batch,
  * an lse of minus infinity.
  *
  * `workspace` is device memory of at least tpl_kv_attend_workspace() bytes,
- * 16-byte aligned.  Its first TPL_KV_COUNTERS bytes (or all of it, if it is
- * smaller) must be zero before the first call that it is given to; every call
- * leaves them zero, so that one workspace serves any number of calls on one
+ * 16-byte aligned.  Its first TPL_KV_COUNTERS bytes must be zero before the
+ * first call that it is given to; every call leaves them zero, whichever
+ * kernels it runs, so that one workspace serves any number of calls on one
  * stream.  Calls that may run at the same time need one each.
  */
 #define TPL_KV_COUNTERS 4096

@@ -61,7 +61,10 @@ const char* check_batch(const tpl_kv_cache& c, const tpl_kv_batch* g) {
 struct Choice {
     bool few, tile;
     int dc, mr, dk;
-    int64_t few_bytes, tile_bytes;
+    int64_t few_bytes, tile_bytes;   // of parts
+    // The counters come first in every workspace, also in one for a call that
+    // counts nothing: the next call on it may, and has to find them zero.
+    int64_t bytes() const { return few_bytes + tile_bytes > 0 ? kCounters * 4 + few_bytes + tile_bytes : 0; }
 };
 
 static const char* choose(const tpl_kv_cache* c, const tpl_kv_batch* g, const tpl_kv_query* a, AttendArgs& p, Choice& q,
@@ -144,7 +147,7 @@ static const char* choose(const tpl_kv_cache* c, const tpl_kv_batch* g, const tp
         if (most > INT_MAX) return "tokens and table are too large together";
         if (shares > most) shares = most;
         p.shares = shares < 1 ? 1 : (int)shares;
-        q.few_bytes = kCounters * 4 + (int64_t)p.shares * c->kv_heads * 2 * few_part_floats(q.dc, q.mr) * 4;
+        q.few_bytes = (int64_t)p.shares * c->kv_heads * 2 * few_part_floats(q.dc, q.mr) * 4;
     }
     if (q.tile) {
         q.dk = c->dim <= 64 ? 64 : c->dim <= 96 ? 96 : c->dim <= 128 ? 128 : c->dim <= 192 ? 192 : 256;
@@ -184,11 +187,11 @@ static int attend_impl(const tpl_kv_cache* c, const tpl_kv_batch* g, const tpl_k
     if (!a->q || !a->out) return fail_status(TPL_E_ARG, "q and out must not be NULL");
     if (!aligned16(a->q, a->q_token, a->q_head, 2) || !aligned16(a->out, a->o_token, a->o_head, 2))
         return fail_status(TPL_E_LAYOUT, "q and out must start, and their rows and heads lie, on 16 bytes");
-    if (q.few_bytes + q.tile_bytes > 0 && (!ws || ((uintptr_t)ws & 15))) return fail_status(TPL_E_ARG, "workspace must lie on 16 bytes");
-    if (ws_bytes < q.few_bytes + q.tile_bytes) return fail_status(TPL_E_ARG, "workspace is too small");
+    if (q.bytes() > 0 && (!ws || ((uintptr_t)ws & 15))) return fail_status(TPL_E_ARG, "workspace must lie on 16 bytes");
+    if (ws_bytes < q.bytes()) return fail_status(TPL_E_ARG, "workspace is too small");
     p.counters = (int*)ws;
     p.parts = (float*)((char*)ws + kCounters * 4);
-    p.tile_parts = (float*)((char*)ws + q.few_bytes);
+    p.tile_parts = (float*)((char*)p.parts + q.few_bytes);
     hipError_t e = hipSuccess;
     if (q.tile) e = launch_tile(p, q.dk, false, st);
     if (e == hipSuccess && q.few) e = launch_few(p, q.dc, q.mr, st);
@@ -220,7 +223,7 @@ int64_t tpl_kv_attend_workspace(const tpl_kv_cache* cache, const tpl_kv_batch* b
             tpl::fail_status(status, why);
             return -1;
         }
-        return q.few_bytes + q.tile_bytes;
+        return q.bytes();
     } catch (...) {
         return -1;
     }

@@ -1,0 +1,46 @@
+"""Paged key/value cache operators where calls meet each other or their limits, against the statement in 64 bits.
+
+Tolerances are those of tests/test_gpu_kv.py, whose checks these tests use."""
+
+from __future__ import annotations
+
+import math
+
+import pytest
+import torch
+
+from oracle import kv_oracle
+from tests import kv_cases
+from tests.test_gpu_kv import TYPES, check_append, check_attend, compare_attend, dev, on_gpu
+
+pytestmark = pytest.mark.gpu
+
+
+def attend_on(cache, host, g, news, lengths, table, heads, dtype, held8, scale=0.125):
+    """One call on a cache that lives on, against the statement."""
+    from tensor_layout_amd import kv
+    k, ks, v, vs = host
+    starts = [sum(news[:b]) for b in range(len(news) + 1)]
+    q = torch.randn((starts[-1], heads, k.shape[3]), generator=g).to(dtype)
+    want = kv_oracle.attend(q, k, v, ks, vs, table, starts, lengths, scale)
+    got, lse = torch.full(q.shape, 7.0, dtype=dtype, device="cuda"), torch.full(q.shape[:2], 7.0, device="cuda")
+    kv.attend(dev(q), cache, dev(table), dev(starts), dev(lengths), scale=scale, out=got, lse=lse)
+    compare_attend(got.cpu(), lse.cpu(), *want, v, vs, dtype, held8, k.shape[3], max(lengths))
+
+
+@pytest.mark.parametrize("dtype,held8", TYPES)
+def test_one_cache_for_a_prompt_and_the_tokens_after_it(dtype, held8):
+    """Calls of every kind in turn on one cache and stream: none leaves anything in the workspace that the next one meets."""
+    from tensor_layout_amd import kv
+    g = torch.Generator().manual_seed(41)
+    page, kv_heads, heads, dim, tokens = 32, 2, 8, 64, 2600
+    _, _, table, pages = kv_cases.batch(g, [1, 1], [tokens, 700], page)
+    host = kv_cases.pools(g, pages, page, kv_heads, dim, dtype, held8, 16, False)
+    cache = kv.PagedCache(on_gpu(host[0]), on_gpu(host[2]), dev(host[1]), dev(host[3]))
+    for _ in range(2):
+        attend_on(cache, host, g, [100], [2000], table[:1], heads, dtype, held8)   # one prompt's chunk, its tokens split
+        attend_on(cache, host, g, [1], [2001], table[:1], heads, dtype, held8)     # the token after it
+        attend_on(cache, host, g, [1, 1], [2002, 650], table, heads, dtype, held8)
+        attend_on(cache, host, g, [1, 90], [2003, 690], table, heads, dtype, held8)
+        torch.cuda.synchronize()
+        assert all(not bool(t[:kv.COUNTERS].any()) for _, _, t in cache._work.values())
