@@ -120,7 +120,8 @@ static const char* choose(const tpl_kv_cache* c, const tpl_kv_batch* g, const tp
         p.few = limit;
     }
     if (q.few) {
-        q.dc = c->dim <= 64 ? 4 : c->dim <= 128 ? 8 : c->dim % 12 == 0 ? 12 : 16;
+        // 16 lanes hold dc channels each: 12 only where those are whole lanes (144 and 192 channels).
+        q.dc = c->dim <= 64 ? 4 : c->dim <= 128 ? 8 : c->dim <= 192 && c->dim % 12 == 0 ? 12 : 16;
         // Rows of a tile: those of an average sequence, or of a decoding one
         // where the average is a prompt's.
         int64_t mean = (rows + g->batch - 1) / g->batch;

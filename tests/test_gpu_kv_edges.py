@@ -44,3 +44,12 @@ def test_one_cache_for_a_prompt_and_the_tokens_after_it(dtype, held8):
         attend_on(cache, host, g, [1, 90], [2003, 690], table, heads, dtype, held8)
         torch.cuda.synchronize()
         assert all(not bool(t[:kv.COUNTERS].any()) for _, _, t in cache._work.values())
+
+
+@pytest.mark.parametrize("dim", range(16, 257, 16))
+@pytest.mark.parametrize("dtype,held8", TYPES)
+def test_every_length_of_a_head(dim, dtype, held8):
+    """Single tokens, drafts and a chunk together, and a prompt by itself."""
+    check_attend(42, [1, 5, 70], [150, 60, 200], heads=8, kv_heads=2, dim=dim, dtype=dtype, held8=held8)
+    check_attend(43, [70], [130], heads=4, kv_heads=2, dim=dim, dtype=dtype, held8=held8)
+    check_attend(44, [4, 4], [90, 300], heads=8, kv_heads=2, dim=dim, dtype=dtype, held8=held8)
