@@ -400,6 +400,10 @@ __global__ void __launch_bounds__(256, few_blocks(HELD8, DC, MR)) k_few(AttendAr
 #pragma unroll
         for (int mr = 0; mr < MR; ++mr) {
             l[mr] = sum16(sum32(l[mr]));
+            // Scores that are no numbers pass a maximum by.  Where there were
+            // no others the sum tells them from a row that saw nothing: any
+            // reference then keeps them for the output.
+            if (m[mr] == neg_inf() && l[mr] != l[mr]) m[mr] = 0.0f;
             if (g == 0) {
                 mbuf[wave][mr * 16 + r] = m[mr];
                 lbuf[wave][mr * 16 + r] = l[mr];

@@ -536,6 +536,7 @@ __global__ void __launch_bounds__(WAVES * 64, D <= 128 ? 2 : 1) k_tile(AttendArg
     }
 
     l = sum32(l);
+    if (m == neg_inf() && l != l) m = 0.0f;   // scores that are no numbers, not a row that saw nothing
     // The row again, from the thread's number, rather than held throughout.
     int again = threadIdx.x;
     asm volatile("" : "+v"(again));

@@ -53,3 +53,33 @@ def test_every_length_of_a_head(dim, dtype, held8):
     check_attend(42, [1, 5, 70], [150, 60, 200], heads=8, kv_heads=2, dim=dim, dtype=dtype, held8=held8)
     check_attend(43, [70], [130], heads=4, kv_heads=2, dim=dim, dtype=dtype, held8=held8)
     check_attend(44, [4, 4], [90, 300], heads=8, kv_heads=2, dim=dim, dtype=dtype, held8=held8)
+
+
+@pytest.mark.parametrize("dtype,held8", TYPES)
+@pytest.mark.parametrize("news,lengths", [([1], [700]), ([1, 4], [33, 150]), ([100], [2000]), ([90, 1], [300, 40]), ([75], [203])])
+def test_queries_that_are_no_numbers(news, lengths, dtype, held8):
+    """A row whose scores are no numbers has no number for its output: it does not pass for one that sees nothing."""
+    def put(q, **_):
+        q[0, 0, 3] = math.nan
+        q[-1, 5] = math.nan
+    check_attend(45, news, lengths, heads=8, kv_heads=2, dim=64, dtype=dtype, held8=held8, tweak=put)
+
+
+@pytest.mark.parametrize("dtype,held8", TYPES)
+@pytest.mark.parametrize("news,lengths,at", [([1], [33], 32), ([1], [1], 0), ([1, 1], [640, 129], 128), ([4], [161], 157),
+                                             ([100], [2000], 1999), ([100], [2000], 512), ([90, 1], [300, 33], 32)])
+def test_a_key_that_is_no_number_shows_wherever_it_stands(news, lengths, at, dtype, held8):
+    """Also where no other token is taken by the same wave, or the same part of a split sequence."""
+    def put(k, table, **_):
+        b = len(table) - 1
+        k[table[b][at // 32], at % 32, 1, 7] = math.nan
+    check_attend(46, news, lengths, heads=8, kv_heads=2, dim=64, dtype=dtype, held8=held8, tweak=put)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("news,lengths,at", [([1], [33], 32), ([1], [640], 128), ([4], [161], 157), ([100], [2000], 512)])
+def test_a_key_without_end(news, lengths, at, dtype):
+    """Scores of plus and minus infinity, as the queries' signs have it."""
+    def put(k, table, **_):
+        k[table[0][at // 32], at % 32, 1, 7] = math.inf
+    check_attend(47, news, lengths, heads=8, kv_heads=2, dim=64, dtype=dtype, held8=False, tweak=put)
