@@ -117,8 +117,12 @@ __device__ __forceinline__ void load_tile(const AttendArgs& p, const Head& h, Pl
     x.ks = x.vs = 1.0f;
     if constexpr (HELD8) {
         const uint32_t blk = fdiv(slot, p.div_block);
-        x.ks = scalar(h.ks + (uint64_t)where * (uint32_t)p.c.ks_page + blk * (uint32_t)p.c.ks_block);
-        x.vs = scalar(h.vs + (uint64_t)where * (uint32_t)p.c.vs_page + blk * (uint32_t)p.c.vs_block);
+        const float ks = scalar(h.ks + (uint64_t)where * (uint32_t)p.c.ks_page + blk * (uint32_t)p.c.ks_block);
+        const float vs = scalar(h.vs + (uint64_t)where * (uint32_t)p.c.vs_page + blk * (uint32_t)p.c.vs_block);
+        // Page 0 may hold nothing, and its scales anything: a product with
+        // them would show in rows that do not see it.
+        x.ks = there ? ks : 1.0f;
+        x.vs = there ? vs : 1.0f;
     }
     const uint32_t kr = r * (uint32_t)(p.c.k_token * W);
 #pragma unroll

@@ -83,3 +83,37 @@ def test_a_key_without_end(news, lengths, at, dtype):
     def put(k, table, **_):
         k[table[0][at // 32], at % 32, 1, 7] = math.inf
     check_attend(47, news, lengths, heads=8, kv_heads=2, dim=64, dtype=dtype, held8=False, tweak=put)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+@pytest.mark.parametrize("news", [[1, 1, 1], [5, 2, 3], [90, 70, 1], [100]])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (40, 4)])
+def test_scales_of_pages_that_hold_nothing(news, window, sinks, bad, dtype):
+    """Pools and scales fresh from the allocator: what no token stands under is read by no row, page 0's among it."""
+    from tensor_layout_amd import kv
+    page, block, kv_heads, dim = 32, 16, 2, 64
+    g = torch.Generator().manual_seed(48)
+    lengths = [400, 500, 100][:len(news)]
+    starts, lengths, table, pages = kv_cases.batch(g, news, lengths, page)
+    spare = next(p for p in range(pages) if not any(p in row for row in table))
+    table = [[spare if p == 0 else p for p in row] for row in table]
+    for b, p in ((0, 0), (0, 3), (1, 1), (1, 11)):
+        if b < len(table):
+            table[b][p] = -1
+    k, ks, v, vs = kv_cases.pools(g, pages, page, kv_heads, dim, dtype, True, block, False)
+    for x in (k, v):
+        kv_cases.poison(x, table, lengths, page)
+    held = torch.zeros((pages, page // block), dtype=torch.bool)
+    for row, n in zip(table, lengths):
+        for j in range(0, n, block):
+            if row[j // page] >= 0:
+                held[row[j // page], j % page // block] = True
+    for x in (ks, vs):
+        x.copy_(torch.where(held[:, None], x, bad))
+    q = torch.randn((starts[-1], 4, dim), generator=g).to(dtype)
+    want = kv_oracle.attend(q, k, v, ks, vs, table, starts, lengths, 0.125, window, sinks)
+    got, lse = torch.empty_like(q, device="cuda"), torch.empty(q.shape[:2], device="cuda")
+    kv.attend(dev(q), kv.PagedCache(on_gpu(k), on_gpu(v), dev(ks), dev(vs)), dev(table), dev(starts), dev(lengths), scale=0.125,
+              window=window, sinks=sinks, out=got, lse=lse)
+    compare_attend(got.cpu(), lse.cpu(), *want, v, vs, dtype, True, dim, 500)
