@@ -18,7 +18,10 @@
  * or not a page of the pool is a page that is not there (its tokens are not
  * written, and no row sees them), and a sequence whose starts do not lie in
  * order inside the rows, that has more new tokens than its length, or more than
- * 2^30 tokens, is skipped.
+ * 2^30 tokens, is skipped and leaves the others as they are.  Of those others
+ * each one's rows lie behind the ones before it: where they do not, rows that
+ * two sequences claim, or that lie before an earlier sequence's, may be served
+ * for either or not at all.
  */
 #ifndef TPL_KV_H
 #define TPL_KV_H

@@ -246,6 +246,34 @@ __device__ __forceinline__ int locate(const AttendArgs& p, int share, int* at_b,
     return (int)total;
 }
 
+// The sequence that row tile x of the tile kernel belongs to: sequence b's
+// tiles are numbered from starts[b] / tile_tokens + b on, and of those in
+// order whose numbers begin at or before x it is the last.  64 are looked at
+// together, with all that is needed of them, so that it is known after one
+// load's latency.  b is -1 where there is none.
+struct TileSeq {
+    int b;
+    Seq s;
+};
+
+__device__ __forceinline__ TileSeq tile_seq(const AttendArgs& p, int x) {
+    const int lane = threadIdx.x & 63;
+    TileSeq t = {-1, {0, 0, 0}};
+    for (int b0 = 0; b0 < p.g.batch; b0 += 64) {
+        const int bb = b0 + lane < p.g.batch ? b0 + lane : p.g.batch - 1;
+        const Seq s = read_seq(p.g, bb);
+        const uint64_t m = __ballot(b0 + lane < p.g.batch && s.n > 0 && s.row0 / p.tile_tokens + bb <= x);
+        if (m) {
+            const int from = 63 - __builtin_clzll(m);
+            t.b = b0 + from;
+            t.s.row0 = __builtin_amdgcn_readlane(s.row0, from);
+            t.s.n = __builtin_amdgcn_readlane(s.n, from);
+            t.s.length = __builtin_amdgcn_readlane(s.length, from);
+        }
+    }
+    return t;
+}
+
 // Part of a row tile that one workgroup of the split kernel leaves: rows of
 // 16 * dc sums, then each row's reference and sum of weights.
 TPL_HD constexpr int few_part_floats(int dc, int mr) { return mr * 16 * (16 * dc + 2); }

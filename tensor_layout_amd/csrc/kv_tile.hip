@@ -78,15 +78,10 @@ __global__ void __launch_bounds__(WAVES * 64, D <= 128 ? 2 : 1) k_tile(AttendArg
     const int rest = blockIdx.x / p.c.kv_heads;
     const int split = rest % p.splits;
     const int x = p.tiles - 1 - rest / p.splits;
-    // Sequence b's tiles are numbered from starts[b] / tile_tokens + b.
-    int before = 0;
-    for (int b0 = 0; b0 < p.g.batch; b0 += 64) {
-        const int bb = b0 + lane;
-        before += __builtin_popcountll(__ballot(bb < p.g.batch && p.g.starts[bb] / p.tile_tokens + bb <= x));
-    }
-    if (before == 0) return;
-    const int b = before - 1;
-    const Seq s = read_seq(p.g, b);
+    const TileSeq mine = tile_seq(p, x);
+    const int b = mine.b;
+    const Seq s = mine.s;
+    if (b < 0) return;
     if ((int64_t)s.n * p.group <= p.few) return;
     const int t0 = (x - s.row0 / p.tile_tokens - b) * p.tile_tokens;   // the tile's first new token
     if (t0 < 0 || t0 >= s.n) return;
@@ -582,16 +577,11 @@ constexpr int kJoinBlocks = 8;   // of a row tile
 template <typename T, int D>
 __global__ void __launch_bounds__(256) k_tile_join(AttendArgs p) {
     typedef typename T::one one;
-    const int lane = threadIdx.x & 63;
     const int h = blockIdx.x % p.c.kv_heads, x = blockIdx.x / p.c.kv_heads;
-    int before = 0;
-    for (int b0 = 0; b0 < p.g.batch; b0 += 64) {
-        const int bb = b0 + lane;
-        before += __builtin_popcountll(__ballot(bb < p.g.batch && p.g.starts[bb] / p.tile_tokens + bb <= x));
-    }
-    if (before == 0) return;
-    const int b = before - 1;
-    const Seq s = read_seq(p.g, b);
+    const TileSeq mine = tile_seq(p, x);
+    const int b = mine.b;
+    const Seq s = mine.s;
+    if (b < 0) return;
     if ((int64_t)s.n * p.group <= p.few) return;
     const int t0 = (x - s.row0 / p.tile_tokens - b) * p.tile_tokens;
     if (t0 < 0 || t0 >= s.n) return;

@@ -117,3 +117,37 @@ def test_scales_of_pages_that_hold_nothing(news, window, sinks, bad, dtype):
     kv.attend(dev(q), kv.PagedCache(on_gpu(k), on_gpu(v), dev(ks), dev(vs)), dev(table), dev(starts), dev(lengths), scale=0.125,
               window=window, sinks=sinks, out=got, lse=lse)
     compare_attend(got.cpu(), lse.cpu(), *want, v, vs, dtype, True, dim, 500)
+
+
+def out_of_order(*changes):
+    """starts[b] = x for each (b, x): the sequences on both sides of it are out of order, all others stay as they are."""
+    def put(starts, **_):
+        for b, x in changes:
+            starts[b] = x
+    return put
+
+
+BAD_STARTS = [((1, 10_000),), ((2, -50),), ((1, 1 << 30), (4, -(1 << 30))), ((5, 0),), ((3, 10_000), (4, 5))]
+
+
+@pytest.mark.parametrize("changes", BAD_STARTS)
+@pytest.mark.parametrize("news", [[40, 40, 150, 1, 130, 90], [80] * 6, [3, 1, 2, 5, 1, 2]])
+def test_prompts_beside_a_sequence_that_is_skipped(news, changes):
+    check_attend(49, news, [n + (60 if n > 8 else 1) for n in news], heads=8, kv_heads=2, dim=64, dtype=torch.bfloat16, held8=True,
+                 tweak=out_of_order(*changes))
+
+
+def test_split_prompts_beside_a_sequence_that_is_skipped():
+    check_attend(50, [10, 60, 90], [70, 1500, 1200], heads=4, kv_heads=1, dim=64, dtype=torch.float16, held8=False,
+                 tweak=out_of_order((1, 500), (0, -3)))
+    def long(lengths, **_):
+        lengths[0] = (1 << 30) + 1
+    check_attend(51, [80, 60, 90], [90, 1500, 1200], heads=4, kv_heads=1, dim=64, dtype=torch.bfloat16, held8=False, width=60,
+                 tweak=long)
+
+
+def test_prompts_of_many_sequences_some_of_which_are_skipped():
+    """Over 64 sequences: they are looked through 64 at a time."""
+    n = [1 + 37 * i % 60 for i in range(150)]
+    check_attend(52, n, [x + 5 for x in n], heads=4, kv_heads=1, dim=16, dtype=torch.bfloat16, held8=True, page=16,
+                 tweak=out_of_order((3, 1 << 20), (70, -4), (149, 0)))
