@@ -215,32 +215,32 @@ __global__ void __launch_bounds__(256, 4) k_append(AppendArgs p) {
     const int id = blockIdx.x, unit = p.unit;
 
     // The sequence of this group: 64 are looked at together, with all that is
-    // needed of them, so that it is known after one load's latency.  A row's
-    // sequence is first looked for at the row's own number and before: most
-    // sequences of a batch of rows have one each.
+    // needed of them, so that it is known after one load's latency; of those in
+    // order it is the last that has the row, or whose groups' numbers begin at
+    // or before this one.  A row's sequence is first looked for at the row's
+    // own number and before: most sequences of a batch of rows have one each.
     int b = -1;
     Seq s = {0, 0, 0};
     auto look = [&](int b0) {
         const int bb = b0 + lane < g.batch ? b0 + lane : g.batch - 1;
-        const int r = g.starts[bb], e = g.starts[bb + 1], n = g.lengths[bb];
-        const bool there = b0 + lane < g.batch && (p.by_token ? (r <= id && id < e) : (r / unit + 2 * bb <= id));
+        const Seq x = read_seq(g, bb);
+        const bool there = b0 + lane < g.batch && x.n > 0 &&
+                           (p.by_token ? (x.row0 <= id && id < x.row0 + x.n) : (x.row0 / unit + 2 * bb <= id));
         const uint64_t m = __ballot(there);
-        if (m) {   // the last of them
+        if (m) {
             const int from = 63 - __builtin_clzll(m);
             b = b0 + from;
-            s.row0 = __builtin_amdgcn_readlane(r, from);
-            s.n = __builtin_amdgcn_readlane(e, from);
-            s.length = __builtin_amdgcn_readlane(n, from);
+            s.row0 = __builtin_amdgcn_readlane(x.row0, from);
+            s.n = __builtin_amdgcn_readlane(x.n, from);
+            s.length = __builtin_amdgcn_readlane(x.length, from);
         }
-        return m;
+        return m != 0;
     };
     const int near = id < g.batch ? id : g.batch - 1;
-    if (!p.by_token || look(near > 63 ? near - 63 : 0) == 0)
+    if (!p.by_token || !look(near > 63 ? near - 63 : 0))
         for (int b0 = 0; b0 < g.batch; b0 += 64)
-            if (look(b0) != ~0ull && (b >= 0 || !p.by_token)) break;
+            if (look(b0) && p.by_token) break;
     if (b < 0) return;
-    s = ordered(s.row0, s.n, s.length, g.tokens);
-    if (s.n == 0) return;
     const int first = s.length - s.n;   // index of the sequence's first new token
     int i0;                             // index of the group's first token
     if (p.by_token) {

@@ -151,3 +151,18 @@ def test_prompts_of_many_sequences_some_of_which_are_skipped():
     n = [1 + 37 * i % 60 for i in range(150)]
     check_attend(52, n, [x + 5 for x in n], heads=4, kv_heads=1, dim=16, dtype=torch.bfloat16, held8=True, page=16,
                  tweak=out_of_order((3, 1 << 20), (70, -4), (149, 0)))
+
+
+@pytest.mark.parametrize("changes", BAD_STARTS)
+@pytest.mark.parametrize("news", [[40, 40, 150, 1, 130, 90], [80] * 6, [1] * 6, [2, 1, 3, 1, 1, 2]])
+@pytest.mark.parametrize("held8", [True, False])
+def test_append_beside_a_sequence_that_is_skipped(news, changes, held8):
+    check_append(53, news, [n + (60 if n > 8 else 1) for n in news], heads=4, kv_heads=2, dim=64, dtype=torch.bfloat16, held8=held8,
+                 tweak=out_of_order(*changes))
+
+
+@pytest.mark.parametrize("n", [1, 20])
+@pytest.mark.parametrize("held8", [True, False])
+def test_append_of_many_sequences_some_of_which_are_skipped(n, held8):
+    check_append(54, [n] * 150, [n + 7 * i % 30 for i in range(150)], heads=2, kv_heads=1, dim=16, dtype=torch.bfloat16, held8=held8,
+                 page=16, tweak=out_of_order((3, 1 << 20), (70, -4), (100, 9), (140, 1 << 30)))
