@@ -302,23 +302,36 @@ def _workspace(cache, batch, args):
     return size
 
 
+def _on(cache, s, stream):
+    """The call's stream as torch's current one: `s`, where the call names it."""
+    return torch.cuda.stream(None if stream is None else torch.cuda.ExternalStream(s, device=cache.device))
+
+
+def _capturing(cache, s, stream):
+    """Whether the call's own stream is being captured, whatever torch's current one is."""
+    if stream is None:
+        return torch.cuda.is_current_stream_capturing()
+    with _on(cache, s, stream):
+        return torch.cuda.is_current_stream_capturing()
+
+
 def _attend_packed(cache, batch, args, size, stream):
     """The call itself, with a workspace of the stream's own."""
     index = cache._index
     s = _stream(index) if stream is None else int(stream)
     ws = cache._work.get(s)
-    if ws is None or ws[1] < size or torch.cuda.is_current_stream_capturing():
-        ws = _new_workspace(cache, size, s, stream is not None)
+    if ws is None or ws[1] < size or _capturing(cache, s, stream):
+        ws = _new_workspace(cache, size, s, stream)
     return _calls[1](cache._at, batch, args, ws[0], size, s)
 
 
-def _new_workspace(cache, size, s, named):
+def _new_workspace(cache, size, s, stream):
     """(address, size, tensor), its counters cleared once: every call leaves them zero.
 
     Calls on one stream follow one another and share it.  A captured call has
     one to itself, whose counters the graph clears: it may be replayed beside eager
     calls on the stream it was captured on."""
-    with torch.cuda.stream(torch.cuda.ExternalStream(s, device=cache.device) if named else None):
+    with _on(cache, s, stream):
         capturing = torch.cuda.is_current_stream_capturing()
         t = torch.empty(size if capturing else max(size, 1 << 20), dtype=torch.uint8, device=cache.device)
         t[:COUNTERS].zero_()
@@ -348,7 +361,7 @@ def attend(q, cache: PagedCache, table, starts, lengths, *, scale: Optional[floa
     if index >= 0 and _device() == index:
         s = _stream(index) if stream is None else int(stream)
         ws = cache._work.get(s)
-        if ws is not None and not torch.cuda.is_current_stream_capturing():
+        if ws is not None and not _capturing(cache, s, stream):
             status = _attend(cache._at, index, q, table, starts, lengths, scale, window, sinks, out, lse, ws[0], ws[1], s)
             if status == 0:
                 return out

@@ -166,3 +166,67 @@ def test_append_beside_a_sequence_that_is_skipped(news, changes, held8):
 def test_append_of_many_sequences_some_of_which_are_skipped(n, held8):
     check_append(54, [n] * 150, [n + 7 * i % 30 for i in range(150)], heads=2, kv_heads=1, dim=16, dtype=torch.bfloat16, held8=held8,
                  page=16, tweak=out_of_order((3, 1 << 20), (70, -4), (100, 9), (140, 1 << 30)))
+
+
+# ---------------------------------------------------------------- streams
+
+
+def step_on(cache, g, new=1, length=1500, heads=8, kv_heads=2, dim=64):
+    """Arguments of one attend call of a sequence on pages in order, and its queries on the GPU."""
+    table = dev([list(range(cache.k.shape[0]))])
+    return torch.randn((new, heads, dim), generator=g).to(cache.k.dtype).cuda(), table, dev([0, new]), dev([length])
+
+
+def small_cache(g, pages=60, page=32, kv_heads=2, dim=64, dtype=torch.bfloat16):
+    from tensor_layout_amd import kv
+    k, _, v, _ = kv_cases.pools(g, pages, page, kv_heads, dim, dtype, False, 16, False)
+    return kv.PagedCache(k.cuda(), v.cuda())
+
+
+def test_a_graph_captured_on_a_named_stream_has_its_own_workspace():
+    """The named stream is the one that captures, whatever torch's current one is: replays leave the eager calls' memory alone."""
+    from tensor_layout_amd import kv
+    g = torch.Generator().manual_seed(55)
+    cache = small_cache(g)
+    q, table, starts, lengths = step_on(cache, g)
+    side, other = torch.cuda.Stream(), torch.cuda.Stream()
+    name = side.cuda_stream
+    want = kv.attend(q, cache, table, starts, lengths)
+    side.wait_stream(torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    out = torch.empty_like(q)
+    kv.attend(q, cache, table, starts, lengths, out=out, stream=name)   # an eager call first: the stream has a workspace
+    torch.cuda.synchronize()
+    before = dict(cache._work)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        with torch.cuda.stream(other):
+            kv.attend(q, cache, table, starts, lengths, out=out, stream=name)
+    assert cache._work == before
+    mine = cache._work[name][2]
+    mine[kv.COUNTERS:].fill_(0x5A)
+    for _ in range(3):
+        out.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+        assert bool((mine[kv.COUNTERS:] == 0x5A).all()) and not bool(mine[:kv.COUNTERS].any())
+    kv.attend(q, cache, table, starts, lengths, out=out.zero_(), stream=name)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+
+
+def test_the_default_stream_by_its_name():
+    from tensor_layout_amd import kv
+    g = torch.Generator().manual_seed(64)
+    cache = small_cache(g)
+    q, table, starts, lengths = step_on(cache, g, new=3)
+    want = kv.attend(q, cache, table, starts, lengths)
+    other = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(other):
+        for _ in range(2):
+            out = kv.attend(q, cache, table, starts, lengths, stream=0)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
