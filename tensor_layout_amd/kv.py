@@ -219,7 +219,7 @@ def append(cache: PagedCache, k, v, table, starts, lengths, *, q=None, q_out=Non
     if _lib is None:
         load()
     if q is not None and q_out is None:
-        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        q_out = _result(q, cache, stream)
     index = cache._index
     if index >= 0 and _device() == index:
         status = _append(cache._at, index, k, v, table, starts, lengths, q, q_out, inv_freq, positions, sections, interleaved,
@@ -307,6 +307,14 @@ def _on(cache, s, stream):
     return torch.cuda.stream(None if stream is None else torch.cuda.ExternalStream(s, device=cache.device))
 
 
+def _result(q, cache, stream):
+    """A new tensor like `q` for the call to write: memory of the call's own stream, not what the current one has just given back."""
+    if stream is None or cache._index < 0:
+        return torch.empty_like(q, memory_format=torch.contiguous_format)
+    with _on(cache, int(stream), stream):
+        return torch.empty_like(q, memory_format=torch.contiguous_format)
+
+
 def _capturing(cache, s, stream):
     """Whether the call's own stream is being captured, whatever torch's current one is."""
     if stream is None:
@@ -356,7 +364,7 @@ def attend(q, cache: PagedCache, table, starts, lengths, *, scale: Optional[floa
     if _lib is None:
         load()
     if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        out = _result(q, cache, stream)
     index = cache._index
     if index >= 0 and _device() == index:
         s = _stream(index) if stream is None else int(stream)

@@ -230,3 +230,24 @@ def test_the_default_stream_by_its_name():
             out = kv.attend(q, cache, table, starts, lengths, stream=0)
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+def test_a_result_made_for_a_named_stream_is_that_streams():
+    """Memory that the current stream has just given back may still be at work there: it is not what a call on another
+    stream gets for its result."""
+    from tensor_layout_amd import kv
+    g = torch.Generator().manual_seed(56)
+    cache = small_cache(g)
+    q, table, starts, lengths = step_on(cache, g, new=40)
+    k = torch.randn((40, 2, 64), generator=g).to(cache.k.dtype).cuda()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for call in (lambda: kv.attend(q, cache, table, starts, lengths, stream=side.cuda_stream),
+                 lambda: kv.append(cache, k, k, table, starts, lengths, q=q, stream=side.cuda_stream)):
+        freed = torch.empty_like(q)
+        at = freed.data_ptr()
+        del freed
+        out = call()
+        assert out.data_ptr() != at
+        assert torch.empty_like(q).data_ptr() == at
+        torch.cuda.synchronize()
