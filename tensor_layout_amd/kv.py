@@ -298,7 +298,7 @@ def _workspace(cache, batch, args):
     load()
     size = _calls[2](cache._at, batch, args)
     if size < 0:
-        raise TplError(tpl.TPL_E_ARG, tpl.tpl_last_error())
+        _raise(_calls[1](cache._at, batch, args, None, 0, None))   # refused the same way, before anything is looked at on the device
     return size
 
 
