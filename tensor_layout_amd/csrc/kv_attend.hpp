@@ -13,6 +13,12 @@ constexpr float kLn2 = 0.69314718055994530942f;
 // by this many powers of two, so that most tiles leave the accumulators as
 // they are; weights reach 2^8 then, far from any type's end.
 constexpr float kSlack = 8.0f;
+// Weights that are multiplied as fp16 numbers have a reference this much under
+// the largest score: they reach 2^15, and the ones that fp16 can no longer
+// hold are under 2^-32 of the largest instead of 2^-25.  100000 tokens of the
+// latter are 0.3 % of a row's sum, which counts them all.
+template <typename V>
+__device__ constexpr float lift() { return std::is_same<V, Fp16>::value ? 7.0f : 0.0f; }
 
 struct AttendArgs {
     tpl_kv_cache c;

@@ -316,6 +316,7 @@ __global__ void __launch_bounds__(256, few_blocks(HELD8, DC, MR)) k_few(AttendAr
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
                     top = fmaxf(top, f2[u] * fmaxf(fmaxf(sc[mr][u][0], sc[mr][u][1]), fmaxf(sc[mr][u][2], sc[mr][u][3])));
+                top -= lift<V>();
                 if (__any(top > m[mr] + kSlack)) {
                     top = max16(max32(fmaxf(top, m[mr])));
                     const float a = top == neg_inf() ? 1.0f : exp2_(m[mr] - top);

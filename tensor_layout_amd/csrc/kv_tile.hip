@@ -434,6 +434,7 @@ __global__ void __launch_bounds__(WAVES * 64, D <= 128 ? 2 : 1) k_tile(AttendArg
                 for (int i = 0; i < 8; ++i) t = fmaxf(t, sc[z >> 1][(z & 1) * 8 + i]);
                 top = fmaxf(top, t * f2[z]);
             }
+            top -= lift<V>();
             if (__any(top > m + kSlack)) {
                 top = max32(fmaxf(top, m));
                 const float a = top == neg_inf() ? 1.0f : exp2_(m - top);

@@ -251,3 +251,21 @@ def test_a_result_made_for_a_named_stream_is_that_streams():
         assert out.data_ptr() != at
         assert torch.empty_like(q).data_ptr() == at
         torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("n,length", [(1, 31), (5, 36), (100, 400)])
+def test_many_small_weights_of_an_fp16_cache(n, length):
+    """Weights 2^-26 of the largest: together they are most of an output, and none may be lost for being small.
+
+    Token 0 has a score of 26 log 2 and a value of zero, all others a score of zero and a value of 30000.  Row i's
+    output is c 30000 2^-26 / (1 + c 2^-26) with c other tokens, off by the scores' rounding (2^-20 of it at most) and
+    by its own rounding in fp16, at outputs under 2^-14 by half of the smallest number."""
+    from tensor_layout_amd import kv
+    k, v = torch.zeros((16, 32, 1, 64)).half(), torch.full((16, 32, 1, 64), 30000.0).half()
+    k[0, 0, 0, 0], v[0, 0] = 26.0, 0.0
+    q = torch.zeros((n, 2, 64)).half()
+    q[:, :, 0] = 1.0
+    got = kv.attend(dev(q), kv.PagedCache(dev(k), dev(v)), dev([list(range(16))]), dev([0, n]), dev([length]), scale=math.log(2.0))
+    c = torch.arange(length - n, length, dtype=torch.float64)[:, None, None]
+    want = c * 30000 * 2.0 ** -26 / (1 + c * 2.0 ** -26)
+    assert bool(((got.cpu().double() - want).abs() <= (2.0 ** -11 + 2.0 ** -20) * want + 2.0 ** -25).all())
