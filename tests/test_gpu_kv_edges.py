@@ -11,6 +11,7 @@ import torch
 
 from oracle import kv_oracle
 from tests import kv_cases
+from tests.kv_cases import half_step
 from tests.test_gpu_kv import TYPES, check_append, check_attend, compare_attend, dev, on_gpu
 
 pytestmark = pytest.mark.gpu
@@ -269,3 +270,37 @@ def test_many_small_weights_of_an_fp16_cache(n, length):
     c = torch.arange(length - n, length, dtype=torch.float64)[:, None, None]
     want = c * 30000 * 2.0 ** -26 / (1 + c * 2.0 ** -26)
     assert bool(((got.cpu().double() - want).abs() <= (2.0 ** -11 + 2.0 ** -20) * want + 2.0 ** -25).all())
+
+
+@pytest.mark.parametrize("dtype,held8", TYPES)
+@pytest.mark.parametrize("news,lengths", [([1, 1, 1], [2, 150, 700]), ([4, 3], [9, 400]), ([8], [300])])
+def test_weights_of_few_rows_keep_16_bits(news, lengths, dtype, held8):
+    """Values that cancel: an output far under the sum of |weight * value| shows its weights' rounding.
+
+    Over e4m3 a weight is two bf16 numbers, each off by half a step (2^-8) of what it holds: 2^-16.  Over bf16 the first
+    is cut off, a step (2^-7) at most, and the second is off by half a step of that and 2^-20 of the weight.  Over fp16
+    it is one number, half a step of 2^-11, and 2^-32 of the largest at least.  The exponential and the sum: 2^-19."""
+    from tensor_layout_amd import kv
+    g = torch.Generator().manual_seed(57)
+    starts, lengths, table, pages = kv_cases.batch(g, news, lengths, 32)
+    k, ks, v, vs = kv_cases.pools(g, pages, 32, 2, 64, dtype, held8, 16, False)
+    q = torch.randn((starts[-1], 8, 64), generator=g).to(dtype)
+    out, _, size, score = kv_oracle.attend(q, k, v, ks, vs, table, starts, lengths, 0.125)
+    got = kv.attend(dev(q), kv.PagedCache(on_gpu(k), on_gpu(v), dev(ks), dev(vs)), dev(table), dev(starts), dev(lengths)).cpu()
+    u_w = 2.0 ** -16 if held8 else 2.0 ** -15 + 2.0 ** -20 if dtype == torch.bfloat16 else 2.0 ** -11
+    tol = (2 * torch.expm1((64 + 8) * 2.0 ** -24 * score)[..., None] + u_w + 2.0 ** -19) * size + half_step(dtype) * out.abs()
+    if dtype == torch.float16:
+        tol += 2.0 ** -25   # an output under fp16's normal numbers
+        tol += 0.0 if held8 else max(lengths) * 2.0 ** -32 * float(v.float().abs().max())
+    assert bool(((got.double() - out).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("value", [math.inf, -math.inf])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("news,lengths", [([1, 1], [40, 900]), ([4, 2], [40, 900]), ([8], [300]), ([70], [200])])
+def test_infinite_values_that_all_rows_see(news, lengths, dtype, value):
+    """They come out as they are, whatever their weights' bits."""
+    def put(v, table, **_):
+        for j in range(0, 33, 3):
+            v[table[-1][j // 32], j % 32, j % 2, j] = value
+    check_attend(65, news, lengths, heads=16, kv_heads=2, dim=64, dtype=dtype, held8=False, tweak=put, spread=1.0)
