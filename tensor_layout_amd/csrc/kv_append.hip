@@ -99,12 +99,29 @@ __device__ __forceinline__ Raw<MODE> load_raw(const typename T::one* row, int ch
     return r;
 }
 
-// The channels, rotated.  `cs`: the row's table of (cos, sin).  Products are
+// (cos, sin) of a row's pairs, taken where they are asked for: what stands for
+// a row of the workgroup's table where there is none.
+struct Taken {
+    const AppendArgs& p;
+    int row, index;   // of the token: its row, and its place in its sequence
+    __device__ __forceinline__ float2 operator[](int f) const {
+        int pos = index;
+        if (p.a.positions) {
+            int axis = 0;
+#pragma unroll
+            for (int k = 0; k < TPL_KV_MAX_AXES - 1; ++k) axis += (k + 1 < p.a.axes && f >= p.sec_end[k]) ? 1 : 0;
+            pos = p.a.positions[axis * p.a.positions_row + row];
+        }
+        return cos_sin((double)pos * (double)p.a.inv_freq[f]);
+    }
+};
+
+// The channels, rotated.  `cs`: the row's (cos, sin) by pair.  Products are
 // rounded before they are added, as the formula's plain evaluation does, so
 // that a block's maximum does not depend on which of the two products a fused
 // multiply-add would keep whole.
-template <typename T, int MODE, int FROM>
-__device__ __forceinline__ void rotate(const Raw<FROM>& r, const typename T::one* row, int ch, int half, const float2* cs,
+template <typename T, int MODE, int FROM, typename Angles>
+__device__ __forceinline__ void rotate(const Raw<FROM>& r, const typename T::one* row, int ch, int half, Angles cs,
                                        float (&y)[8]) {
 #pragma clang fp contract(off)
 #pragma unroll
@@ -129,14 +146,14 @@ __device__ __forceinline__ void rotate(const Raw<FROM>& r, const typename T::one
             const int c = ch + 4 * j;
             if (c < 2 * half) {
                 const bool first = c < half;
-                const float2* t = cs + (first ? c : c - half);
                 const uint32_t sign = first ? 0x80000000u : 0u;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const uint32_t w = r.other[j][i >> 1];
                     const float b = (i & 1) ? hi16<T>(w) : lo16<T>(w);
-                    const float sn = t[i].y;
-                    const float x = y[4 * j + i] * t[i].x, z = b * __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, sn) ^ sign);
+                    const float2 t = cs[(first ? c : c - half) + i];
+                    const float sn = t.y;
+                    const float x = y[4 * j + i] * t.x, z = b * __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, sn) ^ sign);
                     y[4 * j + i] = x + z;
                 }
             }
@@ -202,9 +219,13 @@ __device__ __forceinline__ float scale_of(float amax) {
     return __builtin_amdgcn_ldexpf(1.0f, e);
 }
 
-// U: rows of a lane whose loads are under way at once.
-template <typename T, bool HELD8, int U, int MODE>
-__global__ void __launch_bounds__(256, 4) k_append(AppendArgs p) {
+// U: rows of a lane whose loads are under way at once.  TABLE: the angles of
+// all tokens of a group fit the workgroup's LDS.  Where they do not (blocks of
+// over 128 tokens at 128 channels) those of keys, and of by_token's queries,
+// are taken for each head and pass anew, which bounds the call: the three
+// prompts named above take 350 us in blocks of 256 tokens, 67 in blocks of 128.
+template <typename T, bool HELD8, int U, int MODE, bool TABLE>
+__global__ void __launch_bounds__(256, TABLE ? 4 : 2) k_append(AppendArgs p) {
     typedef typename T::one one;
     constexpr int WAVES = 4;
     extern __shared__ float2 table[];
@@ -284,7 +305,7 @@ __global__ void __launch_bounds__(256, 4) k_append(AppendArgs p) {
     };
     if (!queries && h < c.kv_heads) load(0);
 
-    if (pairs && (keys || queries)) {
+    if (pairs && (TABLE ? keys || queries : queries && !p.by_token)) {
         for (int i = threadIdx.x; i < (to_ - from) * pairs; i += 64 * WAVES) {
             const int u = i / pairs, f = i - u * pairs, t = from + u;
             int pos = i0 + t;
@@ -311,7 +332,10 @@ __global__ void __launch_bounds__(256, 4) k_append(AppendArgs p) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int i = t0 + u * rpw + lr, j = i < count ? i : count - 1;
-                rotate<T, M>(raw[u], x + j * xs, mine ? ch : 0, pairs, table + j * pairs, y[u]);
+                if constexpr (TABLE)
+                    rotate<T, M>(raw[u], x + j * xs, mine ? ch : 0, pairs, table + j * pairs, y[u]);
+                else
+                    rotate<T, M>(raw[u], x + j * xs, mine ? ch : 0, pairs, Taken{p, row0 + j, i0 + j}, y[u]);
             }
         };
         if constexpr (!HELD8) {
@@ -348,7 +372,10 @@ __global__ void __launch_bounds__(256, 4) k_append(AppendArgs p) {
                 for (int t = lr; t < count; t += rpw) {
                     if (!mine) break;
                     float z[8];
-                    rotate<T, M>(load_raw<T, M>(x + t * xs, ch, pairs), x + t * xs, ch, pairs, table + t * pairs, z);
+                    if constexpr (TABLE)
+                        rotate<T, M>(load_raw<T, M>(x + t * xs, ch, pairs), x + t * xs, ch, pairs, table + t * pairs, z);
+                    else
+                        rotate<T, M>(load_raw<T, M>(x + t * xs, ch, pairs), x + t * xs, ch, pairs, Taken{p, row0 + t, i0 + t}, z);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) amax = finite(z[i]) ? fmaxf(amax, __builtin_fabsf(z[i])) : amax;
                 }
@@ -421,8 +448,14 @@ __global__ void __launch_bounds__(256, 4) k_append(AppendArgs p) {
             const int r = r0 + u * stride + lr;
             if (mine && r < rows) {
                 const int t = r / a.heads, hq = r - t * a.heads;
+                const one* x = (const one*)a.q + (row0 + from + t) * a.q_token + hq * a.q_head;
                 float y[8];
-                rotate<T, MODE>(w[u], (const one*)a.q + (row0 + from + t) * a.q_token + hq * a.q_head, ch, pairs, table + t * pairs, y);
+                if constexpr (TABLE)
+                    rotate<T, MODE>(w[u], x, ch, pairs, table + t * pairs, y);
+                else if (p.by_token)
+                    rotate<T, MODE>(w[u], x, ch, pairs, Taken{p, row0 + from + t, i0 + from + t}, y);
+                else
+                    rotate<T, MODE>(w[u], x, ch, pairs, table + t * pairs, y);
                 store8<T>((one*)a.q_out + (row0 + from + t) * a.o_token + hq * a.o_head + ch, y);
             }
         }
@@ -432,11 +465,11 @@ __global__ void __launch_bounds__(256, 4) k_append(AppendArgs p) {
 template <typename T, bool HELD8, int MODE>
 static void launch_u(const AppendArgs& p, int u, dim3 grid, size_t lds, hipStream_t st) {
     if (u == 1)
-        k_append<T, HELD8, 1, MODE><<<grid, 256, lds, st>>>(p);
+        k_append<T, HELD8, 1, MODE, true><<<grid, 256, lds, st>>>(p);
     else if (u == 2)
-        k_append<T, HELD8, 2, MODE><<<grid, 256, lds, st>>>(p);
+        k_append<T, HELD8, 2, MODE, true><<<grid, 256, lds, st>>>(p);
     else
-        k_append<T, HELD8, 4, MODE><<<grid, 256, lds, st>>>(p);
+        k_append<T, HELD8, 4, MODE, true><<<grid, 256, lds, st>>>(p);
 }
 
 template <typename T, bool HELD8>
@@ -449,6 +482,15 @@ static hipError_t launch_mode(const AppendArgs& p, int u, dim3 grid, size_t lds,
         launch_u<T, HELD8, kQuads>(p, u, grid, lds, st);
     else
         launch_u<T, HELD8, kSingles>(p, u, grid, lds, st);
+    return hipGetLastError();
+}
+
+template <typename T>
+static hipError_t launch_long(const AppendArgs& p, dim3 grid, size_t lds, hipStream_t st) {
+    if (p.a.interleaved)
+        k_append<T, true, 1, kPairs, false><<<grid, 256, lds, st>>>(p);
+    else
+        k_append<T, true, 1, kSingles, false><<<grid, 256, lds, st>>>(p);
     return hipGetLastError();
 }
 
@@ -514,16 +556,28 @@ static int append_impl(const tpl_kv_cache* c, const tpl_kv_batch* g, const tpl_k
     const int rpw = 64 / (c->dim / 8);
     const int u = p.by_token ? 1 : p.unit > 2 * rpw ? 4 : 2;
     // A head a wave; the queries of single tokens in slices of a row a wave,
-    // those of longer groups by kQueryTokens tokens.
+    // those of longer groups by kQueryTokens tokens, or by 4 times as many
+    // where a block's would be more workgroups than grid.y takes.
     p.ky = (c->kv_heads + 3) / 4;
     p.qt = 1, p.q_tokens = p.unit, p.q_slices = 0;
     if (a->q && p.by_token) p.q_slices = (int)((a->heads + 4 * (int64_t)rpw - 1) / (4 * rpw));
-    if (a->q && !p.by_token) p.qt = p.unit / kQueryTokens, p.q_tokens = kQueryTokens, p.q_slices = 1;
+    if (a->q && !p.by_token) {
+        p.q_tokens = p.unit <= 32768 * kQueryTokens ? kQueryTokens : 4 * kQueryTokens;
+        p.qt = (p.unit + p.q_tokens - 1) / p.q_tokens, p.q_slices = 1;
+    }
     const int64_t gy = 2 * p.ky + p.qt * p.q_slices;
-    const size_t lds = a->inv_freq ? (size_t)p.unit * (a->rot / 2) * sizeof(float2) : 0;
-    if (lds > 64 * 1024) return fail_status(TPL_E_ARG, "block * rotated channels must be at most 16384");
+    // The table of angles: a group's tokens are no more than there are.  Over
+    // 64 KiB only queries of longer groups have one.
+    const int64_t angle = p.a.rot / 2 * (int64_t)sizeof(float2);
+    int64_t lds = (p.unit < g->tokens ? p.unit : g->tokens) * angle;
+    const bool fits = lds <= 64 * 1024;
+    if (!fits) lds = a->q && !p.by_token ? p.q_tokens * angle : 0;
     const dim3 grid((unsigned)gx, (unsigned)gy);
-    const hipError_t e = a->type == TPL_KV_BF16 ? launch_append<Bf16>(p, u, grid, lds, st) : launch_append<Fp16>(p, u, grid, lds, st);
+    hipError_t e;
+    if (a->type == TPL_KV_BF16)
+        e = fits ? launch_append<Bf16>(p, u, grid, (size_t)lds, st) : launch_long<Bf16>(p, grid, (size_t)lds, st);
+    else
+        e = fits ? launch_append<Fp16>(p, u, grid, (size_t)lds, st) : launch_long<Fp16>(p, grid, (size_t)lds, st);
     if (e != hipSuccess) return fail_status(TPL_E_HIP, std::string("HIP launch failed: ") + hipGetErrorString(e));
     return TPL_OK;
 }

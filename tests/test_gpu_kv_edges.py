@@ -304,3 +304,32 @@ def test_infinite_values_that_all_rows_see(news, lengths, dtype, value):
         for j in range(0, 33, 3):
             v[table[-1][j // 32], j % 32, j % 2, j] = value
     check_attend(65, news, lengths, heads=16, kv_heads=2, dim=64, dtype=dtype, held8=False, tweak=put, spread=1.0)
+
+
+@pytest.mark.parametrize("page,block,dim,rot,interleaved", [(256, 256, 128, 128, False), (256, 128, 256, 256, True), (1024, 512, 64, 64, False),
+                                                            (512, 512, 128, 36, False), (512, 256, 256, 130, True)])
+@pytest.mark.parametrize("news,lengths", [([700, 1, 300], [900, 77, 300]), ([1] * 150, [1 + 37 * i % 400 for i in range(150)]), ([140], [530])])
+def test_append_to_long_blocks(page, block, dim, rot, interleaved, news, lengths):
+    """One scale for so many tokens that their angles do not fit a workgroup's memory."""
+    sections = (rot // 8, rot // 2 - rot // 8) if interleaved else None
+    far = 100_000 if interleaved else None
+    check_append(66, news, lengths, heads=3, kv_heads=2, dim=dim, dtype=torch.bfloat16 if interleaved else torch.float16, held8=True, rot=rot,
+                 interleaved=interleaved, sections=sections, far=far, page=page, block=block, in_place=True, old=2.0 ** -9)
+
+
+def test_append_to_a_block_of_half_a_million_tokens():
+    """The queries are dealt as for any other block: the same bits, and the same scale and values at the sequence's end."""
+    from tensor_layout_amd import kv
+    g = torch.Generator().manual_seed(67)
+    k, q = (torch.randn((40, n, 16), generator=g).to(torch.bfloat16).cuda() for n in (1, 3))
+    inv = (10_000.0 ** (-torch.arange(0, 16, 2) / 16)).float().cuda()
+    got = []
+    for page, length in ((1 << 19, 300_000), (64, 64)):
+        pool = [torch.zeros((2, page, 1, 16), dtype=torch.uint8, device="cuda").view(kv_cases.E4M3) for _ in range(2)]
+        scale = [torch.full((2, 1, 1), 2.0 ** -20, device="cuda") for _ in range(2)]
+        at = torch.arange(1000, 1040, dtype=torch.int32, device="cuda")[None]
+        out = kv.append(kv.PagedCache(*pool, *scale), k, k, dev([[1]]), dev([0, 40]), dev([length]), q=q, inv_freq=inv, positions=at)
+        got.append((out, scale[0][1], *(x.view(torch.uint8)[1, length - 40:length].clone() for x in pool)))
+        assert not bool(pool[0].view(torch.uint8)[:, :length - 40].any())
+    for x, y in zip(*got):
+        assert torch.equal(x, y)
