@@ -16,11 +16,11 @@
 // it needs once, in LDS, in 64 bits, while its first rows are on their way.
 //
 // Measured on an MI355X (HBM copies run at 5.1 to 5.2 TB/s): 65536 tokens of
-// 16 + 16 + 16 heads of 64 into a 16-bit cache 158 us, 5.1 TB/s; three prompts
-// of up to 4093 tokens, 28 + 4 + 4 heads of 128, e4m3 in blocks of 64: 55 us,
-// 3.2 TB/s (before keys, values and queries had workgroups of their own
-// 67 us, with one row under way at a time 82 us); one token, 32 + 8 + 8 heads
-// of 128: 5.5 us; 256 single tokens of the same heads: 9.2 us.
+// 16 + 16 + 16 heads of 64 into a 16-bit cache 156 us, 5.2 TB/s; three prompts
+// of up to 4093 tokens, 28 + 4 + 4 heads of 128, e4m3 in blocks of 64: 51 us,
+// 3.4 TB/s (before keys, values and queries had workgroups of their own 16 us
+// more, with one row under way at a time 31); one token, 32 + 8 + 8 heads of
+// 128: 4.8 us; 256 single tokens of the same heads: 8.0 us.
 #include "kv.hpp"
 
 namespace tpl {
@@ -223,7 +223,7 @@ __device__ __forceinline__ float scale_of(float amax) {
 // all tokens of a group fit the workgroup's LDS.  Where they do not (blocks of
 // over 128 tokens at 128 channels) those of keys, and of by_token's queries,
 // are taken for each head and pass anew, which bounds the call: the three
-// prompts named above take 350 us in blocks of 256 tokens, 67 in blocks of 128.
+// prompts named above take 320 us in blocks of 256 tokens, 64 in blocks of 128.
 template <typename T, bool HELD8, int U, int MODE, bool TABLE>
 __global__ void __launch_bounds__(256, TABLE ? 4 : 2) k_append(AppendArgs p) {
     typedef typename T::one one;
@@ -286,10 +286,10 @@ __global__ void __launch_bounds__(256, TABLE ? 4 : 2) k_append(AppendArgs p) {
 
     // A wave's task: a head's keys, or its values.  Rows t0 + lr, + rpw, ...
     // are loaded together: past the last one, and in lanes that have no row,
-    // the last one again, so that nothing branches.  The first task's are on
+    // the last one again, so that nothing branches.  The first of them are on
     // their way while the angles are taken.
     const bool keys = (int)blockIdx.y < p.ky, queries = (int)blockIdx.y >= 2 * p.ky;
-    int h = (blockIdx.y - (keys ? 0 : p.ky)) * WAVES + wave;
+    const int h = (blockIdx.y - (keys ? 0 : p.ky)) * WAVES + wave;
     const int qy = blockIdx.y - 2 * p.ky, slice = qy / p.qt, from = queries ? (qy - slice * p.qt) * p.q_tokens : 0;
     const int to_ = queries && from + p.q_tokens < count ? from + p.q_tokens : count;   // tokens whose angles it needs
     if (from >= count) return;
@@ -422,13 +422,11 @@ __global__ void __launch_bounds__(256, TABLE ? 4 : 2) k_append(AppendArgs p) {
     };
     if (!queries) {
         if (where < 0 || where >= c.pages) return;
-        for (bool begun = true; h < c.kv_heads; h += p.ky * WAVES, begun = false) {
-            if (!begun) load(0);
-            if (keys)
-                write(std::integral_constant<int, MODE>(), std::true_type());
-            else
-                write(std::integral_constant<int, kStill>(), std::false_type());
-        }
+        if (h >= c.kv_heads) return;
+        if (keys)
+            write(std::integral_constant<int, MODE>(), std::true_type());
+        else
+            write(std::integral_constant<int, kStill>(), std::false_type());
         return;
     }
 

@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(256, few_blocks(HELD8, DC, MR)) k_few(AttendAr
     if (b < 0) return;
     int c = share * chunk;
     const int cend = chunk < total - c ? c + chunk : total;
-    if (c >= cend || b < 0) return;
+    if (c >= cend) return;
 
     while (c < cend) {
         const int off = c - seq_step, all = (int)f.all();
