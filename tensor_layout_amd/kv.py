@@ -66,6 +66,9 @@ _pack_batch = struct.Struct("3Pq3i4x").pack
 _pack_new = struct.Struct("6P9q5i4i4x").pack
 _pack_query = struct.Struct("3P6qf4i4x").pack
 
+# attend's workspaces: (address, bytes, tensor) by device, then stream.
+_workspaces = {}
+
 _lib = None
 _calls = []   # append, attend, workspace
 _append = _attend = None   # the extension's, which read the tensors too
@@ -76,13 +79,16 @@ def load():
     global _lib, _append, _attend
     if _lib is None:
         lib = tpl.load()
+        held = ctypes.PyDLL(lib._name)
         c, b, n, q = (ctypes.POINTER(x) for x in (Cache, Batch, New, Query))
         for name, arg, rest, res in (("tpl_kv_append", n, [_P], ctypes.c_int),
                                      ("tpl_kv_attend", q, [_P, _I64, _P], ctypes.c_int),
                                      ("tpl_kv_attend_workspace", q, [], _I64)):
             f = getattr(lib, name)
             f.argtypes, f.restype = [c, b, arg] + rest, res
-            f = lib[name]   # a second handle, which takes packed bytes in the structures' places
+            # A second handle, which takes packed bytes in the structures' places.  It keeps the interpreter's lock, as
+            # the extension does: the launches of one call follow one another on a stream whose workspace others use.
+            f = held[name]
             f.argtypes, f.restype = [_P, _P, _P] + rest, res
             _calls.append(f)
         try:
@@ -155,8 +161,9 @@ class PagedCache:
     Any order in memory is taken as long as a head's channels are contiguous
     and pages, tokens and heads lie on 16 bytes: [pages, kv_heads, page, dim]
     storage goes in as its transposed view.  The object keeps the tensors and
-    their sizes and strides, and workspaces for ``attend``, nothing of their
-    values."""
+    their sizes and strides, nothing of their values.  The workspaces that
+    ``attend`` needs are one for each device and stream, shared by all caches
+    (a model has one a layer) and kept for the next call."""
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
         _need(k.dim() == 4 and tuple(k.shape) == tuple(v.shape), "k and v must be [pages, page, kv_heads, dim]",
@@ -185,7 +192,7 @@ class PagedCache:
                         _TYPES[k.dtype], page, block, kv_heads, dim)
         self._at = ctypes.addressof(self._c)
         self._index = k.get_device()
-        self._work = {}    # workspaces by stream
+        self._work = _workspaces.setdefault(self._index, {})
 
 
 def _batch(cache, table, starts, lengths, tokens):
@@ -336,7 +343,7 @@ def _attend_packed(cache, batch, args, size, stream):
 def _new_workspace(cache, size, s, stream):
     """(address, size, tensor), its counters cleared once: every call leaves them zero.
 
-    Calls on one stream follow one another and share it.  A captured call has
+    Calls on one stream follow one another and share it, whatever their caches.  A captured call has
     one to itself, whose counters the graph clears: it may be replayed beside eager
     calls on the stream it was captured on."""
     with _on(cache, s, stream):

@@ -333,3 +333,23 @@ def test_append_to_a_block_of_half_a_million_tokens():
         assert not bool(pool[0].view(torch.uint8)[:, :length - 40].any())
     for x, y in zip(*got):
         assert torch.equal(x, y)
+
+
+def test_caches_share_a_streams_workspace():
+    """A model has a cache a layer; only the first call on a stream, and a larger one, takes memory."""
+    from tensor_layout_amd import kv
+    g = torch.Generator().manual_seed(68)
+    caches = [small_cache(g) for _ in range(5)]
+    q, table, starts, lengths = step_on(caches[0], g)
+    outs = [torch.empty_like(q) for _ in caches]
+    first = [kv.attend(q, c, table, starts, lengths).clone() for c in caches]
+    torch.cuda.synchronize()
+    for stream in (torch.cuda.current_stream(), torch.cuda.Stream()):
+        with torch.cuda.stream(stream):
+            kv.attend(q, caches[0], table, starts, lengths, out=outs[0])
+            held = torch.cuda.memory_allocated()
+            for c, out in zip(caches, outs):
+                kv.attend(q, c, table, starts, lengths, out=out)
+            assert torch.cuda.memory_allocated() == held
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(first, outs))
