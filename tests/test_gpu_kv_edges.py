@@ -353,3 +353,104 @@ def test_caches_share_a_streams_workspace():
             assert torch.cuda.memory_allocated() == held
         torch.cuda.synchronize()
         assert all(torch.equal(x, y) for x, y in zip(first, outs))
+
+
+# ---------------------------------------------------------------- sizes that choose other kernels
+
+
+def values64(pool, scale):
+    """A pool's values in 64 bits, on the GPU."""
+    x = pool.float().double()
+    return x if scale is None else x * scale.double().repeat_interleave(pool.shape[1] // scale.shape[2], 2).transpose(1, 2)[..., None]
+
+
+def attend64(q, k, v, ks, vs, table, starts, lengths, scale, window=0, sinks=0):
+    """The statement's out, lse, size and score on the GPU, a cache head and 1024 rows at a time, for batches too large for its loops."""
+    kx, vx = values64(k, ks), values64(v, vs)
+    page, kv_heads, group = k.shape[1], k.shape[2], q.shape[1] // k.shape[2]
+    out = torch.zeros(q.shape, dtype=torch.float64, device="cuda")
+    lse = torch.full(q.shape[:2], -math.inf, dtype=torch.float64, device="cuda")
+    size, score = torch.zeros_like(out), torch.zeros_like(lse)
+    for b, length in enumerate(lengths):
+        n = starts[b + 1] - starts[b]
+        if n == 0:
+            continue
+        j = torch.tensor([j for j in range(length) if table[b][j // page] >= 0], device="cuda")
+        where = torch.tensor(table[b], device="cuda")[j // page]
+        for i in range(0, n, 1024):
+            rows = slice(starts[b] + i, starts[b] + min(n, i + 1024))
+            pos = torch.arange(length - n + i, length - n + min(n, i + 1024), device="cuda")[:, None]
+            see = j <= pos
+            if window:
+                see &= (pos - j < window) | (j < sinks)
+            for h in range(kv_heads):
+                kk, vv = kx[where, j % page, h], vx[where, j % page, h]
+                for a in range(h * group, (h + 1) * group):
+                    x = q[rows, a].double()
+                    score[rows, a] = ((x.abs() @ kk.abs().t()) * scale).masked_fill_(~see, 0.0).amax(-1)
+                    x = (x @ kk.t() * scale).masked_fill_(~see, -math.inf)
+                    lse[rows, a] = x.logsumexp(-1)
+                    x = (x - lse[rows, a][:, None].nan_to_num(neginf=0.0)).exp()
+                    out[rows, a], size[rows, a] = x @ vv, x @ vv.abs()
+    return out, lse, size, score
+
+
+def check_large(seed, news, lengths, *, heads, kv_heads, dim, dtype, held8, page=64, block=16, window=0, sinks=0, by_head=False, width=None):
+    from tensor_layout_amd import kv
+    g = torch.Generator().manual_seed(seed)
+    starts, lengths, table, pages = kv_cases.batch(g, news, lengths, page, width=width)
+    k, ks, v, vs = kv_cases.pools(g, pages, page, kv_heads, dim, dtype, held8, block, by_head)
+    for x in (k, v):
+        kv_cases.poison(x, table, lengths, page)
+    q = torch.randn((starts[-1], heads, dim), generator=g).mul_(2).to(dtype).cuda()
+    gpu = [on_gpu(k), on_gpu(v), dev(ks), dev(vs)]
+    got, lse = torch.full(q.shape, 7.0, dtype=dtype, device="cuda"), torch.full(q.shape[:2], 7.0, device="cuda")
+    kv.attend(q, kv.PagedCache(*gpu), dev(table), dev(starts), dev(lengths), scale=dim ** -0.5, window=window, sinks=sinks, out=got, lse=lse)
+    want = attend64(q, *gpu, table, starts, lengths, dim ** -0.5, window, sinks)
+    compare_attend(got.cpu(), lse.cpu(), *(x.cpu() for x in want), v, vs, dtype, held8, dim, max(lengths))
+
+
+@pytest.mark.parametrize("dtype,held8", TYPES)
+@pytest.mark.parametrize("heads,kv_heads,dim,new,length", [(64, 16, 64, 2100, 2100), (48, 16, 96, 2800, 2900), (32, 32, 128, 4200, 4500)])
+def test_row_tiles_of_256(heads, kv_heads, dim, new, length, dtype, held8):
+    """Prompts long enough for them: over 2 workgroups of 256 rows for each of 256 compute units."""
+    check_large(58, [new], [length], heads=heads, kv_heads=kv_heads, dim=dim, dtype=dtype, held8=held8)
+
+
+def test_row_tiles_of_256_of_several_prompts():
+    check_large(59, [1500, 1, 900, 0, 1300], [1500, 777, 1000, 0, 1333], heads=64, kv_heads=16, dim=64, dtype=torch.bfloat16, held8=True)
+
+
+@pytest.mark.parametrize("dtype,held8,dim", [(torch.bfloat16, True, 128), (torch.float16, True, 64), (torch.bfloat16, False, 64),
+                                             (torch.float16, False, 64), (torch.bfloat16, True, 112)])
+@pytest.mark.parametrize("new", [1, 3, 8])
+def test_two_heads_of_the_cache_a_workgroup(dtype, held8, dim, new):
+    """Many sequences and a wide table, as the host's choice goes by; lengths that leave tiles of one step and of many shares."""
+    lengths = [max(new, x) for x in ([4096, 1, 33, 4000, 700, 64, 129, 2500] + [3 + 61 * i % 900 for i in range(40)])]
+    check_large(60, [new] * 48, lengths, heads=32, kv_heads=8, dim=dim, dtype=dtype, held8=held8, page=32, width=128)
+
+
+@pytest.mark.parametrize("batch", [65, 257, 300, 600])
+@pytest.mark.parametrize("news", [(1,), (1, 3, 0, 2)])
+def test_many_sequences(batch, news):
+    """More than a workgroup's threads: each then counts several."""
+    n = [news[i % len(news)] for i in range(batch)]
+    lengths = [x + 41 * i % 230 for i, x in enumerate(n)]
+    check_large(61, n, lengths, heads=4, kv_heads=2, dim=64, dtype=torch.bfloat16, held8=True, page=16)
+
+
+@pytest.mark.parametrize("dtype,held8", TYPES)
+@pytest.mark.parametrize("dim", [64, 128, 192])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (1900, 100)])
+def test_prompts_split_over_their_tokens(dtype, held8, dim, window, sinks):
+    """A few rows on many tokens: five and more parts a row tile, and none for a part that a row sees nothing of."""
+    check_large(62, [70], [2900], heads=4, kv_heads=2, dim=dim, dtype=dtype, held8=held8, page=32, window=window, sinks=sinks)
+    check_large(63, [33, 1, 90], [2600, 500, 2700], heads=8, kv_heads=2, dim=dim, dtype=dtype, held8=held8, page=32, window=window,
+                sinks=sinks)
+
+
+@pytest.mark.parametrize("kv_heads", [5, 7, 13, 600])
+@pytest.mark.parametrize("news,lengths", [([1, 2], [900, 40]), ([60, 1], [300, 600])])
+def test_odd_and_many_heads_of_the_cache(kv_heads, news, lengths):
+    """Shares that do not divide by the heads, and more heads than a workgroup each can have at once."""
+    check_large(69, news, lengths, heads=2 * kv_heads, kv_heads=kv_heads, dim=16, dtype=torch.bfloat16, held8=True, page=32)
