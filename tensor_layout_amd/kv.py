@@ -110,6 +110,7 @@ _stream = (getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 _TYPES = {torch.bfloat16: BF16, torch.float16: FP16, torch.float8_e4m3fn: E4M3}
 _INT32 = torch.int32
+_FLOAT_MAX = torch.finfo(torch.float32).max
 
 
 def _need(ok: bool, message: str, status: int = tpl.TPL_E_ARG) -> None:
@@ -406,9 +407,13 @@ def _attend_checked(q, cache, table, starts, lengths, scale, window, sinks, out,
             _need(False, f"lse must be on {cache.device}")
         lp = lse.data_ptr()
         lt, lh = lse.stride()
+    scale = dim ** -0.5 if scale is None else scale
+    # What the structure can hold; the entry point judges it.
+    _need(-_FLOAT_MAX <= scale <= _FLOAT_MAX, "scale must be a finite number over zero")
+    _need(abs(window) < 1 << 31 and abs(sinks) < 1 << 31, "window and sinks must be 0 .. 2^30")
     qt, qh, _ = q.stride()
     ot, oh, _ = out.stride()
-    args = _pack_query(q.data_ptr(), out.data_ptr(), lp, qt, qh, ot, oh, lt, lh, dim ** -0.5 if scale is None else scale,
+    args = _pack_query(q.data_ptr(), out.data_ptr(), lp, qt, qh, ot, oh, lt, lh, scale,
                        _TYPES[dtype], heads, window, sinks)
     size = _workspace(cache, batch, args)
     _need(index >= 0, "tensors must live on the GPU")

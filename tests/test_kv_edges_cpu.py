@@ -27,3 +27,16 @@ def test_attend_says_what_the_entry_point_says():
         with pytest.raises(TplError) as e:
             kv.attend(kw.pop("q", q), cache, t, s, n, **kw)
         assert e.value.status == status, e.value
+
+
+def test_numbers_that_no_structure_holds_are_refused():
+    """Out of the entry points' ranges, they are a refused call like any other."""
+    cache = kv.PagedCache(*pools())
+    i32 = dict(dtype=torch.int32)
+    t, s, n = torch.zeros((1, 3), **i32), torch.zeros(2, **i32), torch.zeros(1, **i32)
+    q = torch.zeros((1, 4, 64), dtype=torch.bfloat16)
+    for kw in (dict(window=1 << 40), dict(window=-(1 << 40)), dict(window=16, sinks=1 << 31), dict(scale=1e300), dict(scale=-1e300),
+               dict(scale=float("inf")), dict(scale=1e-300)):
+        with pytest.raises(TplError) as e:
+            kv.attend(q, cache, t, s, n, **kw)
+        assert e.value.status == tpl.TPL_E_ARG
