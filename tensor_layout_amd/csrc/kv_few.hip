@@ -22,9 +22,10 @@
 // sequences of up to 8192 tokens 174 -> 155 us; with pages laid out by head
 // it takes 140 us).
 //
-// Measured on an MI355X: that batch at 4.6 TB/s, two sequences of 131009
-// tokens, 64 heads on 8, pages by head, at 4.7 TB/s (114 us); a batch of 64
-// even ones by head at 5.5 TB/s (a large copy: 5.2).
+// Measured on an MI355X: that batch at 4.6 TB/s (154 us), in bf16 instead of
+// e4m3 at 5.2 TB/s (275 us), in e4m3 with heads of 256 at 4.7 TB/s (301 us);
+// two sequences of 131009 tokens, 64 heads on 8, pages by head, at 4.7 TB/s
+// (115 us); a batch of 64 even ones by head at 5.5 TB/s (a large copy: 5.2).
 //
 // Layout.  S^T = K Q^T with 16 tokens as the rows of a 16x16x32 product:
 // lane (r = lane % 16, g = lane / 16) holds channels of token r, and its part

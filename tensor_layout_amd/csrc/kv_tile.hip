@@ -21,15 +21,19 @@
 //
 // Measured on an MI355X (a matrix product of 8192^3 in bf16 runs at 1240
 // TFLOP/s): a prompt of 8192 tokens, 32 heads of 128 on 8 in e4m3, 566 us,
-// 971 TFLOP/s.  Steps there: two waves a SIMD instead of one 1400 -> 752 us;
-// no short-circuit conditions, which had cost registers, 737; products in
-// groups whose operands are read one group ahead, the weights' arithmetic
-// beside them and the scores of the next step before the values of this one
-// 604; keys' halves apart in LDS 598; 8 waves that share a step 572; their
-// products first 3 % less again.  What is
-// left is vector arithmetic: about 260 instructions a wave and step beside
-// 32 matrix products, 51 % of the vector units' time and 40 % of the matrix
-// units', which hardly overlap further with two waves a SIMD.
+// 970 TFLOP/s (555 to 592 us from card to card).  Steps there, on one card:
+// two waves a SIMD instead of one 1400 -> 752 us; no short-circuit conditions,
+// which had cost registers, 737; products in groups whose operands are read
+// one group ahead, the weights' arithmetic beside them and the scores of the
+// next step before the values of this one 604; keys' halves apart in LDS 598;
+// 8 waves that share a step 572; their products first 3 % less again.  What is
+// left is vector arithmetic: about 265 instructions a wave and step beside 32
+// matrix products, 49 % of the vector units' time and 43 % of the matrix
+// units', which hardly overlap further with two waves a SIMD.  With 64
+// channels a head there are 16 products beside about 315 vector instructions,
+// and the values of a step are transposed by half of the waves: two prompts of
+// up to 8000 tokens under a window of 1024, 16 heads of 64 in fp16, 152 us,
+// 50 % of the vector units' time and 19 % of the matrix units'.
 #include "kv_attend.hpp"
 
 namespace tpl {

@@ -222,6 +222,7 @@ def append(cache: PagedCache, k, v, table, starts, lengths, *, q=None, q_out=Non
     sections      with more axes than one, how many pairs turn by each, in order.
     interleaved   pairs are channels (2c, 2c + 1), otherwise (c, c + rot / 2).
     q_out         takes the rotated queries (default: a new tensor); may be ``q``.
+    stream        the handle of the stream to run on (default: torch's current one).
 
     ``lengths`` counts the new tokens.  Returns ``q_out``."""
     if _lib is None:
@@ -367,6 +368,7 @@ def attend(q, cache: PagedCache, table, starts, lengths, *, scale: Optional[floa
     scale   default dim ** -0.5.
     out     takes the result (default: a new tensor).
     lse     fp32 [tokens, heads]: takes the logarithm of each row's sum of exponentials.
+    stream  the handle of the stream to run on (default: torch's current one).
 
     A row that sees nothing gets zeros and an lse of minus infinity.  Returns ``out``."""
     if _lib is None:
