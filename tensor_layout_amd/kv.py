@@ -6,9 +6,11 @@ their positions and writes keys and values into their pages; ``attend`` lets
 the queries attend to what the cache holds.  A batch is packed: sequence ``b``
 owns rows ``starts[b]:starts[b + 1]`` of the token tensors, ``lengths[b]``
 tokens with those, and the pages that its row of ``table`` names in order (a
-negative entry is a page that is not there).  Both run on torch's current
-stream without waiting, read ``table``, ``starts`` and ``lengths`` on the
-device only, and may be captured into a graph.
+negative entry is a page that is not there).  Rows of no sequence, and of one
+that is skipped because its numbers are out of order, are left as they are.
+Both run on torch's current stream, or a named one, without waiting, read
+``table``, ``starts`` and ``lengths`` on the device only, and may be captured
+into a graph.
 
 Arguments are checked here for their types and shapes, and by the C entry
 points of include/tpl_kv.h, which every call ends in; a refused call raises
