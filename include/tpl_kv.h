@@ -95,6 +95,22 @@ typedef struct {
     int32_t sinks;             /* with a window: first tokens that stay visible */
 } tpl_kv_query;
 
+/* Rows that take what a cache holds: [tokens, kv_heads, dim]. */
+typedef struct {
+    void *k, *v;               /* either may be NULL: not read */
+    int64_t k_token, k_head, v_token, v_head;
+    int32_t type;              /* TPL_KV_BF16 or TPL_KV_FP16; that of a 16-bit cache */
+} tpl_kv_rows;
+
+/* Groups of sequences that share their first tokens: device arrays.  Group g is
+ * sequences groups[g] .. groups[g+1] - 1, and its first shared[g] tokens are the
+ * ones that the row of the table of its first sequence names. */
+typedef struct {
+    const int32_t *groups;     /* [count + 1] */
+    const int32_t *shared;     /* [count] */
+    int32_t count;
+} tpl_kv_groups;
+
 /*
  * Enqueue: rotate the new keys and queries to their positions, write keys and
  * values into their pages.
@@ -132,6 +148,34 @@ int tpl_kv_attend(const tpl_kv_cache *cache, const tpl_kv_batch *batch,
  * would refuse the call. */
 int64_t tpl_kv_attend_workspace(const tpl_kv_cache *cache, const tpl_kv_batch *batch,
                                 const tpl_kv_query *args);
+
+/*
+ * Enqueue: the same attention (window and sinks: 0) for a batch whose sequences
+ * share their first tokens group by group: those are read, and multiplied with
+ * the queries, once for all rows of a group.  A sequence in no group, or whose
+ * group is not in order (groups and its first and last sequence's starts, a
+ * shared number of 1 .. what a row of the table holds), or that has a new token
+ * among its first shared[g] ones, attends to what its own row of the table
+ * names: nothing changes where that row names the shared pages too.
+ *
+ * `workspace` as tpl_kv_attend takes it (the two may use one in turn), of
+ * tpl_kv_attend_shared_workspace() bytes.
+ */
+int tpl_kv_attend_shared(const tpl_kv_cache *cache, const tpl_kv_batch *batch,
+                         const tpl_kv_groups *groups, const tpl_kv_query *args,
+                         void *workspace, int64_t workspace_bytes, hipStream_t stream);
+
+int64_t tpl_kv_attend_shared_workspace(const tpl_kv_cache *cache, const tpl_kv_batch *batch,
+                                       const tpl_kv_groups *groups, const tpl_kv_query *args);
+
+/*
+ * Enqueue: each sequence's last tokens (as many as it has rows) out of the
+ * cache, rounded once to the rows' type; from a 16-bit cache, bit for bit.  A
+ * token whose page is not there gives zeros.  Rows and heads of the result must
+ * not lie over one another.
+ */
+int tpl_kv_read(const tpl_kv_cache *cache, const tpl_kv_batch *batch,
+                const tpl_kv_rows *rows, hipStream_t stream);
 
 #ifdef __cplusplus
 }

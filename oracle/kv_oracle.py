@@ -27,9 +27,22 @@ def ordered(starts, lengths, tokens, b):
     return (r, e - r, n) if 0 <= r < e <= tokens and e - r <= n <= 1 << 30 else (0, 0, 0)
 
 
-def attend(q, k_pool, v_pool, k_scale, v_scale, table, starts, lengths, scale, window=0, sinks=0, fill=None):
+def sharing(groups, shared, starts, lengths, tokens, cap, b):
+    """(sequence that holds its first tokens, how many): a sequence's group, or itself and none."""
+    for g in range(len(shared)):
+        a, e = groups[g], groups[g + 1]
+        if 0 <= a <= b < e <= len(lengths) and 1 <= shared[g] <= cap and 0 <= starts[a] < starts[e] <= tokens:
+            r, n, length = ordered(starts, lengths, tokens, b)
+            if n and starts[a] <= r and r + n <= starts[e] and shared[g] <= length - n:
+                return a, shared[g]
+    return b, 0
+
+
+def attend(q, k_pool, v_pool, k_scale, v_scale, table, starts, lengths, scale, window=0, sinks=0, fill=None, groups=None,
+           shared=()):
     """(out, lse, size, score): size is each output's sum of |weight * value|, score each row's largest sum of
-    |scale * q * k| over what it sees.  Rows of no sequence keep `fill`."""
+    |scale * q * k| over what it sees.  Rows of no sequence keep `fill`.  With `groups`, a sequence's first tokens
+    are its group's first sequence's."""
     tokens, heads, dim = q.shape
     k_all, v_all = values(k_pool, k_scale), values(v_pool, v_scale)
     page, kv_heads = k_pool.shape[1], k_pool.shape[2]
@@ -41,9 +54,11 @@ def attend(q, k_pool, v_pool, k_scale, v_scale, table, starts, lengths, scale, w
     qd = q.double()
     for b in range(len(lengths)):
         r0, n, length = ordered(starts, lengths, tokens, b)
-        there = [j for j in range(min(length, len(table[b]) * page)) if 0 <= table[b][j // page] < k_pool.shape[0]]
+        leader, common = sharing(groups, shared, starts, lengths, tokens, len(table[b]) * page, b) if groups else (b, 0)
+        row = [table[leader if j < common else b][j // page] for j in range(min(length, len(table[b]) * page))]
+        there = [j for j, x in enumerate(row) if 0 <= x < k_pool.shape[0]]
         js = torch.tensor(there, dtype=torch.long)
-        pg = torch.tensor([table[b][j // page] for j in there], dtype=torch.long)
+        pg = torch.tensor([row[j] for j in there], dtype=torch.long)
         for i in range(n):
             pos = length - n + i
             see = js <= pos
@@ -66,6 +81,19 @@ def attend(q, k_pool, v_pool, k_scale, v_scale, table, starts, lengths, scale, w
                 size[r0 + i, hs] = pn @ v.abs()
                 score[r0 + i, hs] = (qd[r0 + i, hs].abs() @ k.abs().t() * scale).amax(-1)
     return out, lse, size, score
+
+
+def read(pool, scale, table, starts, lengths, tokens, fill):
+    """[tokens, kv_heads, dim] in 64 bits: every sequence's last tokens; `tokens`: the result's rows."""
+    x, page = values(pool, scale), pool.shape[1]
+    out = torch.full((tokens, pool.shape[2], pool.shape[3]), fill, dtype=torch.float64)
+    for b in range(len(lengths)):
+        r0, n, length = ordered(starts, lengths, tokens, b)
+        for i in range(n):
+            j = length - n + i
+            pg = table[b][j // page] if j // page < len(table[b]) else -1
+            out[r0 + i] = x[pg, j % page] if 0 <= pg < pool.shape[0] else 0.0
+    return out
 
 
 def rotated(x, place, inv_freq, sections, interleaved):

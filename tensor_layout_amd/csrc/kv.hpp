@@ -130,5 +130,38 @@ __device__ __forceinline__ Seq read_seq(const tpl_kv_batch& g, int b) {
     return ordered(g.starts[b], g.starts[b + 1], g.lengths[b], g.tokens);
 }
 
+// The sequence that row tile x belongs to, where a tile has up to `per` rows:
+// sequence b's tiles are numbered from starts[b] / per + b on, and of those in
+// order whose numbers begin at or before x it is the last.  64 are looked at
+// together, with all that is needed of them, so that it is known after one
+// load's latency.  b is -1 where there is none.
+struct TileSeq {
+    int b;
+    Seq s;
+};
+
+__device__ __forceinline__ TileSeq seq_of_tile(const tpl_kv_batch& g, int per, int x) {
+    const int lane = threadIdx.x & 63;
+    TileSeq t = {-1, {0, 0, 0}};
+    for (int b0 = 0; b0 < g.batch; b0 += 64) {
+        const int bb = b0 + lane < g.batch ? b0 + lane : g.batch - 1;
+        const Seq s = read_seq(g, bb);
+        const uint64_t m = __ballot(b0 + lane < g.batch && s.n > 0 && s.row0 / per + bb <= x);
+        if (m) {
+            const int from = 63 - __builtin_clzll(m);
+            t.b = b0 + from;
+            t.s.row0 = __builtin_amdgcn_readlane(s.row0, from);
+            t.s.n = __builtin_amdgcn_readlane(s.n, from);
+            t.s.length = __builtin_amdgcn_readlane(s.length, from);
+        }
+    }
+    return t;
+}
+
+// What the operators check alike (kv_attend.hip).
+const char* check_cache(const tpl_kv_cache* c);
+const char* check_batch(const tpl_kv_cache& c, const tpl_kv_batch* g);
+bool aligned16(const void* p, int64_t s0, int64_t s1, int bytes);
+
 }  // namespace kv
 }  // namespace tpl

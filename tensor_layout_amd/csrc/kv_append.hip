@@ -497,10 +497,6 @@ static hipError_t launch_append(const AppendArgs& p, int u, dim3 grid, size_t ld
     return p.c.type == TPL_KV_E4M3 ? launch_mode<T, true>(p, u, grid, lds, st) : launch_mode<T, false>(p, u, grid, lds, st);
 }
 
-const char* check_cache(const tpl_kv_cache* c);                                   // kv_attend.hip
-const char* check_batch(const tpl_kv_cache& c, const tpl_kv_batch* g);
-bool aligned16(const void* p, int64_t s0, int64_t s1, int bytes);
-
 static int append_impl(const tpl_kv_cache* c, const tpl_kv_batch* g, const tpl_kv_new* a, hipStream_t st) {
     if (!c || !g || !a) return fail_status(TPL_E_ARG, "cache, batch and arguments must not be NULL");
     if (const char* why = check_cache(c)) return fail_status(TPL_E_ARG, why);

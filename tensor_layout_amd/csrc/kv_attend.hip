@@ -67,6 +67,69 @@ struct Choice {
     int64_t bytes() const { return few_bytes + tile_bytes > 0 ? kCounters * 4 + few_bytes + tile_bytes : 0; }
 };
 
+// The split kernel's sizes for `items` sequences (or groups) of `rows` rows in
+// all, of which it takes those of up to `limit`.
+static const char* plan_few(AttendArgs& p, Choice& q, int64_t rows, int64_t items, int limit, bool pairs) {
+    // 16 lanes hold dc channels each: 12 only where those are whole lanes (144 and 192 channels).
+    q.dc = p.c.dim <= 64 ? 4 : p.c.dim <= 128 ? 8 : p.c.dim <= 192 && p.c.dim % 12 == 0 ? 12 : 16;
+    // Rows of a tile: those of an average sequence, or of a decoding one
+    // where the average is a prompt's.
+    int64_t mean = (rows + items - 1) / items;
+    if (mean > limit) mean = p.group;
+    q.mr = mean <= 16 ? 1 : mean <= 32 || q.dc > 8 ? 2 : 4;
+    // No more shares than steps there can be.
+    const int64_t tiles = (rows + q.mr * 16 - 1) / (q.mr * 16) + items;
+    const int64_t most = tiles * (((int64_t)p.cap + 31) / 32 + 1);
+    // Two heads a workgroup where they lie next to each other within 256
+    // bytes and a share is long: it then reads whole 256 bytes of a token.
+    // 64 sequences of up to 8192 tokens (64 steps a share at most): 155
+    // against 174 us; 24 of them (24 steps): 65 against 72.  At 16 steps,
+    // where the parts that are left weigh more, it goes both ways: 8 of up
+    // to 16384 58 against 62, 2 of up to 65536 63 against 60, 32 of up to
+    // 4096 46 against 49 with a row each and 48 against 46 with four.
+    // Under a window of 1024, 64 of them (8 steps): 28 against 22 us.
+    int64_t seen = p.cap;
+    if (p.a.window && (int64_t)p.a.window + p.a.sinks < seen) seen = (int64_t)p.a.window + p.a.sinks;
+    const int64_t blocks = kCUs * few_blocks(p.c.type == TPL_KV_E4M3, q.dc, q.mr);
+    const int w = p.c.type == TPL_KV_E4M3 ? 1 : 2;
+    p.heads_log = pairs && p.c.kv_heads % 2 == 0 && p.c.k_head * w < 256 && p.c.k_head < p.c.k_token && p.c.v_head < p.c.v_token &&
+                  items * (seen / 128) * p.c.kv_heads >= 24 * blocks ? 1 : 0;
+    int64_t shares = blocks / (p.c.kv_heads >> p.heads_log);
+    if (most > INT_MAX) return "tokens and table are too large together";
+    if (shares > most) shares = most;
+    p.shares = shares < 1 ? 1 : (int)shares;
+    q.few_bytes = (int64_t)p.shares * p.c.kv_heads * 2 * few_part_floats(q.dc, q.mr) * 4;
+    return nullptr;
+}
+
+// The tile kernel's.
+static const char* plan_tile(AttendArgs& p, Choice& q, int64_t rows, int64_t items) {
+    q.dk = p.c.dim <= 64 ? 64 : p.c.dim <= 96 ? 96 : p.c.dim <= 128 ? 128 : p.c.dim <= 192 ? 192 : 256;
+    // Row tiles of 256 (8 waves that share a step's keys and values) where
+    // they still give every CU two, else of 128.  One prompt of 8192
+    // tokens, 32 heads of 128: 572 against 598 us; a chunk of 1024 tokens
+    // (128 tiles of 256): 169 against 139 us.  Under a window larger tiles
+    // see more that most of their rows do not (window 1024: 178 against
+    // 158 us), and longer heads do not fit 8 waves' registers.
+    const bool large = q.dk <= 128 && p.a.window == 0 && rows / 256 * p.c.kv_heads >= 2 * kCUs;
+    p.tile_rows = large ? 256 : 128;
+    p.tile_tokens = p.tile_rows / p.group;
+    const int64_t tiles = (int64_t)p.g.tokens / p.tile_tokens + items;
+    const int64_t units = tiles * p.c.kv_heads;
+    int64_t most = p.cap;
+    if (p.a.window && (int64_t)p.a.window + p.a.sinks + p.tile_tokens < most) most = (int64_t)p.a.window + p.a.sinks + p.tile_tokens;
+    most = (most + 511) / 512;
+    int64_t splits = 2 * kCUs / units;
+    if (splits > most) splits = most;
+    if (splits > 32) splits = 32;
+    if (splits < 1) splits = 1;
+    p.tiles = (int)tiles;
+    p.splits = (int)splits;
+    if (units * splits > INT_MAX) return "too many row tiles";
+    if (splits > 1) q.tile_bytes = units * splits * tile_part_floats(q.dk, p.tile_rows) * 4;
+    return nullptr;
+}
+
 static const char* choose(const tpl_kv_cache* c, const tpl_kv_batch* g, const tpl_kv_query* a, AttendArgs& p, Choice& q,
                           int* status) {
     *status = TPL_E_ARG;
@@ -92,6 +155,10 @@ static const char* choose(const tpl_kv_cache* c, const tpl_kv_batch* g, const tp
     if (a->window == 0) p.a.sinks = 0;
     p.counters = nullptr;
     p.parts = p.tile_parts = nullptr;
+    p.s = tpl_kv_groups{};
+    p.prefix = p.before_splits = 0;
+    p.before = nullptr;
+    p.before_ml = nullptr;
     p.group = a->heads / c->kv_heads;
     p.cap = g->width * c->page;
     p.factor = a->scale * kLog2e;
@@ -119,63 +186,19 @@ static const char* choose(const tpl_kv_cache* c, const tpl_kv_batch* g, const tp
         q.few = q.tile = true;
         p.few = limit;
     }
-    if (q.few) {
-        // 16 lanes hold dc channels each: 12 only where those are whole lanes (144 and 192 channels).
-        q.dc = c->dim <= 64 ? 4 : c->dim <= 128 ? 8 : c->dim <= 192 && c->dim % 12 == 0 ? 12 : 16;
-        // Rows of a tile: those of an average sequence, or of a decoding one
-        // where the average is a prompt's.
-        int64_t mean = (rows + g->batch - 1) / g->batch;
-        if (mean > limit) mean = p.group;
-        q.mr = mean <= 16 ? 1 : mean <= 32 || q.dc > 8 ? 2 : 4;
-        // No more shares than steps there can be.
-        const int64_t tiles = (rows + q.mr * 16 - 1) / (q.mr * 16) + g->batch;
-        const int64_t most = tiles * (((int64_t)p.cap + 31) / 32 + 1);
-        // Two heads a workgroup where they lie next to each other within 256
-        // bytes and a share is long: it then reads whole 256 bytes of a token.
-        // 64 sequences of up to 8192 tokens (64 steps a share at most): 155
-        // against 174 us; 24 of them (24 steps): 65 against 72.  At 16 steps,
-        // where the parts that are left weigh more, it goes both ways: 8 of up
-        // to 16384 58 against 62, 2 of up to 65536 63 against 60, 32 of up to
-        // 4096 46 against 49 with a row each and 48 against 46 with four.
-        // Under a window of 1024, 64 of them (8 steps): 28 against 22 us.
-        int64_t seen = p.cap;
-        if (a->window && (int64_t)a->window + a->sinks < seen) seen = (int64_t)a->window + a->sinks;
-        const int64_t blocks = kCUs * few_blocks(c->type == TPL_KV_E4M3, q.dc, q.mr);
-        const int w = c->type == TPL_KV_E4M3 ? 1 : 2;
-        p.heads_log = c->kv_heads % 2 == 0 && c->k_head * w < 256 && c->k_head < c->k_token && c->v_head < c->v_token &&
-                      g->batch * (seen / 128) * c->kv_heads >= 24 * blocks ? 1 : 0;
-        int64_t shares = blocks / (c->kv_heads >> p.heads_log);
-        if (most > INT_MAX) return "tokens and table are too large together";
-        if (shares > most) shares = most;
-        p.shares = shares < 1 ? 1 : (int)shares;
-        q.few_bytes = (int64_t)p.shares * c->kv_heads * 2 * few_part_floats(q.dc, q.mr) * 4;
-    }
-    if (q.tile) {
-        q.dk = c->dim <= 64 ? 64 : c->dim <= 96 ? 96 : c->dim <= 128 ? 128 : c->dim <= 192 ? 192 : 256;
-        // Row tiles of 256 (8 waves that share a step's keys and values) where
-        // they still give every CU two, else of 128.  One prompt of 8192
-        // tokens, 32 heads of 128: 572 against 598 us; a chunk of 1024 tokens
-        // (128 tiles of 256): 169 against 139 us.  Under a window larger tiles
-        // see more that most of their rows do not (window 1024: 178 against
-        // 158 us), and longer heads do not fit 8 waves' registers.
-        const bool large = q.dk <= 128 && a->window == 0 && rows / 256 * c->kv_heads >= 2 * kCUs;
-        p.tile_rows = large ? 256 : 128;
-        p.tile_tokens = p.tile_rows / p.group;
-        const int64_t tiles = (int64_t)g->tokens / p.tile_tokens + g->batch;
-        const int64_t units = tiles * c->kv_heads;
-        int64_t most = p.cap;
-        if (a->window && (int64_t)a->window + a->sinks + p.tile_tokens < most) most = (int64_t)a->window + a->sinks + p.tile_tokens;
-        most = (most + 511) / 512;
-        int64_t splits = 2 * kCUs / units;
-        if (splits > most) splits = most;
-        if (splits > 32) splits = 32;
-        if (splits < 1) splits = 1;
-        p.tiles = (int)tiles;
-        p.splits = (int)splits;
-        if (units * splits > INT_MAX) return "too many row tiles";
-        if (splits > 1) q.tile_bytes = units * splits * tile_part_floats(q.dk, p.tile_rows) * 4;
-    }
+    if (q.few)
+        if (const char* why = plan_few(p, q, rows, g->batch, limit, true)) return why;
+    if (q.tile) return plan_tile(p, q, rows, g->batch);
     return nullptr;
+}
+
+static int check_query(const tpl_kv_query* a, void* ws, int64_t ws_bytes, int64_t need) {
+    if (!a->q || !a->out) return fail_status(TPL_E_ARG, "q and out must not be NULL");
+    if (!aligned16(a->q, a->q_token, a->q_head, 2) || !aligned16(a->out, a->o_token, a->o_head, 2))
+        return fail_status(TPL_E_LAYOUT, "q and out must start, and their rows and heads lie, on 16 bytes");
+    if (need > 0 && (!ws || ((uintptr_t)ws & 15))) return fail_status(TPL_E_ARG, "workspace must lie on 16 bytes");
+    if (ws_bytes < need) return fail_status(TPL_E_ARG, "workspace is too small");
+    return TPL_OK;
 }
 
 static int attend_impl(const tpl_kv_cache* c, const tpl_kv_batch* g, const tpl_kv_query* a, void* ws, int64_t ws_bytes,
@@ -185,11 +208,7 @@ static int attend_impl(const tpl_kv_cache* c, const tpl_kv_batch* g, const tpl_k
     int status;
     if (const char* why = choose(c, g, a, p, q, &status)) return fail_status(status, why);
     if (!q.few && !q.tile) return TPL_OK;
-    if (!a->q || !a->out) return fail_status(TPL_E_ARG, "q and out must not be NULL");
-    if (!aligned16(a->q, a->q_token, a->q_head, 2) || !aligned16(a->out, a->o_token, a->o_head, 2))
-        return fail_status(TPL_E_LAYOUT, "q and out must start, and their rows and heads lie, on 16 bytes");
-    if (q.bytes() > 0 && (!ws || ((uintptr_t)ws & 15))) return fail_status(TPL_E_ARG, "workspace must lie on 16 bytes");
-    if (ws_bytes < q.bytes()) return fail_status(TPL_E_ARG, "workspace is too small");
+    if (const int bad = check_query(a, ws, ws_bytes, q.bytes())) return bad;
     p.counters = (int*)ws;
     p.parts = (float*)((char*)ws + kCounters * 4);
     p.tile_parts = (float*)((char*)p.parts + q.few_bytes);
@@ -197,6 +216,74 @@ static int attend_impl(const tpl_kv_cache* c, const tpl_kv_batch* g, const tpl_k
     if (q.tile) e = launch_tile(p, q.dk, false, st);
     if (e == hipSuccess && q.few) e = launch_few(p, q.dc, q.mr, st);
     if (e == hipSuccess && q.tile && p.splits > 1) e = launch_tile(p, q.dk, true, st);
+    if (e != hipSuccess) return fail_status(TPL_E_HIP, std::string("HIP launch failed: ") + hipGetErrorString(e));
+    return TPL_OK;
+}
+
+// Two launches of the same kernels: groups' rows over the tokens that they
+// share, whose results stay in 32 bits in the workspace, then sequences' rows
+// over their own tokens, which begin from those results.
+struct SharedChoice {
+    Choice q1, q2;
+    int64_t few_bytes, rows;   // of both launches' parts; rows * heads of the results between them
+    int64_t bytes;
+};
+
+static const char* choose_shared(const tpl_kv_cache* c, const tpl_kv_batch* g, const tpl_kv_groups* s, const tpl_kv_query* a,
+                                 AttendArgs& p1, AttendArgs& p2, SharedChoice& x, int* status) {
+    if (!s) {
+        *status = TPL_E_ARG;
+        return "groups must not be NULL";
+    }
+    if (const char* why = choose(c, g, a, p2, x.q2, status)) return why;
+    if (a->window || a->sinks) return "sequences that share tokens have no window and no sinks";
+    if (s->count < 0 || s->count > (1 << 20)) return "groups must be 0 .. 2^20";
+    x.bytes = x.q2.bytes();
+    x.q1 = Choice{};
+    if (s->count == 0 || (!x.q2.few && !x.q2.tile)) return nullptr;
+    if (!s->groups || !s->shared) return "groups and shared must not be NULL";
+    p2.s = *s;
+    p1 = p2;
+    p1.prefix = 1;
+    const int64_t rows = (int64_t)g->tokens * p1.group, mean = (rows + s->count - 1) / s->count;
+    if (p1.group > 128 || mean <= 64) {
+        x.q1.few = true;
+        p1.few = INT_MAX;
+        if (const char* why = plan_few(p1, x.q1, rows, s->count, 64, true)) return why;
+        p1.before_splits = 1;
+    } else {
+        x.q1.tile = true;
+        p1.few = 0;
+        if (const char* why = plan_tile(p1, x.q1, rows, s->count)) return why;
+        p1.before_splits = p1.splits;
+    }
+    if (x.q2.few)   // how long sequences' own tokens are is not known: a head a workgroup
+        if (const char* why = plan_few(p2, x.q2, rows, g->batch, 64, false)) return why;
+    p2.before_splits = p1.before_splits;
+    x.few_bytes = x.q1.few_bytes > x.q2.few_bytes ? x.q1.few_bytes : x.q2.few_bytes;
+    x.rows = (int64_t)p1.before_splits * g->tokens * a->heads;
+    x.bytes = kCounters * 4 + x.few_bytes + x.q2.tile_bytes + x.rows * (c->dim * 4 + 8);
+    return nullptr;
+}
+
+static int attend_shared_impl(const tpl_kv_cache* c, const tpl_kv_batch* g, const tpl_kv_groups* s, const tpl_kv_query* a, void* ws,
+                              int64_t ws_bytes, hipStream_t st) {
+    AttendArgs p1, p2;
+    SharedChoice x;
+    int status;
+    if (const char* why = choose_shared(c, g, s, a, p1, p2, x, &status)) return fail_status(status, why);
+    if (!x.q2.few && !x.q2.tile) return TPL_OK;
+    if (s->count == 0) return attend_impl(c, g, a, ws, ws_bytes, st);
+    if (const int bad = check_query(a, ws, ws_bytes, x.bytes)) return bad;
+    p1.counters = p2.counters = (int*)ws;
+    p1.parts = p2.parts = (float*)((char*)ws + kCounters * 4);
+    p2.tile_parts = (float*)((char*)p2.parts + x.few_bytes);
+    p1.before = p2.before = (float*)((char*)p2.tile_parts + x.q2.tile_bytes);
+    p1.before_ml = p2.before_ml = (float2*)(p1.before + x.rows * c->dim);
+    hipError_t e = x.q1.tile ? launch_tile_shared(p1, x.q1.dk, false, st) : launch_few_shared(p1, x.q1.dc, x.q1.mr, st);
+    if (e == hipSuccess && x.q2.tile) e = launch_tile_shared(p2, x.q2.dk, false, st);
+    if (e == hipSuccess && x.q2.few) e = launch_few_shared(p2, x.q2.dc, x.q2.mr, st);
+    if (e == hipSuccess && x.q2.tile && p2.splits > 1) e = launch_tile_shared(p2, x.q2.dk, true, st);
     if (e != hipSuccess) return fail_status(TPL_E_HIP, std::string("HIP launch failed: ") + hipGetErrorString(e));
     return TPL_OK;
 }
@@ -212,6 +299,31 @@ int tpl_kv_attend(const tpl_kv_cache* cache, const tpl_kv_batch* batch, const tp
         return tpl::kv::attend_impl(cache, batch, args, workspace, workspace_bytes, stream);
     } catch (...) {
         return TPL_E_ARG;
+    }
+}
+
+int tpl_kv_attend_shared(const tpl_kv_cache* cache, const tpl_kv_batch* batch, const tpl_kv_groups* groups,
+                         const tpl_kv_query* args, void* workspace, int64_t workspace_bytes, hipStream_t stream) {
+    try {
+        return tpl::kv::attend_shared_impl(cache, batch, groups, args, workspace, workspace_bytes, stream);
+    } catch (...) {
+        return TPL_E_ARG;
+    }
+}
+
+int64_t tpl_kv_attend_shared_workspace(const tpl_kv_cache* cache, const tpl_kv_batch* batch, const tpl_kv_groups* groups,
+                                       const tpl_kv_query* args) {
+    try {
+        tpl::kv::AttendArgs p1, p2;
+        tpl::kv::SharedChoice x;
+        int status;
+        if (const char* why = tpl::kv::choose_shared(cache, batch, groups, args, p1, p2, x, &status)) {
+            tpl::fail_status(status, why);
+            return -1;
+        }
+        return x.bytes;
+    } catch (...) {
+        return -1;
     }
 }
 

@@ -40,6 +40,12 @@ struct AttendArgs {
     int32_t tiles;         // bound on the row tiles, grid order
     int32_t splits;        // parts of each tile's tokens
     float* tile_parts;
+    // Sequences that share their first tokens (the kernels' SHARED forms).
+    tpl_kv_groups s;
+    int32_t prefix;        // 1: groups' rows and the tokens they share; 0: sequences and their own tokens
+    int32_t before_splits; // parts that the first of these launches leaves of each row
+    float* before;         // [before_splits][tokens][heads][dim], weights' sums not yet divided by
+    float2* before_ml;     // [before_splits][tokens][heads]: a row's reference and sum of weights
 };
 
 // Where a token stands that is not there: beyond every position.
@@ -52,6 +58,53 @@ struct Span {
     int na, lo, n;
     __device__ __forceinline__ int base(int t) const { return t < na ? t * 16 : lo + (t - na) * 16; }
 };
+
+// The groups that hold tokens lo .. hi - 1.
+__device__ __forceinline__ Span span_from(int lo, int hi) {
+    Span s;
+    s.na = 0;
+    s.lo = lo & ~15;
+    s.n = hi > s.lo ? ((hi + 15) >> 4) - (lo >> 4) : 0;
+    return s;
+}
+
+// Group g of the sequences that share their first tokens, and their number:
+// its rows, which are those of its sequences, and as its length the tokens
+// that they share.  One that is not in order has no rows.
+struct Group {
+    int first, end;   // sequences
+    Seq s;
+};
+
+__device__ __forceinline__ Group read_group(const AttendArgs& p, int g) {
+    Group x;
+    x.first = p.s.groups[g];
+    x.end = p.s.groups[g + 1];
+    const int shared = p.s.shared[g];
+    x.s = Seq{0, 0, 0};
+    if (x.first < 0 || x.end <= x.first || x.end > p.g.batch || shared < 1 || shared > p.cap) return x;
+    const int row0 = p.g.starts[x.first], end = p.g.starts[x.end];
+    if (row0 >= 0 && end > row0 && end <= p.g.tokens) x.s = Seq{row0, end - row0, shared};
+    return x;
+}
+
+// How many of sequence b's first tokens are taken with its group: that group's,
+// or none where b has to look for itself.  Its group is the last of those in
+// order that begin at or before it.
+__device__ __forceinline__ int shared_of(const AttendArgs& p, int b, const Seq& s) {
+    int lo = 0, hi = p.s.count;   // groups[lo] <= b, as far as they are in order
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (p.s.groups[mid] <= b)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    const Group g = read_group(p, lo);
+    const bool ok = g.s.n > 0 && g.first <= b && b < g.end && s.n > 0 && g.s.row0 <= s.row0 && s.row0 + s.n <= g.s.row0 + g.s.n &&
+                    g.s.length <= s.length - s.n;
+    return ok ? g.s.length : 0;
+}
 
 __device__ __forceinline__ Span span_of(const AttendArgs& p, int first_pos, int last_pos) {
     Span s;
@@ -119,23 +172,43 @@ struct FewSeq {
     Span span;
     int tiles;      // row tiles
     int steps;      // steps of one row tile, at least 1
+    int row;        // SHARED: its row of the table
+    int lo;         // SHARED: its first token here
     __device__ __forceinline__ uint64_t all() const { return (uint64_t)tiles * (uint32_t)steps; }
 };
 
-template <int ROWS>
+// What the split kernel takes in turn: sequences, or groups of them.
+template <bool SHARED>
+__device__ __forceinline__ int few_items(const AttendArgs& p) { return SHARED && p.prefix ? p.s.count : p.g.batch; }
+
+template <int ROWS, bool SHARED>
 __device__ __forceinline__ FewSeq few_seq(const AttendArgs& p, int b) {
     FewSeq f;
-    f.s = read_seq(p.g, b);
+    f.row = b;
+    f.lo = 0;
+    if (SHARED && p.prefix) {
+        const Group g = read_group(p, b);
+        f.s = g.s;
+        f.row = g.first;
+    } else {
+        f.s = read_seq(p.g, b);
+    }
     const int64_t rows = (int64_t)f.s.n * p.group;
     if (rows > p.few) f.s.n = 0;
     f.tiles = f.s.n ? (int)((rows + ROWS - 1) / ROWS) : 0;
-    f.span = span_of(p, f.s.length - f.s.n, f.s.length - 1);
+    if constexpr (SHARED) {
+        if (!p.prefix) f.lo = shared_of(p, b, f.s);
+        f.span = span_from(f.lo, f.s.length < p.cap ? f.s.length : p.cap);
+    } else {
+        f.span = span_of(p, f.s.length - f.s.n, f.s.length - 1);
+    }
     const int log = 3 - p.heads_log;   // kStepGroups a wave's share of them
     f.steps = (f.span.n + (1 << log) - 1) >> log;
     if (f.steps < 1) f.steps = 1;
     return f;
 }
 
+template <bool SHARED>
 __device__ __forceinline__ FewSeq uniform(FewSeq f) {
     f.s.row0 = uniform(f.s.row0);
     f.s.n = uniform(f.s.n);
@@ -145,9 +218,14 @@ __device__ __forceinline__ FewSeq uniform(FewSeq f) {
     f.span.n = uniform(f.span.n);
     f.tiles = uniform(f.tiles);
     f.steps = uniform(f.steps);
+    if constexpr (SHARED) {
+        f.row = uniform(f.row);
+        f.lo = uniform(f.lo);
+    }
     return f;
 }
 
+template <bool SHARED>
 __device__ __forceinline__ FewSeq from_lane(FewSeq f, int lane) {
     f.s.row0 = __builtin_amdgcn_readlane(f.s.row0, lane);
     f.s.n = __builtin_amdgcn_readlane(f.s.n, lane);
@@ -157,6 +235,10 @@ __device__ __forceinline__ FewSeq from_lane(FewSeq f, int lane) {
     f.span.n = __builtin_amdgcn_readlane(f.span.n, lane);
     f.tiles = __builtin_amdgcn_readlane(f.tiles, lane);
     f.steps = __builtin_amdgcn_readlane(f.steps, lane);
+    if constexpr (SHARED) {
+        f.row = __builtin_amdgcn_readlane(f.row, lane);
+        f.lo = __builtin_amdgcn_readlane(f.lo, lane);
+    }
     return f;
 }
 
@@ -164,9 +246,9 @@ __device__ __forceinline__ FewSeq from_lane(FewSeq f, int lane) {
 // joining of a tile's parts (8 at a time) short beside its steps.  An average
 // sequence of n steps takes about c + n / (8 c) of a step's time with c a
 // share, least at c = sqrt(n / 8).
-__device__ __forceinline__ int share_of(const AttendArgs& p, int total) {
+__device__ __forceinline__ int share_of(const AttendArgs& p, int items, int total) {
     const int equal = (int)(((uint32_t)total + (uint32_t)p.shares - 1) / (uint32_t)p.shares);
-    const int short_ = (int)__builtin_sqrtf((float)total / (float)(p.g.batch * 8)) + 1;
+    const int short_ = (int)__builtin_sqrtf((float)total / (float)(items * 8)) + 1;
     return equal > short_ ? equal : short_;
 }
 
@@ -176,20 +258,21 @@ __device__ __forceinline__ int share_of(const AttendArgs& p, int total) {
 // begins in (-1: none) with that sequence's own first step.  More steps than
 // 31 bits hold can only be counted for sequences that claim one another's
 // rows (the host refuses sizes that allow them otherwise): nothing is done.
-template <int ROWS>
+template <int ROWS, bool SHARED>
 __device__ __forceinline__ int locate(const AttendArgs& p, int share, int* at_b, FewSeq* at_seq, int* at_step, int* chunk) {
     __shared__ uint64_t sums[4];
     __shared__ int found_step, found_b;
     __shared__ FewSeq found;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const bool alone = p.g.batch <= 64;   // every wave counts them all
-    const int per = alone ? 1 : (p.g.batch + 255) / 256, me = alone ? lane : tid;
+    const int items = few_items<SHARED>(p);
+    const bool alone = items <= 64;   // every wave counts them all
+    const int per = alone ? 1 : (items + 255) / 256, me = alone ? lane : tid;
     uint64_t mine = 0;
     FewSeq f = {};
     for (int i = 0; i < per; ++i) {
         const int b = me * per + i;
-        if (b < p.g.batch) {
-            f = few_seq<ROWS>(p, b);
+        if (b < items) {
+            f = few_seq<ROWS, SHARED>(p, b);
             mine += f.all();
         }
     }
@@ -217,7 +300,7 @@ __device__ __forceinline__ int locate(const AttendArgs& p, int share, int* at_b,
     *at_b = -1;
     *at_step = *chunk = 0;
     if (total == 0 || total > 0x7fffffffu) return 0;
-    *chunk = uniform(share_of(p, (int)total));
+    *chunk = uniform(share_of(p, items, (int)total));
     const uint64_t c = (uint64_t)share * (uint32_t)*chunk;
     const bool here = mine && before <= c && c < before + mine;
     if (alone) {
@@ -225,7 +308,7 @@ __device__ __forceinline__ int locate(const AttendArgs& p, int share, int* at_b,
         if (m) {
             const int from = __builtin_ctzll(m);
             *at_b = from;
-            *at_seq = from_lane(f, from);
+            *at_seq = from_lane<SHARED>(f, from);
             *at_step = __builtin_amdgcn_readlane((int)before, from);
         }
         return (int)total;
@@ -234,8 +317,8 @@ __device__ __forceinline__ int locate(const AttendArgs& p, int share, int* at_b,
         int b = tid;
         for (int i = 0; per > 1 && i < per; ++i) {
             b = tid * per + i;
-            if (b >= p.g.batch) break;
-            f = few_seq<ROWS>(p, b);
+            if (b >= items) break;
+            f = few_seq<ROWS, SHARED>(p, b);
             if (c < before + f.all()) break;
             before += f.all();
         }
@@ -247,37 +330,9 @@ __device__ __forceinline__ int locate(const AttendArgs& p, int share, int* at_b,
     // The same in every lane, which the compiler has to be told for what
     // follows from them to stay in scalar registers.
     *at_b = uniform(found_b);
-    *at_seq = uniform(found);
+    *at_seq = uniform<SHARED>(found);
     *at_step = uniform(found_step);
     return (int)total;
-}
-
-// The sequence that row tile x of the tile kernel belongs to: sequence b's
-// tiles are numbered from starts[b] / tile_tokens + b on, and of those in
-// order whose numbers begin at or before x it is the last.  64 are looked at
-// together, with all that is needed of them, so that it is known after one
-// load's latency.  b is -1 where there is none.
-struct TileSeq {
-    int b;
-    Seq s;
-};
-
-__device__ __forceinline__ TileSeq tile_seq(const AttendArgs& p, int x) {
-    const int lane = threadIdx.x & 63;
-    TileSeq t = {-1, {0, 0, 0}};
-    for (int b0 = 0; b0 < p.g.batch; b0 += 64) {
-        const int bb = b0 + lane < p.g.batch ? b0 + lane : p.g.batch - 1;
-        const Seq s = read_seq(p.g, bb);
-        const uint64_t m = __ballot(b0 + lane < p.g.batch && s.n > 0 && s.row0 / p.tile_tokens + bb <= x);
-        if (m) {
-            const int from = 63 - __builtin_clzll(m);
-            t.b = b0 + from;
-            t.s.row0 = __builtin_amdgcn_readlane(s.row0, from);
-            t.s.n = __builtin_amdgcn_readlane(s.n, from);
-            t.s.length = __builtin_amdgcn_readlane(s.length, from);
-        }
-    }
-    return t;
 }
 
 // Part of a row tile that one workgroup of the split kernel leaves: rows of
@@ -295,6 +350,8 @@ TPL_HD constexpr int few_blocks(bool held8, int dc, int mr) {
 
 hipError_t launch_few(const AttendArgs& p, int dc, int mr, hipStream_t st);
 hipError_t launch_tile(const AttendArgs& p, int dk, bool join, hipStream_t st);
+hipError_t launch_few_shared(const AttendArgs& p, int dc, int mr, hipStream_t st);
+hipError_t launch_tile_shared(const AttendArgs& p, int dk, bool join, hipStream_t st);
 
 TPL_HD int tile_part_floats(int dk, int rows) { return rows * (dk + 2); }
 

@@ -19,9 +19,16 @@ typedef int (*AppendFn)(const tpl_kv_cache*, const tpl_kv_batch*, const tpl_kv_n
 typedef int (*AttendFn)(const tpl_kv_cache*, const tpl_kv_batch*, const tpl_kv_query*, void*, int64_t, hipStream_t);
 typedef int64_t (*WorkspaceFn)(const tpl_kv_cache*, const tpl_kv_batch*, const tpl_kv_query*);
 
+typedef int (*SharedFn)(const tpl_kv_cache*, const tpl_kv_batch*, const tpl_kv_groups*, const tpl_kv_query*, void*, int64_t, hipStream_t);
+typedef int64_t (*SharedWorkspaceFn)(const tpl_kv_cache*, const tpl_kv_batch*, const tpl_kv_groups*, const tpl_kv_query*);
+typedef int (*ReadFn)(const tpl_kv_cache*, const tpl_kv_batch*, const tpl_kv_rows*, hipStream_t);
+
 AppendFn g_append = nullptr;
 AttendFn g_attend = nullptr;
 WorkspaceFn g_workspace = nullptr;
+SharedFn g_shared = nullptr;
+SharedWorkspaceFn g_shared_workspace = nullptr;
+ReadFn g_read = nullptr;
 
 constexpr long kLook = -1;       // something is not right, or not known here
 constexpr long kWorkspace = -2;  // the workspace is too small
@@ -130,38 +137,47 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
 }
 
+// A query's tensors and numbers; whether all is as it should be.  A Python
+// error may be left.
+bool query_of(const tpl_kv_cache* c, int64_t index, const at::Tensor* q, PyObject* scale, PyObject* out, PyObject* lse, tpl_kv_query& x) {
+    if (!c || index < 0 || !q || q->dim() != 3 || q->size(1) > INT32_MAX) return false;
+    const at::Tensor* o = tensor_of(out);
+    const at::ScalarType type = q->scalar_type();
+    const int64_t tokens = q->size(0), heads = q->size(1);
+    if ((type != at::kBFloat16 && type != at::kHalf) || !rows(q, type, index, tokens, heads, c->dim) ||
+        !rows(o, type, index, tokens, heads, c->dim))
+        return false;
+    x.q = q->data_ptr(), x.out = o->data_ptr();
+    x.q_token = q->stride(0), x.q_head = q->stride(1), x.o_token = o->stride(0), x.o_head = o->stride(1);
+    x.type = type == at::kBFloat16 ? TPL_KV_BF16 : TPL_KV_FP16;
+    x.heads = (int32_t)heads;
+    x.scale = (float)(scale == Py_None ? 1.0 / std::sqrt((double)c->dim) : PyFloat_AsDouble(scale));
+    if (lse != Py_None) {
+        const at::Tensor* l = tensor_of(lse);
+        if (!l || l->scalar_type() != at::kFloat || l->dim() != 2 || l->size(0) != tokens || l->size(1) != heads || !on(*l, index))
+            return false;
+        x.lse = (float*)l->data_ptr();
+        x.l_token = l->stride(0), x.l_head = l->stride(1);
+    }
+    return true;
+}
+
 // attend(cache, index, q, table, starts, lengths, scale, window, sinks, out, lse, workspace, bytes, stream)
 PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (n != 14) return PyErr_Format(PyExc_TypeError, "attend takes 14 arguments"), nullptr;
     try {
         const tpl_kv_cache* c = (const tpl_kv_cache*)PyLong_AsVoidPtr(a[0]);
         const int64_t index = PyLong_AsLongLong(a[1]);
-        const at::Tensor *q = tensor_of(a[2]), *o = tensor_of(a[9]);
-        if (!g_attend || !c || index < 0 || !q || q->dim() != 3 || q->size(1) > INT32_MAX) return PyLong_FromLong(kLook);
-        const at::ScalarType type = q->scalar_type();
-        const int64_t tokens = q->size(0), heads = q->size(1);
-        if ((type != at::kBFloat16 && type != at::kHalf) || !rows(q, type, index, tokens, heads, c->dim) ||
-            !rows(o, type, index, tokens, heads, c->dim))
-            return PyLong_FromLong(kLook);
-        tpl_kv_batch g;
-        if (!batch_of(a[3], a[4], a[5], index, tokens, g)) return PyLong_FromLong(kLook);
+        const at::Tensor* q = tensor_of(a[2]);
         tpl_kv_query x = {};
-        x.q = q->data_ptr(), x.out = o->data_ptr();
-        x.q_token = q->stride(0), x.q_head = q->stride(1), x.o_token = o->stride(0), x.o_head = o->stride(1);
-        x.type = type == at::kBFloat16 ? TPL_KV_BF16 : TPL_KV_FP16;
-        x.heads = (int32_t)heads;
-        x.scale = (float)(a[6] == Py_None ? 1.0 / std::sqrt((double)c->dim) : PyFloat_AsDouble(a[6]));
+        const bool ok = g_attend && query_of(c, index, q, a[6], a[9], a[10], x);
+        if (PyErr_Occurred()) return nullptr;
+        tpl_kv_batch g;
+        if (!ok || !batch_of(a[3], a[4], a[5], index, q->size(0), g)) return PyLong_FromLong(kLook);
         const int64_t window = PyLong_AsLongLong(a[7]), sinks = PyLong_AsLongLong(a[8]);
         if (PyErr_Occurred()) return nullptr;
         if (window < INT32_MIN || window > INT32_MAX || sinks < INT32_MIN || sinks > INT32_MAX) return PyLong_FromLong(kLook);
         x.window = (int32_t)window, x.sinks = (int32_t)sinks;
-        if (a[10] != Py_None) {
-            const at::Tensor* l = tensor_of(a[10]);
-            if (!l || l->scalar_type() != at::kFloat || l->dim() != 2 || l->size(0) != tokens || l->size(1) != heads || !on(*l, index))
-                return PyLong_FromLong(kLook);
-            x.lse = (float*)l->data_ptr();
-            x.l_token = l->stride(0), x.l_head = l->stride(1);
-        }
         void* ws = PyLong_AsVoidPtr(a[11]);
         const int64_t bytes = PyLong_AsLongLong(a[12]);
         hipStream_t st = (hipStream_t)PyLong_AsVoidPtr(a[13]);
@@ -175,18 +191,77 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
 }
 
-// bind(append, attend, workspace): the loaded library's entry points.
+// attend_shared(cache, index, q, table, starts, lengths, groups, shared, scale, out, lse, workspace, bytes, stream)
+PyObject* attend_shared(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    if (n != 14) return PyErr_Format(PyExc_TypeError, "attend_shared takes 14 arguments"), nullptr;
+    try {
+        const tpl_kv_cache* c = (const tpl_kv_cache*)PyLong_AsVoidPtr(a[0]);
+        const int64_t index = PyLong_AsLongLong(a[1]);
+        const at::Tensor *q = tensor_of(a[2]), *gs = tensor_of(a[6]), *sh = tensor_of(a[7]);
+        tpl_kv_query x = {};
+        const bool ok = g_shared && query_of(c, index, q, a[8], a[9], a[10], x);
+        if (PyErr_Occurred()) return nullptr;
+        tpl_kv_batch g;
+        if (!ok || !batch_of(a[3], a[4], a[5], index, q->size(0), g) || !ints(gs, 1, index) || !ints(sh, 1, index) ||
+            gs->size(0) != sh->size(0) + 1 || sh->size(0) > INT32_MAX)
+            return PyLong_FromLong(kLook);
+        const tpl_kv_groups s = {(const int32_t*)gs->data_ptr(), (const int32_t*)sh->data_ptr(), (int32_t)sh->size(0)};
+        void* ws = PyLong_AsVoidPtr(a[11]);
+        const int64_t bytes = PyLong_AsLongLong(a[12]);
+        hipStream_t st = (hipStream_t)PyLong_AsVoidPtr(a[13]);
+        if (PyErr_Occurred()) return nullptr;
+        const int64_t need = g_shared_workspace(c, &g, &s, &x);
+        if (need < 0) return PyLong_FromLong(kLook);
+        if (need > bytes) return PyLong_FromLong(kWorkspace);
+        return PyLong_FromLong(g_shared(c, &g, &s, &x, ws, bytes, st));
+    } catch (const std::exception& e) {
+        return PyErr_Format(PyExc_RuntimeError, "%s", e.what()), nullptr;
+    }
+}
+
+// read(cache, index, table, starts, lengths, k, v, stream)
+PyObject* read(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    if (n != 8) return PyErr_Format(PyExc_TypeError, "read takes 8 arguments"), nullptr;
+    try {
+        const tpl_kv_cache* c = (const tpl_kv_cache*)PyLong_AsVoidPtr(a[0]);
+        const int64_t index = PyLong_AsLongLong(a[1]);
+        const at::Tensor *k = tensor_of(a[5]), *v = tensor_of(a[6]), *some = k ? k : v;
+        if (!g_read || !c || index < 0 || !some || some->dim() != 3 || (!k && a[5] != Py_None) || (!v && a[6] != Py_None))
+            return PyLong_FromLong(kLook);
+        const at::ScalarType type = some->scalar_type();
+        const int64_t tokens = some->size(0);
+        if ((type != at::kBFloat16 && type != at::kHalf) || (k && !rows(k, type, index, tokens, c->kv_heads, c->dim)) ||
+            (v && !rows(v, type, index, tokens, c->kv_heads, c->dim)))
+            return PyLong_FromLong(kLook);
+        tpl_kv_batch g;
+        if (!batch_of(a[2], a[3], a[4], index, tokens, g)) return PyLong_FromLong(kLook);
+        tpl_kv_rows x = {};
+        if (k) x.k = k->data_ptr(), x.k_token = k->stride(0), x.k_head = k->stride(1);
+        if (v) x.v = v->data_ptr(), x.v_token = v->stride(0), x.v_head = v->stride(1);
+        x.type = type == at::kBFloat16 ? TPL_KV_BF16 : TPL_KV_FP16;
+        hipStream_t st = (hipStream_t)PyLong_AsVoidPtr(a[7]);
+        if (PyErr_Occurred()) return nullptr;
+        return PyLong_FromLong(g_read(c, &g, &x, st));
+    } catch (const std::exception& e) {
+        return PyErr_Format(PyExc_RuntimeError, "%s", e.what()), nullptr;
+    }
+}
+
+// bind: the loaded library's entry points, in the order of kv.py's EXPORTED.
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    if (n != 3) return PyErr_Format(PyExc_TypeError, "bind takes 3 arguments"), nullptr;
-    g_append = (AppendFn)PyLong_AsVoidPtr(a[0]);
-    g_attend = (AttendFn)PyLong_AsVoidPtr(a[1]);
-    g_workspace = (WorkspaceFn)PyLong_AsVoidPtr(a[2]);
+    if (n != 6) return PyErr_Format(PyExc_TypeError, "bind takes 6 arguments"), nullptr;
+    void* p[6];
+    for (int i = 0; i < 6; ++i) p[i] = PyLong_AsVoidPtr(a[i]);
     if (PyErr_Occurred()) return nullptr;
+    g_append = (AppendFn)p[0], g_attend = (AttendFn)p[1], g_workspace = (WorkspaceFn)p[2];
+    g_shared = (SharedFn)p[3], g_shared_workspace = (SharedWorkspaceFn)p[4], g_read = (ReadFn)p[5];
     Py_RETURN_NONE;
 }
 
 PyMethodDef methods[] = {{"append", (PyCFunction)(void*)append, METH_FASTCALL, nullptr},
                          {"attend", (PyCFunction)(void*)attend, METH_FASTCALL, nullptr},
+                         {"attend_shared", (PyCFunction)(void*)attend_shared, METH_FASTCALL, nullptr},
+                         {"read", (PyCFunction)(void*)read, METH_FASTCALL, nullptr},
                          {"bind", (PyCFunction)(void*)bind, METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_kv_call", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -3,13 +3,15 @@
 ``PagedCache`` names the two pools of pages that a program holds (and the
 scales of an e4m3 one); ``append`` rotates a batch's new keys and queries to
 their positions and writes keys and values into their pages; ``attend`` lets
-the queries attend to what the cache holds.  A batch is packed: sequence ``b``
+the queries attend to what the cache holds, and ``attend_shared`` does so for
+sequences that share their first tokens; ``read`` takes tokens out of the pages
+again.  A batch is packed: sequence ``b``
 owns rows ``starts[b]:starts[b + 1]`` of the token tensors, ``lengths[b]``
 tokens with those, and the pages that its row of ``table`` names in order (a
 negative entry is a page that is not there).  Rows of no sequence, and of one
 that is skipped because its numbers are out of order, are left as they are.
-Both run on torch's current stream, or a named one, without waiting, read
-``table``, ``starts`` and ``lengths`` on the device only, and may be captured
+All run on torch's current stream, or a named one, without waiting, read
+``table``, ``starts``, ``lengths`` and groups on the device only, and may be captured
 into a graph.
 
 Arguments are checked here for their types and shapes, and by the C entry
@@ -32,7 +34,8 @@ BF16, FP16, E4M3 = 0, 1, 2
 MAX_AXES = 4
 COUNTERS = 4096   # TPL_KV_COUNTERS: the bytes of a workspace that a call finds zero and leaves zero
 
-EXPORTED = ("tpl_kv_append", "tpl_kv_attend", "tpl_kv_attend_workspace")
+EXPORTED = ("tpl_kv_append", "tpl_kv_attend", "tpl_kv_attend_workspace", "tpl_kv_attend_shared",
+            "tpl_kv_attend_shared_workspace", "tpl_kv_read")
 
 _P, _I32, _I64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
 
@@ -63,35 +66,48 @@ class Query(ctypes.Structure):
                 + [("scale", ctypes.c_float)] + [(n, _I32) for n in ("type", "heads", "window", "sinks")])
 
 
+class Rows(ctypes.Structure):
+    _fields_ = ([(n, _P) for n in ("k", "v")] + [(n, _I64) for n in ("k_token", "k_head", "v_token", "v_head")] + [("type", _I32)])
+
+
+class Groups(ctypes.Structure):
+    _fields_ = [("groups", _P), ("shared", _P), ("count", _I32)]
+
+
 # The same layouts for packing a call's numbers in one go.
 _pack_batch = struct.Struct("3Pq3i4x").pack
 _pack_new = struct.Struct("6P9q5i4i4x").pack
 _pack_query = struct.Struct("3P6qf4i4x").pack
+_pack_rows = struct.Struct("2P4qi4x").pack
+_pack_groups = struct.Struct("2Pi4x").pack
 
 # attend's workspaces: (address, bytes, tensor) by device, then stream.
 _workspaces = {}
 
 _lib = None
-_calls = []   # append, attend, workspace
-_append = _attend = None   # the extension's, which read the tensors too
+_calls = []   # as EXPORTED
+_append = _attend = _attend_shared = _read = None   # the extension's, which read the tensors too
 
 
 def load():
     """libtpl.so with this module's entry points declared."""
-    global _lib, _append, _attend
+    global _lib, _append, _attend, _attend_shared, _read
     if _lib is None:
         lib = tpl.load()
         held = ctypes.PyDLL(lib._name)
-        c, b, n, q = (ctypes.POINTER(x) for x in (Cache, Batch, New, Query))
-        for name, arg, rest, res in (("tpl_kv_append", n, [_P], ctypes.c_int),
-                                     ("tpl_kv_attend", q, [_P, _I64, _P], ctypes.c_int),
-                                     ("tpl_kv_attend_workspace", q, [], _I64)):
+        c, b, n, q, r, g = (ctypes.POINTER(x) for x in (Cache, Batch, New, Query, Rows, Groups))
+        for name, args, rest, res in (("tpl_kv_append", [n], [_P], ctypes.c_int),
+                                      ("tpl_kv_attend", [q], [_P, _I64, _P], ctypes.c_int),
+                                      ("tpl_kv_attend_workspace", [q], [], _I64),
+                                      ("tpl_kv_attend_shared", [g, q], [_P, _I64, _P], ctypes.c_int),
+                                      ("tpl_kv_attend_shared_workspace", [g, q], [], _I64),
+                                      ("tpl_kv_read", [r], [_P], ctypes.c_int)):
             f = getattr(lib, name)
-            f.argtypes, f.restype = [c, b, arg] + rest, res
+            f.argtypes, f.restype = [c, b] + args + rest, res
             # A second handle, which takes packed bytes in the structures' places.  It keeps the interpreter's lock, as
             # the extension does: the launches of one call follow one another on a stream whose workspace others use.
             f = held[name]
-            f.argtypes, f.restype = [_P, _P, _P] + rest, res
+            f.argtypes, f.restype = [_P] * (2 + len(args)) + rest, res
             _calls.append(f)
         try:
             from . import _kv_call
@@ -99,7 +115,7 @@ def load():
             raise RuntimeError("tensor_layout_amd/_kv_call.so is missing or was built for another torch: build it "
                                "(python -c 'import __graft_entry__ as g; g.build()')") from e
         _kv_call.bind(*(ctypes.cast(getattr(lib, n), _P).value for n in EXPORTED))
-        _append, _attend = _kv_call.append, _kv_call.attend
+        _append, _attend, _attend_shared, _read = _kv_call.append, _kv_call.attend, _kv_call.attend_shared, _kv_call.read
         _lib = lib
     return _lib
 
@@ -305,11 +321,12 @@ def _append_checked(cache, k, v, table, starts, lengths, q, q_out, inv_freq, pos
     return q_out
 
 
-def _workspace(cache, batch, args):
+def _workspace(cache, call, *args):
+    """Of `call` (1: attend, 3: attend_shared) for these packed arguments."""
     load()
-    size = _calls[2](cache._at, batch, args)
+    size = _calls[call + 1](cache._at, *args)
     if size < 0:
-        _raise(_calls[1](cache._at, batch, args, None, 0, None))   # refused the same way, before anything is looked at on the device
+        _raise(_calls[call](cache._at, *args, None, 0, None))   # refused the same way, before anything is looked at on the device
     return size
 
 
@@ -334,14 +351,14 @@ def _capturing(cache, s, stream):
         return torch.cuda.is_current_stream_capturing()
 
 
-def _attend_packed(cache, batch, args, size, stream):
+def _attend_packed(cache, call, args, size, stream):
     """The call itself, with a workspace of the stream's own."""
     index = cache._index
     s = _stream(index) if stream is None else int(stream)
     ws = cache._work.get(s)
     if ws is None or ws[1] < size or _capturing(cache, s, stream):
         ws = _new_workspace(cache, size, s, stream)
-    return _calls[1](cache._at, batch, args, ws[0], size, s)
+    return _calls[call](cache._at, *args, ws[0], size, s)
 
 
 def _new_workspace(cache, size, s, stream):
@@ -387,10 +404,40 @@ def attend(q, cache: PagedCache, table, starts, lengths, *, scale: Optional[floa
                 return out
             if status > 0:
                 _raise(status)
-    return _attend_checked(q, cache, table, starts, lengths, scale, window, sinks, out, lse, stream)
+    return _attend_checked(q, cache, table, starts, lengths, None, None, scale, window, sinks, out, lse, stream)
 
 
-def _attend_checked(q, cache, table, starts, lengths, scale, window, sinks, out, lse, stream):
+def attend_shared(q, cache: PagedCache, table, starts, lengths, groups, shared, *, scale: Optional[float] = None, out=None,
+                  lse=None, stream: Optional[int] = None):
+    """``attend`` for sequences that share their first tokens, which are read and multiplied once for all of a group's rows.
+
+    groups  int32 [n + 1]: group g is sequences groups[g] .. groups[g + 1] - 1.
+    shared  int32 [n]: how many first tokens they share, held in the pages that their first one's row of ``table`` names.
+
+    From there on each sequence has the tokens of its own row of ``table``.  A sequence in no group, or with new tokens
+    among the shared ones, attends by itself to its own row's pages, which has the same result where those begin with the
+    shared pages (a page that is shared in part is copied: ``read``, ``append``).  Groups follow one another: rows of two
+    that overlap may be served for either or not at all.
+
+    The rest is ``attend``'s; there is no window.  Returns ``out``."""
+    if _lib is None:
+        load()
+    if out is None:
+        out = _result(q, cache, stream)
+    index = cache._index
+    if index >= 0 and _device() == index:
+        s = _stream(index) if stream is None else int(stream)
+        ws = cache._work.get(s)
+        if ws is not None and not _capturing(cache, s, stream):
+            status = _attend_shared(cache._at, index, q, table, starts, lengths, groups, shared, scale, out, lse, ws[0], ws[1], s)
+            if status == 0:
+                return out
+            if status > 0:
+                _raise(status)
+    return _attend_checked(q, cache, table, starts, lengths, groups, shared, scale, 0, 0, out, lse, stream)
+
+
+def _attend_checked(q, cache, table, starts, lengths, groups, shared, scale, window, sinks, out, lse, stream):
     """The same, each argument by itself: says what is wrong, or makes the call, with a new workspace where it needs one."""
     index, dtype = cache._index, q.dtype
     shape = q.shape
@@ -419,13 +466,56 @@ def _attend_checked(q, cache, table, starts, lengths, scale, window, sinks, out,
     ot, oh, _ = out.stride()
     args = _pack_query(q.data_ptr(), out.data_ptr(), lp, qt, qh, ot, oh, lt, lh, scale,
                        _TYPES[dtype], heads, window, sinks)
-    size = _workspace(cache, batch, args)
+    call, packed = 1, (batch, args)
+    if groups is not None:
+        if not (_ints_ok(groups, index, None) and groups.shape[0] > 0 and _ints_ok(shared, index, groups.shape[0] - 1)):
+            _ints("groups", groups, cache.device, None)
+            _need(groups.shape[0] > 0, "groups must have a number more than there are groups", tpl.TPL_E_EXTENT)
+            _ints("shared", shared, cache.device, groups.shape[0] - 1)
+        call, packed = 3, (batch, _pack_groups(groups.data_ptr(), shared.data_ptr(), shared.shape[0]), args)
+    size = _workspace(cache, call, *packed)
     _need(index >= 0, "tensors must live on the GPU")
     if _device() == index:
-        status = _attend_packed(cache, batch, args, size, stream)
+        status = _attend_packed(cache, call, packed, size, stream)
     else:
         with torch.cuda.device(index):
-            status = _attend_packed(cache, batch, args, size, stream)
+            status = _attend_packed(cache, call, packed, size, stream)
     if status:
         _raise(status)
     return out
+
+
+def read(cache: PagedCache, table, starts, lengths, k=None, v=None, *, stream: Optional[int] = None) -> None:
+    """Write each sequence's last tokens, as many as it has rows, out of the cache into ``k`` and ``v`` [tokens, kv_heads, dim].
+
+    They are what ``append`` with the same ``table``, ``starts`` and ``lengths`` wrote: an e4m3 value times its block's
+    scale, rounded once to the tensors' type (bf16 or fp16); a 16-bit cache is read as its own type, bit for bit.  Other
+    tokens are read by naming other lengths: ``lengths`` = n and n rows read a sequence's first n.  Either of ``k`` and
+    ``v`` may be None.  A token whose page is not there gives zeros."""
+    if _lib is None:
+        load()
+    index = cache._index
+    if index >= 0 and _device() == index:
+        status = _read(cache._at, index, table, starts, lengths, k, v, _stream(index) if stream is None else int(stream))
+        if status == 0:
+            return
+        if status > 0:
+            _raise(status)
+    _need(k is not None or v is not None, "k and v must not both be None")
+    some = v if k is None else k
+    _need(some.dim() == 3, "k and v must be [tokens, kv_heads, dim]", tpl.TPL_E_EXTENT)
+    _need(some.dtype in (torch.bfloat16, torch.float16), "k and v must be bf16 or fp16", tpl.TPL_E_DTYPE)
+    tokens = some.shape[0]
+    ptr, strides = [], []
+    for name, t in (("k", k), ("v", v)):
+        if t is not None:
+            _heads(name, t, some.dtype, cache.device, (tokens, cache.kv_heads, cache.dim))
+        ptr.append(0 if t is None else t.data_ptr())
+        strides += (0, 0) if t is None else t.stride()[:2]
+    _, _, batch = _batch(cache, table, starts, lengths, tokens)
+    args = _pack_rows(*ptr, *strides, _TYPES[some.dtype])
+    _need(index >= 0, "tensors must live on the GPU")
+    with torch.cuda.device(index):
+        status = _calls[5](cache._at, batch, args, _stream(index) if stream is None else int(stream))
+    if status:
+        _raise(status)
