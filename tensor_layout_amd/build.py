@@ -17,7 +17,8 @@ LIB = os.path.join(HERE, "libtpl.so")
 SOURCES = ["planner.cpp", "kernels.hip", "kernels_stream.hip", "kernels_quad.hip", "kernels_lds.hip",
            "kernels_lds_w12.hip", "kernels_lds_w48.hip", "kernels_lds_w16.hip",
            "kernels_swap.hip", "kernels_rec.hip", "kernels_etile.hip", "staged.hip",
-           "kv_tile.hip", "kv_tile_shared.hip", "kv_few.hip", "kv_few_shared.hip", "kv_append.hip", "kv_attend.hip", "kv_read.hip"]
+           "kv_tile.hip", "kv_tile_shared.hip", "kv_few.hip", "kv_few_shared.hip", "kv_append.hip", "kv_attend.hip", "kv_read.hip",
+           "linear_chunk.hip", "linear_step.hip", "linear.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [

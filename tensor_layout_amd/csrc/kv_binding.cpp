@@ -1,10 +1,11 @@
-// kv_binding.cpp -- reading of torch tensors for tensor_layout_amd/kv.py.
+// kv_binding.cpp -- reading of torch tensors for tensor_layout_amd/kv.py and
+// linear.py.
 //
 // A call's tensors are looked at and its structures filled here, then the C
 // entry point is called: 3.6 to 4 us a call with its launch, against 9 to 11
 // through Python's own attributes and ctypes, which is more than the smallest
 // calls take on the GPU.  Nothing is judged here: where anything is not as it
-// should be the call returns kLook, and kv.py looks for what it is and says
+// should be the call returns kLook, and the Python looks for what it is and says
 // so.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
@@ -12,6 +13,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "../../include/tpl_kv.h"
+#include "../../include/tpl_linear.h"
 
 namespace {
 
@@ -23,12 +25,17 @@ typedef int (*SharedFn)(const tpl_kv_cache*, const tpl_kv_batch*, const tpl_kv_g
 typedef int64_t (*SharedWorkspaceFn)(const tpl_kv_cache*, const tpl_kv_batch*, const tpl_kv_groups*, const tpl_kv_query*);
 typedef int (*ReadFn)(const tpl_kv_cache*, const tpl_kv_batch*, const tpl_kv_rows*, hipStream_t);
 
+typedef int (*LinearFn)(const tpl_linear_pool*, const tpl_linear_batch*, const tpl_linear_new*, void*, int64_t, hipStream_t);
+typedef int64_t (*LinearWorkspaceFn)(const tpl_linear_pool*, const tpl_linear_batch*, const tpl_linear_new*);
+
 AppendFn g_append = nullptr;
 AttendFn g_attend = nullptr;
 WorkspaceFn g_workspace = nullptr;
 SharedFn g_shared = nullptr;
 SharedWorkspaceFn g_shared_workspace = nullptr;
 ReadFn g_read = nullptr;
+LinearFn g_linear = nullptr;
+LinearWorkspaceFn g_linear_workspace = nullptr;
 
 constexpr long kLook = -1;       // something is not right, or not known here
 constexpr long kWorkspace = -2;  // the workspace is too small
@@ -258,11 +265,58 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Py_RETURN_NONE;
 }
 
+// linear_attend(pool, index, q, k, v, slots, starts, sources, scale, out, stream)
+PyObject* linear_attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    if (n != 11) return PyErr_Format(PyExc_TypeError, "linear_attend takes 11 arguments"), nullptr;
+    try {
+        const tpl_linear_pool* c = (const tpl_linear_pool*)PyLong_AsVoidPtr(a[0]);
+        const int64_t index = PyLong_AsLongLong(a[1]);
+        const at::Tensor *q = tensor_of(a[2]), *k = tensor_of(a[3]), *v = tensor_of(a[4]), *sl = tensor_of(a[5]), *st = tensor_of(a[6]),
+                         *so = tensor_of(a[7]), *o = tensor_of(a[9]);
+        if (!g_linear || !c || index < 0 || !q || q->dim() != 3 || q->size(1) > INT32_MAX || (!so && a[7] != Py_None))
+            return PyLong_FromLong(kLook);
+        const at::ScalarType type = q->scalar_type();
+        const int64_t tokens = q->size(0), heads = q->size(1);
+        if ((type != at::kBFloat16 && type != at::kHalf) || tokens > INT32_MAX || !rows(q, type, index, tokens, heads, c->key_dim) ||
+            !rows(k, type, index, tokens, heads, c->key_dim) || !rows(v, type, index, tokens, c->heads, c->value_dim) ||
+            !rows(o, type, index, tokens, c->heads, c->value_dim) || !ints(sl, 1, index) || !ints(st, 1, index) ||
+            st->size(0) != sl->size(0) + 1 || sl->size(0) > INT32_MAX || (so && (!ints(so, 1, index) || so->size(0) != sl->size(0))))
+            return PyLong_FromLong(kLook);
+        const tpl_linear_batch g = {(const int32_t*)sl->data_ptr(), so ? (const int32_t*)so->data_ptr() : nullptr,
+                                    (const int32_t*)st->data_ptr(), (int32_t)sl->size(0), (int32_t)tokens};
+        tpl_linear_new x = {};
+        x.q = q->data_ptr(), x.k = k->data_ptr(), x.v = v->data_ptr(), x.out = o->data_ptr();
+        x.q_token = q->stride(0), x.q_head = q->stride(1), x.k_token = k->stride(0), x.k_head = k->stride(1);
+        x.v_token = v->stride(0), x.v_head = v->stride(1), x.o_token = o->stride(0), x.o_head = o->stride(1);
+        x.scale = (float)(a[8] == Py_None ? 1.0 / std::sqrt((double)c->key_dim) : PyFloat_AsDouble(a[8]));
+        x.type = type == at::kBFloat16 ? TPL_KV_BF16 : TPL_KV_FP16;
+        x.key_heads = (int32_t)heads;
+        hipStream_t stream = (hipStream_t)PyLong_AsVoidPtr(a[10]);
+        if (PyErr_Occurred()) return nullptr;
+        const int64_t need = g_linear_workspace(c, &g, &x);
+        if (need < 0) return PyLong_FromLong(kLook);
+        if (need > 0) return PyLong_FromLong(kWorkspace);
+        return PyLong_FromLong(g_linear(c, &g, &x, nullptr, 0, stream));
+    } catch (const std::exception& e) {
+        return PyErr_Format(PyExc_RuntimeError, "%s", e.what()), nullptr;
+    }
+}
+
+PyObject* bind_linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    if (n != 2) return PyErr_Format(PyExc_TypeError, "bind_linear takes 2 arguments"), nullptr;
+    g_linear = (LinearFn)PyLong_AsVoidPtr(a[0]);
+    g_linear_workspace = (LinearWorkspaceFn)PyLong_AsVoidPtr(a[1]);
+    if (PyErr_Occurred()) return nullptr;
+    Py_RETURN_NONE;
+}
+
 PyMethodDef methods[] = {{"append", (PyCFunction)(void*)append, METH_FASTCALL, nullptr},
                          {"attend", (PyCFunction)(void*)attend, METH_FASTCALL, nullptr},
                          {"attend_shared", (PyCFunction)(void*)attend_shared, METH_FASTCALL, nullptr},
                          {"read", (PyCFunction)(void*)read, METH_FASTCALL, nullptr},
+                         {"linear_attend", (PyCFunction)(void*)linear_attend, METH_FASTCALL, nullptr},
                          {"bind", (PyCFunction)(void*)bind, METH_FASTCALL, nullptr},
+                         {"bind_linear", (PyCFunction)(void*)bind_linear, METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_kv_call", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

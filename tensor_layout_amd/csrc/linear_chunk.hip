@@ -1,0 +1,511 @@
+// linear_chunk.hip -- linear attention of many new tokens a sequence: chunks of
+// 64 tokens through the matrix units.
+//
+// With l = exp(decay), i and j a chunk's tokens from 0 on and S the state before it
+//
+//   out_i = l^(i+1) q_i S + sum_{j <= i} l^(i-j) (q_i k_j) v_j
+//   S'    = l^n S + sum_j l^(n-1-j) k_j v_j^T
+//
+// A workgroup takes one head of one sequence (or of a segment of it) and walks
+// over its chunks with the state in registers, 32 value channels a wave.  Queries,
+// keys and values stand in LDS as they lie in memory, and every product of
+// 32x32x16 reads them from there or has its operand in registers already:
+//
+//   P^T = K Q^T      its result (column i, rows j) is, with decay and mask, the
+//                    second operand of
+//   O^T = V^T P^T    where V^T's operands come by transposing reads of LDS, 4
+//                    tokens of a channel each, in the order of P^T's rows;
+//   O^T += S^T Q^T   the state's registers (column: value channel, rows: key
+//                    channels) are S^T's operand as they lie, if Q's operand
+//                    names key channels in the same order;
+//   S += K^T (w V)   K^T by transposing reads, w V from the registers of V^T.
+//
+// So neither the state nor the outputs pass through LDS.  P is computed once
+// for all waves, a block of 32x32 each, and handed over in LDS as operands.
+//
+// Roundings: P, S and w V are fp32 numbers and go into the products as the sum
+// of two 16-bit ones (16 or 22 bits).  In fp16 each is brought near 2^14 by a
+// power of two before, so that nothing leaves that type's range.
+//
+// A value that is no finite number would reach earlier rows of its chunk as its
+// product with a weight of zero: such a chunk is taken token by token.
+#include "linear.hpp"
+
+namespace tpl {
+namespace linear {
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+// 4 numbers of a column: of 16 lanes each 4 name a row's 16 columns, and lane l
+// of them gets column l of the 4 rows.
+__device__ __forceinline__ u32x2 read_column(const uint16_t* p) {
+    const s16x4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)p);
+    return __builtin_bit_cast(u32x2, v);
+}
+
+__device__ __forceinline__ float max_swap32(float x) {
+    const uint32_t u = __builtin_bit_cast(uint32_t, x);
+    const u32x2 r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    const uint32_t a = r[0], b = r[1];
+    return fmaxf(__builtin_bit_cast(float, a), __builtin_bit_cast(float, b));
+}
+__device__ __forceinline__ float max_wave(float x) {
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor(x, d));
+    return max_swap32(x);
+}
+
+// The power of two that brings a largest magnitude to 2^14 .. 2^15 (of small
+// ones as near as an fp32 number's exponent allows), and its reciprocal.
+struct Scale {
+    float up, down;
+};
+__device__ __forceinline__ Scale scale_of(float most) {
+    int e = (int)(__builtin_bit_cast(uint32_t, most) >> 23 & 255);   // 127 + its exponent
+    e = e < 40 ? 40 : e > 254 ? 254 : e;
+    return Scale{__builtin_bit_cast(float, (uint32_t)(127 + 127 + 14 - e) << 23), __builtin_bit_cast(float, (uint32_t)(e - 14) << 23)};
+}
+
+// Two numbers as the sum of two 16-bit ones each.
+template <typename T>
+__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
+    hi = pack2<T>(a, b);
+    lo = pack2<T>(a - lo16<T>(hi), b - hi16<T>(hi));
+}
+
+// The sequence that segment x belongs to (see seq_of_tile of kv.hpp).
+struct At {
+    int b;
+    Rows s;
+};
+__device__ __forceinline__ At seq_of_segment(const LinearArgs& p, int x) {
+    const int lane = threadIdx.x & 63;
+    At t = {-1, {0, 0}};
+    for (int b0 = 0; b0 < p.g.batch; b0 += 64) {
+        const int bb = b0 + lane < p.g.batch ? b0 + lane : p.g.batch - 1;
+        const Rows s = rows_of(p.g, bb);
+        const uint64_t m = __ballot(b0 + lane < p.g.batch && s.n > 0 && s.row0 / p.segment + bb <= x);
+        if (m) {
+            const int from = 63 - __builtin_clzll(m);
+            t.b = b0 + from;
+            t.s.row0 = __builtin_amdgcn_readlane(s.row0, from);
+            t.s.n = __builtin_amdgcn_readlane(s.n, from);
+        }
+    }
+    return t;
+}
+
+template <typename T, int NK, int WAVES, int MODE>
+__global__ void __launch_bounds__(WAVES * 64, NK <= 4 ? 2 : 1) k_chunk(LinearArgs p) {
+    typedef typename T::one one;
+    typedef typename T::x8 x8;
+    constexpr bool kScaled = std::is_same<T, kv::Fp16>::value;
+    constexpr int THREADS = WAVES * 64, DK = NK * 32, VC = WAVES * 32;
+    // Rows padded by 16 bytes: 32 rows' pieces at one place reach all banks.
+    constexpr int QP = DK + 8, VP = VC + 8;
+    constexpr int QUERIES = MODE == kState ? 0 : kChunk * QP, BLOCKS = MODE == kState ? 0 : 3;
+    __shared__ __attribute__((aligned(16))) uint16_t lds[QUERIES + kChunk * QP + kChunk * VP];
+    __shared__ u32x4 pbuf[BLOCKS + 1][2][2][64];   // block, part, product, lane
+    __shared__ float pdown[BLOCKS + 1][64];
+    __shared__ __attribute__((aligned(16))) float weight[kChunk];   // l^(n-1-j)
+    __shared__ int bad;
+    uint16_t *qs = lds, *ks = lds + QUERIES, *vs = ks + kChunk * QP;
+
+    const int tid = threadIdx.x, lane = tid & 63, r = lane & 31, hh = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int sl = blockIdx.x % p.slices, rest = blockIdx.x / p.slices, h = rest % p.p.heads, unit = rest / p.p.heads;
+    int b, row0, n;
+    if constexpr (MODE == kWhole) {
+        const Rows s = rows_of(p.g, unit);
+        b = unit, row0 = s.row0, n = s.n;
+        if (n == 0 || n <= p.few) return;
+    } else {
+        const At t = seq_of_segment(p, unit);
+        if (t.b < 0 || t.s.n <= p.few) return;
+        const int t0 = (unit - t.s.row0 / p.segment - t.b) * p.segment;
+        if (t0 < 0 || t0 >= t.s.n) return;
+        b = t.b, row0 = t.s.row0 + t0, n = t.s.n - t0 < p.segment ? t.s.n - t0 : p.segment;
+    }
+    const float g2 = decay_of(p, h);
+    const int kh = h / p.share;
+    const int dv0 = sl * VC;   // the workgroup's value channels; this wave's: 32 from dv0 + wave * 32 on
+    const int dvw = dv0 + wave * 32;
+    const bool active = dvw < p.p.value_dim;
+    const one* gq = (const one*)p.a.q + (int64_t)row0 * p.a.q_token + kh * p.a.q_head;
+    const one* gk = (const one*)p.a.k + (int64_t)row0 * p.a.k_token + kh * p.a.k_head;
+    const one* gv = (const one*)p.a.v + (int64_t)row0 * p.a.v_token + h * p.a.v_head + dv0;
+    one* go = (one*)p.a.out + (int64_t)row0 * p.a.o_token + h * p.a.o_head;
+
+    // The state: register i of block kb is key channel kb * 32 + 8 (i / 4) + 4 hh + i % 4 of value channel dvw + r.
+    f32x16 S[NK];
+    const float* from = nullptr;
+    int64_t s_key = p.p.value_dim;
+    float* mine = p.parts + ((int64_t)unit * p.p.heads + h) * p.p.key_dim * p.p.value_dim;
+    if constexpr (MODE == kWhole) from = source_of(p, b, h), s_key = p.p.s_key;
+    if constexpr (MODE == kOutput) from = mine;
+#pragma unroll
+    for (int kb = 0; kb < NK; ++kb)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int ch = kb * 32 + (i >> 2) * 8 + hh * 4 + (i & 3);
+            S[kb][i] = 0.0f;
+            if (MODE != kState && from && ch < p.p.key_dim && dvw + r < p.p.value_dim) S[kb][i] = from[ch * s_key + dvw + r];
+        }
+
+    constexpr int KPR = DK / 8, KN = (kChunk * KPR + THREADS - 1) / THREADS;   // pieces of 8 channels: of a row, of a thread
+    constexpr int VPR = VC / 8, VN = (kChunk * VPR + THREADS - 1) / THREADS;
+    u32x4 qreg[MODE == kState ? 1 : KN], kreg[KN], vreg[VN];
+    auto fetch = [&](int t, int count) {   // zeros beyond the chunk's tokens and the head's channels
+#pragma unroll
+        for (int i = 0; i < KN; ++i) {
+            const int id = i * THREADS + tid, tok = id / KPR, ch = (id - tok * KPR) * 8;
+            const bool there = tok < count && ch < p.p.key_dim;
+            kreg[i] = u32x4{0, 0, 0, 0};
+            if (there) kreg[i] = *reinterpret_cast<const u32x4*>(gk + (t + tok) * p.a.k_token + ch);
+            if constexpr (MODE != kState) {
+                qreg[i] = u32x4{0, 0, 0, 0};
+                if (there) qreg[i] = *reinterpret_cast<const u32x4*>(gq + (t + tok) * p.a.q_token + ch);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < VN; ++i) {
+            const int id = i * THREADS + tid, tok = id / VPR, ch = (id - tok * VPR) * 8;
+            vreg[i] = u32x4{0, 0, 0, 0};
+            if (tok < count && dv0 + ch < p.p.value_dim) vreg[i] = *reinterpret_cast<const u32x4*>(gv + (t + tok) * p.a.v_token + ch);
+        }
+    };
+    auto put = [&](int count) {
+        bool some = false;
+#pragma unroll
+        for (int i = 0; i < KN; ++i) {
+            const int id = i * THREADS + tid, tok = id / KPR, ch = (id - tok * KPR) * 8;
+            if (KN * THREADS == kChunk * KPR || id < kChunk * KPR) {
+                *reinterpret_cast<u32x4*>(ks + tok * QP + ch) = kreg[i];
+                if constexpr (MODE != kState) *reinterpret_cast<u32x4*>(qs + tok * QP + ch) = qreg[i];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < VN; ++i) {
+            const int id = i * THREADS + tid, tok = id / VPR, ch = (id - tok * VPR) * 8;
+            if (VN * THREADS == kChunk * VPR || id < kChunk * VPR) {
+                if constexpr (MODE != kState) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        uint32_t w = vreg[i][e];
+                        some |= kv::clear_bad<T>(w);
+                    }
+                }
+                *reinterpret_cast<u32x4*>(vs + tok * VP + ch) = vreg[i];
+            }
+        }
+        if (some && count > 1) bad = 1;
+        if (tid < kChunk) weight[tid] = tid < count ? exp2_(g2 * (float)(count - 1 - tid)) : 0.0f;
+    };
+
+    if (tid == 0) bad = 0;
+    __syncthreads();
+    int t = 0, count = n < kChunk ? n : kChunk, single = 0;   // tokens before `single` are taken one by one
+    fetch(0, count);
+    while (t < n) {
+        put(count);
+        __syncthreads();
+        if (MODE != kState && bad && count > 1) {
+            __syncthreads();
+            if (tid == 0) bad = 0;
+            single = t + count;
+            count = 1;
+            fetch(t, 1);
+            __syncthreads();
+            continue;
+        }
+        const int here = t, now = count;
+        t += count;
+        count = t < single ? 1 : n - t < kChunk ? n - t : kChunk;
+        if (t < n) fetch(t, count);
+
+        f32x16 o[2];
+        if constexpr (MODE != kState) {
+            // P^T's blocks: rows of j = 0 and columns of i = 0, of j = 0 and i = 1, of j = 1 and i = 1.
+#pragma unroll 1
+            for (int blk = wave; blk < 3; blk += WAVES) {
+                const int jb = blk >> 1, ib = (blk + 1) >> 1;
+                f32x16 x;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) x[i] = 0.0f;
+#pragma unroll
+                for (int s = 0; s < NK * 2; ++s) {
+                    const u32x4 kw = *reinterpret_cast<const u32x4*>(ks + (jb * 32 + r) * QP + s * 16 + hh * 8);
+                    const u32x4 qw = *reinterpret_cast<const u32x4*>(qs + (ib * 32 + r) * QP + s * 16 + hh * 8);
+                    x = T::mfma32(__builtin_bit_cast(x8, kw), __builtin_bit_cast(x8, qw), x);
+                }
+                const int d0 = (ib - jb) * 32 + r - hh * 4;   // i - j of register 0
+                float most = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int d = d0 - (i >> 2) * 8 - (i & 3);
+                    x[i] = d < 0 ? 0.0f : x[i] * exp2_(g2 * (float)d);
+                    if constexpr (kScaled) most = fmaxf(most, __builtin_fabsf(x[i]));
+                }
+                if constexpr (kScaled) {
+                    const Scale sc = scale_of(max_swap32(most));
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) x[i] *= sc.up;
+                    pdown[blk][lane] = sc.down;
+                }
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    u32x4 hi, lo;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t a, c;
+                        split2<T>(x[s * 8 + i * 2], x[s * 8 + i * 2 + 1], a, c);
+                        hi[i] = a, lo[i] = c;
+                    }
+                    pbuf[blk][0][s][lane] = hi;
+                    pbuf[blk][1][s][lane] = lo;
+                }
+            }
+            // What the state before the chunk gives.
+#pragma unroll
+            for (int ib = 0; ib < 2; ++ib)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[ib][i] = 0.0f;
+            Scale sc = {1.0f, 1.0f};
+            if constexpr (kScaled) {
+                float most = 0.0f;
+#pragma unroll
+                for (int kb = 0; kb < NK; ++kb)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) most = fmaxf(most, __builtin_fabsf(S[kb][i]));
+                most = max_wave(most);
+                if (!(most < __builtin_inff())) {   // an infinity says nothing of the other channels
+                    most = 0.0f;
+#pragma unroll
+                    for (int kb = 0; kb < NK; ++kb)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const float x = __builtin_fabsf(S[kb][i]);
+                            most = x < __builtin_inff() ? fmaxf(most, x) : most;
+                        }
+                    most = max_wave(most);
+                }
+                sc = scale_of(most);
+            }
+#pragma unroll
+            for (int kb = 0; kb < NK; ++kb)
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    u32x4 hi, lo;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t a, c;
+                        split2<T>(S[kb][s * 8 + i * 2] * sc.up, S[kb][s * 8 + i * 2 + 1] * sc.up, a, c);
+                        hi[i] = a, lo[i] = c;
+                    }
+#pragma unroll
+                    for (int ib = 0; ib < 2; ++ib) {
+                        const uint16_t* q = qs + (ib * 32 + r) * QP + kb * 32 + s * 16 + hh * 4;
+                        const u32x2 q0 = *reinterpret_cast<const u32x2*>(q), q1 = *reinterpret_cast<const u32x2*>(q + 8);
+                        const x8 qw = __builtin_bit_cast(x8, (u32x4{q0[0], q0[1], q1[0], q1[1]}));
+                        o[ib] = T::mfma32(__builtin_bit_cast(x8, hi), qw, o[ib]);
+                        o[ib] = T::mfma32(__builtin_bit_cast(x8, lo), qw, o[ib]);
+                    }
+                }
+#pragma unroll
+            for (int ib = 0; ib < 2; ++ib) {
+                const float f = exp2_(g2 * (float)(ib * 32 + r + 1)) * sc.down;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[ib][i] *= f;
+            }
+            __syncthreads();   // P is there
+        }
+
+        // Values, transposed: of 16 tokens those at 4 hh .. + 3 and 8 + 4 hh .. + 3.
+        const int trow = hh * 4 + ((lane & 15) >> 2), tcol = (lane >> 4 & 1) * 16 + (lane & 3) * 4;
+        u32x4 vt[4];
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+            const u32x2 a = read_column(vs + (z * 16 + trow) * VP + wave * 32 + tcol);
+            const u32x2 c = read_column(vs + (z * 16 + 8 + trow) * VP + wave * 32 + tcol);
+            vt[z] = u32x4{a[0], a[1], c[0], c[1]};
+        }
+        if constexpr (MODE != kState) {
+#pragma unroll
+            for (int blk = 0; blk < 3; ++blk) {
+                const int jb = blk >> 1, ib = (blk + 1) >> 1;
+                f32x16 x;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) x[i] = kScaled ? 0.0f : o[ib][i];
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+#pragma unroll
+                    for (int part = 0; part < 2; ++part)
+                        x = T::mfma32(__builtin_bit_cast(x8, vt[jb * 2 + s]), __builtin_bit_cast(x8, pbuf[blk][part][s][lane]), x);
+                const float down = kScaled ? pdown[blk][lane] : 1.0f;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[ib][i] = kScaled ? o[ib][i] + x[i] * down : x[i];
+            }
+#pragma unroll
+            for (int ib = 0; ib < 2; ++ib) {
+                const int tok = ib * 32 + r;
+                if (tok >= now || !active) continue;
+                one* to = go + (here + tok) * p.a.o_token + dvw + hh * 4;
+#pragma unroll
+                for (int a = 0; a < 4; ++a)
+                    if (dvw + a * 8 < p.p.value_dim)
+                        *reinterpret_cast<u32x2*>(to + a * 8) =
+                            u32x2{pack2<T>(o[ib][a * 4] * p.a.scale, o[ib][a * 4 + 1] * p.a.scale),
+                                  pack2<T>(o[ib][a * 4 + 2] * p.a.scale, o[ib][a * 4 + 3] * p.a.scale)};
+            }
+        }
+
+        if (MODE != kOutput || t < n) {
+            const float keep = exp2_(g2 * (float)now);
+            u32x4 hi[4], lo[4];
+            float w[4][8], most = 0.0f;
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+                const f32x4 a = *reinterpret_cast<const f32x4*>(weight + z * 16 + hh * 4);
+                const f32x4 c = *reinterpret_cast<const f32x4*>(weight + z * 16 + 8 + hh * 4);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float f0 = i < 2 ? a[i * 2] : c[i * 2 - 4], f1 = i < 2 ? a[i * 2 + 1] : c[i * 2 - 3];
+                    w[z][i * 2] = lo16<T>(vt[z][i]) * f0;
+                    w[z][i * 2 + 1] = hi16<T>(vt[z][i]) * f1;
+                    if constexpr (kScaled) most = fmaxf(most, fmaxf(__builtin_fabsf(w[z][i * 2]), __builtin_fabsf(w[z][i * 2 + 1])));
+                }
+            }
+            Scale sc = {1.0f, 1.0f};
+            if constexpr (kScaled) sc = scale_of(max_swap32(most));
+#pragma unroll
+            for (int z = 0; z < 4; ++z)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t a, c;
+                    split2<T>(w[z][i * 2] * sc.up, w[z][i * 2 + 1] * sc.up, a, c);
+                    hi[z][i] = a, lo[z][i] = c;
+                }
+#pragma unroll
+            for (int kb = 0; kb < NK; ++kb) {
+                f32x16 x;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) x[i] = kScaled ? 0.0f : S[kb][i] * keep;
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {
+                    const u32x2 a = read_column(ks + (z * 16 + trow) * QP + kb * 32 + tcol);
+                    const u32x2 c = read_column(ks + (z * 16 + 8 + trow) * QP + kb * 32 + tcol);
+                    const x8 kt = __builtin_bit_cast(x8, (u32x4{a[0], a[1], c[0], c[1]}));
+                    x = T::mfma32(kt, __builtin_bit_cast(x8, hi[z]), x);
+                    x = T::mfma32(kt, __builtin_bit_cast(x8, lo[z]), x);
+                }
+#pragma unroll
+                for (int i = 0; i < 16; ++i) S[kb][i] = kScaled ? __builtin_fmaf(x[i], sc.down, S[kb][i] * keep) : x[i];
+            }
+        }
+        __syncthreads();   // the chunk's LDS is free
+    }
+
+    float* to = nullptr;
+    if constexpr (MODE == kWhole) to = state_at(p, p.g.slots[b], h);
+    if constexpr (MODE == kState) to = mine;
+    if (to && dvw + r < p.p.value_dim)
+#pragma unroll
+        for (int kb = 0; kb < NK; ++kb)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int ch = kb * 32 + (i >> 2) * 8 + hh * 4 + (i & 3);
+                if (ch < p.p.key_dim) to[ch * s_key + dvw + r] = S[kb][i];
+            }
+}
+
+// From what each segment adds to what stands before it, and the sequence's
+// last state.
+__global__ void __launch_bounds__(256) k_scan(LinearArgs p) {
+    const int h = blockIdx.x % p.p.heads, b = blockIdx.x / p.p.heads;
+    const Rows s = rows_of(p.g, b);
+    if (s.n == 0 || s.n <= p.few) return;
+    const int quads = p.p.value_dim / 4, i = blockIdx.y * 256 + threadIdx.x;
+    const int key = i / quads, c = (i - key * quads) * 4;
+    if (key >= p.p.key_dim) return;
+    const float g2 = decay_of(p, h);
+    const int64_t state = (int64_t)p.p.key_dim * p.p.value_dim, next = state * p.p.heads;
+    float* at = p.parts + (int64_t)(s.row0 / p.segment + b) * next + h * state + key * p.p.value_dim + c;
+    const float* from = source_of(p, b, h);
+    f32x4 x = {0, 0, 0, 0};
+    if (from) x = *reinterpret_cast<const f32x4*>(from + key * p.p.s_key + c);
+    const int count = (s.n + p.segment - 1) / p.segment;
+    const float keep = exp2_(g2 * (float)p.segment);
+    constexpr int AHEAD = 4;   // segments' parts under way
+    f32x4 y[AHEAD];
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) y[k] = k < count ? *reinterpret_cast<const f32x4*>(at + k * next) : f32x4{0, 0, 0, 0};
+    for (int k0 = 0; k0 < count; k0 += AHEAD)
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) {
+            const int seg = k0 + k;
+            if (seg >= count) break;
+            const f32x4 added = y[k];
+            if (seg + AHEAD < count) y[k] = *reinterpret_cast<const f32x4*>(at + (seg + AHEAD) * next);
+            *reinterpret_cast<f32x4*>(at + seg * next) = x;
+            const float f = seg + 1 < count ? keep : exp2_(g2 * (float)(s.n - seg * p.segment));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = __builtin_fmaf(x[e], f, added[e]);
+        }
+    float* to = state_at(p, p.g.slots[b], h);
+    if (to) *reinterpret_cast<f32x4*>(to + key * p.p.s_key + c) = x;
+}
+
+// Waves of a workgroup: a head's value channels by 32, at most 4, evenly.
+static int waves_of(int value_dim) {
+    const int blocks = (value_dim + 31) / 32, slices = (blocks + 3) / 4, w = (blocks + slices - 1) / slices;
+    return w < 2 ? 2 : w;
+}
+int chunk_slices(int value_dim) {
+    const int w = waves_of(value_dim) * 32;
+    return (value_dim + w - 1) / w;
+}
+
+template <typename T, int NK, int WAVES>
+static hipError_t go_mode(const LinearArgs& p, int mode, unsigned grid, hipStream_t st) {
+    if (mode == kWhole)
+        k_chunk<T, NK, WAVES, kWhole><<<grid, WAVES * 64, 0, st>>>(p);
+    else if (mode == kState)
+        k_chunk<T, NK, WAVES, kState><<<grid, WAVES * 64, 0, st>>>(p);
+    else
+        k_chunk<T, NK, WAVES, kOutput><<<grid, WAVES * 64, 0, st>>>(p);
+    return hipGetLastError();
+}
+
+template <typename T, int NK>
+static hipError_t go_waves(const LinearArgs& p, int mode, unsigned grid, hipStream_t st) {
+    switch (waves_of(p.p.value_dim)) {
+    case 2: return go_mode<T, NK, 2>(p, mode, grid, st);
+    case 3: return go_mode<T, NK, 3>(p, mode, grid, st);
+    default: return go_mode<T, NK, 4>(p, mode, grid, st);
+    }
+}
+
+template <typename T>
+static hipError_t go_keys(const LinearArgs& p, int mode, unsigned grid, hipStream_t st) {
+    const int d = p.p.key_dim;
+    if (d <= 32) return go_waves<T, 1>(p, mode, grid, st);
+    if (d <= 64) return go_waves<T, 2>(p, mode, grid, st);
+    if (d <= 96) return go_waves<T, 3>(p, mode, grid, st);
+    if (d <= 128) return go_waves<T, 4>(p, mode, grid, st);
+    if (d <= 192) return go_waves<T, 6>(p, mode, grid, st);
+    return go_waves<T, 8>(p, mode, grid, st);
+}
+
+hipError_t launch_chunk(const LinearArgs& p, int mode, int64_t units, hipStream_t st) {
+    const unsigned grid = (unsigned)(units * p.p.heads * p.slices);
+    return p.a.type == TPL_KV_BF16 ? go_keys<kv::Bf16>(p, mode, grid, st) : go_keys<kv::Fp16>(p, mode, grid, st);
+}
+
+hipError_t launch_scan(const LinearArgs& p, hipStream_t st) {
+    const int64_t n = (int64_t)p.p.key_dim * (p.p.value_dim / 4);
+    k_scan<<<dim3((unsigned)(p.g.batch * p.p.heads), (unsigned)((n + 255) / 256)), 256, 0, st>>>(p);
+    return hipGetLastError();
+}
+
+}  // namespace linear
+}  // namespace tpl
