@@ -32,7 +32,8 @@ extern "C" {
 #endif
 
 /* Strides are in elements; a state's value channels and a head's channels are
- * contiguous.  Every base and stride lies on 16 bytes. */
+ * contiguous.  Every base and stride lies on 16 bytes; rows of q, k and v lie
+ * under 2^24 elements apart. */
 typedef struct {
     float *state;              /* [slots, heads, key_dim, value_dim] */
     const float *decay;        /* [heads]: logarithms; what is over zero counts as zero */

@@ -28,6 +28,8 @@ FLAGS = [
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-I", os.path.join(ROOT, "include"),
 ]
+# An early pass makes one vector of a state's or an output's two blocks, which then goes through scratch memory (8 times the time).
+MORE_FLAGS = {"linear_chunk.hip": ["-mllvm", "-disable-promote-alloca-to-vector"]}
 
 
 def _run(cmd, verbose):
@@ -77,7 +79,7 @@ def build(verbose: bool = False) -> str:
         objs = [os.path.join(objdir, s + ".o") for s in SOURCES]
         calltmp = CALL + ".tmp"
         jobs = [_call_command(calltmp)]
-        jobs += [[HIPCC] + compile_flags + ["-c", os.path.join(CSRC, s), "-o", o] for s, o in zip(SOURCES, objs)]
+        jobs += [[HIPCC] + compile_flags + MORE_FLAGS.get(s, []) + ["-c", os.path.join(CSRC, s), "-o", o] for s, o in zip(SOURCES, objs)]
         workers = max(1, min(len(jobs), os.cpu_count() or 1, 16))
         with cf.ThreadPoolExecutor(max_workers=workers) as ex:
             for f in [ex.submit(_run, j, verbose) for j in jobs]:

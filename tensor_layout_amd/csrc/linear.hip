@@ -103,6 +103,9 @@ static int attend_impl(const tpl_linear_pool* c, const tpl_linear_batch* g, cons
     if (!lies16(a->q, a->q_token, a->q_head, 2) || !lies16(a->k, a->k_token, a->k_head, 2) || !lies16(a->v, a->v_token, a->v_head, 2) ||
         !lies16(a->out, a->o_token, a->o_head, 2))
         return fail_status(TPL_E_LAYOUT, "q, k, v and out must start, and their rows and heads lie, on 16 bytes");
+    // A chunk's rows have 32-bit offsets in the kernels.
+    for (int64_t x : {a->q_token, a->k_token, a->v_token})
+        if (x < 0 || x > (INT_MAX >> 7)) return fail_status(TPL_E_LAYOUT, "rows of q, k and v must lie under 2^24 elements apart");
     if (q.bytes > 0 && (!ws || ((uintptr_t)ws & 15))) return fail_status(TPL_E_ARG, "workspace must lie on 16 bytes");
     if (ws_bytes < q.bytes) return fail_status(TPL_E_ARG, "workspace is too small");
     p.parts = (float*)ws;

@@ -24,7 +24,8 @@
 // for all waves, a block of 32x32 each, and handed over in LDS as operands.
 //
 // Roundings: P, S and w V are fp32 numbers and go into the products as the sum
-// of two 16-bit ones (16 or 22 bits).  In fp16 each is brought near 2^14 by a
+// of two 16-bit ones (16 or 22 bits), bf16's w V of three (24): outputs are
+// rounded to 8 or 11 bits, but states stay.  In fp16 each is brought near 2^14 by a
 // power of two before, so that nothing leaves that type's range.
 //
 // A value that is no finite number would reach earlier rows of its chunk as its
@@ -55,15 +56,20 @@ __device__ __forceinline__ float max_wave(float x) {
     return max_swap32(x);
 }
 
-// The power of two that brings a largest magnitude to 2^14 .. 2^15 (of small
-// ones as near as an fp32 number's exponent allows), and its reciprocal.
+// The power of two that brings a largest magnitude to 2^14 .. 2^15 (one under
+// 2^-27 not that far: sums that are multiplied by it beside have to stay in
+// range), and its reciprocal.
 struct Scale {
     float up, down;
 };
+__device__ __forceinline__ float inverse2(float x) {   // of a power of two
+    return __builtin_bit_cast(float, (254u << 23) - __builtin_bit_cast(uint32_t, x));
+}
 __device__ __forceinline__ Scale scale_of(float most) {
     int e = (int)(__builtin_bit_cast(uint32_t, most) >> 23 & 255);   // 127 + its exponent
-    e = e < 40 ? 40 : e > 254 ? 254 : e;
-    return Scale{__builtin_bit_cast(float, (uint32_t)(127 + 127 + 14 - e) << 23), __builtin_bit_cast(float, (uint32_t)(e - 14) << 23)};
+    e = e < 100 ? 100 : e > 254 ? 254 : e;
+    const float down = __builtin_bit_cast(float, (uint32_t)(e - 14) << 23);
+    return Scale{inverse2(down), down};
 }
 
 // Two numbers as the sum of two 16-bit ones each.
@@ -152,51 +158,53 @@ __global__ void __launch_bounds__(WAVES * 64, NK <= 4 ? 2 : 1) k_chunk(LinearArg
             if (MODE != kState && from && ch < p.p.key_dim && dvw + r < p.p.value_dim) S[kb][i] = from[ch * s_key + dvw + r];
         }
 
-    constexpr int KPR = DK / 8, KN = (kChunk * KPR + THREADS - 1) / THREADS;   // pieces of 8 channels: of a row, of a thread
-    constexpr int VPR = VC / 8, VN = (kChunk * VPR + THREADS - 1) / THREADS;
+    // What a thread brings: pieces of 8 channels, always the same ones, of every
+    // KR-th (VR-th) token; threads that do not fill a row more bring none.
+    constexpr int KPR = DK / 8, KR = THREADS / KPR, KN = (kChunk + KR - 1) / KR;
+    constexpr int VPR = VC / 8, VR = THREADS / VPR, VN = (kChunk + VR - 1) / VR;
+    const int ktok = tid / KPR, kch = (tid - ktok * KPR) * 8, vtok = tid / VPR, vch = (tid - vtok * VPR) * 8;
+    const bool kput = ktok < KR, vput = vtok < VR;   // it has a place in LDS
+    const bool kmine = kput && kch < p.p.key_dim, vmine = vput && dv0 + vch < p.p.value_dim;
+    // The host keeps 64 rows within 2^31 bytes.
+    const uint32_t qoff = ((uint32_t)ktok * (uint32_t)p.a.q_token + kch) * 2, koff = ((uint32_t)ktok * (uint32_t)p.a.k_token + kch) * 2;
+    const uint32_t voff = ((uint32_t)vtok * (uint32_t)p.a.v_token + vch) * 2;
     u32x4 qreg[MODE == kState ? 1 : KN], kreg[KN], vreg[VN];
     auto fetch = [&](int t, int count) {   // zeros beyond the chunk's tokens and the head's channels
+        const char *bq = (const char*)(gq + t * p.a.q_token), *bk = (const char*)(gk + t * p.a.k_token), *bv = (const char*)(gv + t * p.a.v_token);
 #pragma unroll
         for (int i = 0; i < KN; ++i) {
-            const int id = i * THREADS + tid, tok = id / KPR, ch = (id - tok * KPR) * 8;
-            const bool there = tok < count && ch < p.p.key_dim;
+            const bool there = kmine && ktok + i * KR < count;
             kreg[i] = u32x4{0, 0, 0, 0};
-            if (there) kreg[i] = *reinterpret_cast<const u32x4*>(gk + (t + tok) * p.a.k_token + ch);
+            if (there) kreg[i] = *reinterpret_cast<const u32x4*>(bk + i * KR * p.a.k_token * 2 + koff);
             if constexpr (MODE != kState) {
                 qreg[i] = u32x4{0, 0, 0, 0};
-                if (there) qreg[i] = *reinterpret_cast<const u32x4*>(gq + (t + tok) * p.a.q_token + ch);
+                if (there) qreg[i] = *reinterpret_cast<const u32x4*>(bq + i * KR * p.a.q_token * 2 + qoff);
             }
         }
 #pragma unroll
         for (int i = 0; i < VN; ++i) {
-            const int id = i * THREADS + tid, tok = id / VPR, ch = (id - tok * VPR) * 8;
             vreg[i] = u32x4{0, 0, 0, 0};
-            if (tok < count && dv0 + ch < p.p.value_dim) vreg[i] = *reinterpret_cast<const u32x4*>(gv + (t + tok) * p.a.v_token + ch);
+            if (vmine && vtok + i * VR < count) vreg[i] = *reinterpret_cast<const u32x4*>(bv + i * VR * p.a.v_token * 2 + voff);
         }
     };
     auto put = [&](int count) {
         bool some = false;
 #pragma unroll
-        for (int i = 0; i < KN; ++i) {
-            const int id = i * THREADS + tid, tok = id / KPR, ch = (id - tok * KPR) * 8;
-            if (KN * THREADS == kChunk * KPR || id < kChunk * KPR) {
-                *reinterpret_cast<u32x4*>(ks + tok * QP + ch) = kreg[i];
-                if constexpr (MODE != kState) *reinterpret_cast<u32x4*>(qs + tok * QP + ch) = qreg[i];
+        for (int i = 0; i < KN; ++i)
+            if (kput && (KR * KN == kChunk || ktok + i * KR < kChunk)) {
+                *reinterpret_cast<u32x4*>(ks + (ktok + i * KR) * QP + kch) = kreg[i];
+                if constexpr (MODE != kState) *reinterpret_cast<u32x4*>(qs + (ktok + i * KR) * QP + kch) = qreg[i];
             }
-        }
 #pragma unroll
         for (int i = 0; i < VN; ++i) {
-            const int id = i * THREADS + tid, tok = id / VPR, ch = (id - tok * VPR) * 8;
-            if (VN * THREADS == kChunk * VPR || id < kChunk * VPR) {
-                if constexpr (MODE != kState) {
+            if constexpr (MODE != kState) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        uint32_t w = vreg[i][e];
-                        some |= kv::clear_bad<T>(w);
-                    }
+                for (int e = 0; e < 4; ++e) {
+                    uint32_t w = vreg[i][e];
+                    some |= kv::clear_bad<T>(w);
                 }
-                *reinterpret_cast<u32x4*>(vs + tok * VP + ch) = vreg[i];
             }
+            if (vput && (VR * VN == kChunk || vtok + i * VR < kChunk)) *reinterpret_cast<u32x4*>(vs + (vtok + i * VR) * VP + vch) = vreg[i];
         }
         if (some && count > 1) bad = 1;
         if (tid < kChunk) weight[tid] = tid < count ? exp2_(g2 * (float)(count - 1 - tid)) : 0.0f;
@@ -274,22 +282,15 @@ __global__ void __launch_bounds__(WAVES * 64, NK <= 4 ? 2 : 1) k_chunk(LinearArg
             if constexpr (kScaled) {
                 float most = 0.0f;
 #pragma unroll
-                for (int kb = 0; kb < NK; ++kb)
+                for (int kb = 0; kb < NK; ++kb) {
+                    const f32x16 y = S[kb];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) most = fmaxf(most, __builtin_fabsf(S[kb][i]));
-                most = max_wave(most);
-                if (!(most < __builtin_inff())) {   // an infinity says nothing of the other channels
-                    most = 0.0f;
-#pragma unroll
-                    for (int kb = 0; kb < NK; ++kb)
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const float x = __builtin_fabsf(S[kb][i]);
-                            most = x < __builtin_inff() ? fmaxf(most, x) : most;
-                        }
-                    most = max_wave(most);
+                    for (int i = 0; i < 16; ++i) {
+                        const float x = __builtin_fabsf(y[i]);   // an infinity says nothing of the other channels
+                        most = fmaxf(most, x < __builtin_inff() ? x : 0.0f);
+                    }
                 }
-                sc = scale_of(most);
+                sc = scale_of(max_wave(most));
             }
 #pragma unroll
             for (int kb = 0; kb < NK; ++kb)
@@ -322,28 +323,32 @@ __global__ void __launch_bounds__(WAVES * 64, NK <= 4 ? 2 : 1) k_chunk(LinearArg
 
         // Values, transposed: of 16 tokens those at 4 hh .. + 3 and 8 + 4 hh .. + 3.
         const int trow = hh * 4 + ((lane & 15) >> 2), tcol = (lane >> 4 & 1) * 16 + (lane & 3) * 4;
-        u32x4 vt[4];
-#pragma unroll
-        for (int z = 0; z < 4; ++z) {
-            const u32x2 a = read_column(vs + (z * 16 + trow) * VP + wave * 32 + tcol);
-            const u32x2 c = read_column(vs + (z * 16 + 8 + trow) * VP + wave * 32 + tcol);
-            vt[z] = u32x4{a[0], a[1], c[0], c[1]};
-        }
+        auto column16 = [&](const uint16_t* base, int pitch, int z) {
+            const u32x2 a = read_column(base + (z * 16 + trow) * pitch + tcol), c = read_column(base + (z * 16 + 8 + trow) * pitch + tcol);
+            return u32x4{a[0], a[1], c[0], c[1]};
+        };
         if constexpr (MODE != kState) {
+            // A block of P^T with its 32 tokens' values, on top of what is there.
+            u32x4 vt[2];
 #pragma unroll
             for (int blk = 0; blk < 3; ++blk) {
                 const int jb = blk >> 1, ib = (blk + 1) >> 1;
-                f32x16 x;
+                if (blk != 1) vt[0] = column16(vs + wave * 32, VP, jb * 2), vt[1] = column16(vs + wave * 32, VP, jb * 2 + 1);
+                if constexpr (kScaled) {
+                    const float up = inverse2(pdown[blk][lane]);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) x[i] = kScaled ? 0.0f : o[ib][i];
+                    for (int i = 0; i < 16; ++i) o[ib][i] *= up;
+                }
 #pragma unroll
                 for (int s = 0; s < 2; ++s)
 #pragma unroll
                     for (int part = 0; part < 2; ++part)
-                        x = T::mfma32(__builtin_bit_cast(x8, vt[jb * 2 + s]), __builtin_bit_cast(x8, pbuf[blk][part][s][lane]), x);
-                const float down = kScaled ? pdown[blk][lane] : 1.0f;
+                        o[ib] = T::mfma32(__builtin_bit_cast(x8, vt[s]), __builtin_bit_cast(x8, pbuf[blk][part][s][lane]), o[ib]);
+                if constexpr (kScaled) {
+                    const float down = pdown[blk][lane];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) o[ib][i] = kScaled ? o[ib][i] + x[i] * down : x[i];
+                    for (int i = 0; i < 16; ++i) o[ib][i] *= down;
+                }
             }
 #pragma unroll
             for (int ib = 0; ib < 2; ++ib) {
@@ -361,60 +366,82 @@ __global__ void __launch_bounds__(WAVES * 64, NK <= 4 ? 2 : 1) k_chunk(LinearArg
 
         if (MODE != kOutput || t < n) {
             const float keep = exp2_(g2 * (float)now);
-            u32x4 hi[4], lo[4];
-            float w[4][8], most = 0.0f;
-#pragma unroll
-            for (int z = 0; z < 4; ++z) {
+            // The weighted values of 16 tokens.
+            auto weighted = [&](int z, float (&w)[8]) {
+                const u32x4 v = column16(vs + wave * 32, VP, z);
                 const f32x4 a = *reinterpret_cast<const f32x4*>(weight + z * 16 + hh * 4);
                 const f32x4 c = *reinterpret_cast<const f32x4*>(weight + z * 16 + 8 + hh * 4);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float f0 = i < 2 ? a[i * 2] : c[i * 2 - 4], f1 = i < 2 ? a[i * 2 + 1] : c[i * 2 - 3];
-                    w[z][i * 2] = lo16<T>(vt[z][i]) * f0;
-                    w[z][i * 2 + 1] = hi16<T>(vt[z][i]) * f1;
-                    if constexpr (kScaled) most = fmaxf(most, fmaxf(__builtin_fabsf(w[z][i * 2]), __builtin_fabsf(w[z][i * 2 + 1])));
+                for (int i = 0; i < 2; ++i) {
+                    w[i * 2] = lo16<T>(v[i]) * a[i * 2], w[i * 2 + 1] = hi16<T>(v[i]) * a[i * 2 + 1];
+                    w[i * 2 + 4] = lo16<T>(v[i + 2]) * c[i * 2], w[i * 2 + 5] = hi16<T>(v[i + 2]) * c[i * 2 + 1];
                 }
-            }
+            };
             Scale sc = {1.0f, 1.0f};
-            if constexpr (kScaled) sc = scale_of(max_swap32(most));
-#pragma unroll
-            for (int z = 0; z < 4; ++z)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t a, c;
-                    split2<T>(w[z][i * 2] * sc.up, w[z][i * 2 + 1] * sc.up, a, c);
-                    hi[z][i] = a, lo[z][i] = c;
-                }
-#pragma unroll
-            for (int kb = 0; kb < NK; ++kb) {
-                f32x16 x;
-#pragma unroll
-                for (int i = 0; i < 16; ++i) x[i] = kScaled ? 0.0f : S[kb][i] * keep;
+            if constexpr (kScaled) {   // a value channel's own, as a column of the state has one lane pair
+                float most = 0.0f;
 #pragma unroll
                 for (int z = 0; z < 4; ++z) {
-                    const u32x2 a = read_column(ks + (z * 16 + trow) * QP + kb * 32 + tcol);
-                    const u32x2 c = read_column(ks + (z * 16 + 8 + trow) * QP + kb * 32 + tcol);
-                    const x8 kt = __builtin_bit_cast(x8, (u32x4{a[0], a[1], c[0], c[1]}));
-                    x = T::mfma32(kt, __builtin_bit_cast(x8, hi[z]), x);
-                    x = T::mfma32(kt, __builtin_bit_cast(x8, lo[z]), x);
+                    float w[8];
+                    weighted(z, w);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) most = fmaxf(most, __builtin_fabsf(w[i]));
+                }
+                sc = scale_of(max_swap32(most));
+            }
+            const float first = keep * sc.up;
+#pragma unroll
+            for (int kb = 0; kb < NK; ++kb)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) S[kb][i] *= first;
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+                float w[8];
+                weighted(z, w);
+                // In bf16 three parts: two would leave a state 2^-18 off.
+                constexpr int PARTS = kScaled ? 2 : 3;
+                u32x4 part[PARTS];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float a = w[i * 2] * sc.up, c = w[i * 2 + 1] * sc.up;
+#pragma unroll
+                    for (int k = 0; k < PARTS; ++k) {
+                        const uint32_t x = pack2<T>(a, c);
+                        part[k][i] = x;
+                        a -= lo16<T>(x), c -= hi16<T>(x);
+                    }
                 }
 #pragma unroll
-                for (int i = 0; i < 16; ++i) S[kb][i] = kScaled ? __builtin_fmaf(x[i], sc.down, S[kb][i] * keep) : x[i];
+                for (int kb = 0; kb < NK; ++kb) {
+                    const x8 kt = __builtin_bit_cast(x8, column16(ks + kb * 32, QP, z));
+#pragma unroll
+                    for (int k = 0; k < PARTS; ++k) S[kb] = T::mfma32(kt, __builtin_bit_cast(x8, part[k]), S[kb]);
+                }
+            }
+            if constexpr (kScaled) {
+#pragma unroll
+                for (int kb = 0; kb < NK; ++kb)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) S[kb][i] *= sc.down;
             }
         }
         __syncthreads();   // the chunk's LDS is free
     }
 
+    // The lane again, so that no address is held throughout.
+    int again = threadIdx.x;
+    asm volatile("" : "+v"(again));
+    const int dv = dvw + (again & 31), key0 = (again >> 5 & 1) * 4;
     float* to = nullptr;
     if constexpr (MODE == kWhole) to = state_at(p, p.g.slots[b], h);
     if constexpr (MODE == kState) to = mine;
-    if (to && dvw + r < p.p.value_dim)
+    if (to && dv < p.p.value_dim)
 #pragma unroll
         for (int kb = 0; kb < NK; ++kb)
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                const int ch = kb * 32 + (i >> 2) * 8 + hh * 4 + (i & 3);
-                if (ch < p.p.key_dim) to[ch * s_key + dvw + r] = S[kb][i];
+                const int ch = kb * 32 + (i >> 2) * 8 + key0 + (i & 3);
+                if (ch < p.p.key_dim) to[ch * s_key + dv] = S[kb][i];
             }
 }
 
