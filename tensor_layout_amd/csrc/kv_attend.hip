@@ -156,7 +156,7 @@ static const char* choose(const tpl_kv_cache* c, const tpl_kv_batch* g, const tp
     p.counters = nullptr;
     p.parts = p.tile_parts = nullptr;
     p.s = tpl_kv_groups{};
-    p.prefix = p.before_splits = 0;
+    p.prefix = p.direct = p.before_splits = 0;
     p.before = nullptr;
     p.before_ml = nullptr;
     p.group = a->heads / c->kv_heads;
@@ -220,14 +220,45 @@ static int attend_impl(const tpl_kv_cache* c, const tpl_kv_batch* g, const tpl_k
     return TPL_OK;
 }
 
-// Two launches of the same kernels: groups' rows over the tokens that they
-// share, whose results stay in 32 bits in the workspace, then sequences' rows
-// over their own tokens, which begin from those results.
+// Sequences that share tokens, in one of two ways.
+//
+// Two launches: groups' rows over the tokens that they share, whose results stay
+// in 32 bits in the workspace, then sequences' rows over their own tokens, which
+// begin from those results.
+//
+// Directly: each sequence's rows over the shared tokens and its own.
 struct SharedChoice {
     Choice q1, q2;
     int64_t few_bytes, rows;   // of both launches' parts; rows * heads of the results between them
     int64_t bytes;
 };
+
+// The tile kernel's sizes for groups' rows over their shared tokens.  All tiles
+// of a group see the same tokens, so that nothing but the ends of rounds over
+// the CUs speaks against row tiles of 256: they are taken from 512 rows a group
+// on (256 samples of 32768 tokens, 2048 rows for each of 8 heads, in 4 parts:
+// 318 against 363 us with tiles of 128; 256 rows over 4096 tokens 62 against 59).
+// The number of parts weighs rounds of workgroups, each some steps' time to
+// begin and end, against the parts that every sequence has to read (those 256
+// rows with 4, 8, 16 and 32 parts: 70, 59, 61, 77 us).
+static const char* plan_prefix_tile(AttendArgs& p, Choice& q, int64_t rows, int64_t groups) {
+    q.dk = p.c.dim <= 64 ? 64 : p.c.dim <= 96 ? 96 : p.c.dim <= 128 ? 128 : p.c.dim <= 192 ? 192 : 256;
+    const int64_t mean = (rows + groups - 1) / groups;
+    const bool large = q.dk <= 128 && mean >= 512;
+    p.tile_rows = large ? 256 : 128;
+    p.tile_tokens = p.tile_rows / p.group;
+    const int64_t per = (int64_t)p.tile_tokens * p.group, units = groups * ((mean + per - 1) / per) * p.c.kv_heads;
+    const int64_t slots = large || q.dk > 128 ? kCUs : 2 * kCUs, steps = ((int64_t)p.cap + 63) / 64;
+    int64_t least = INT64_MAX;
+    for (int s = 1; s <= 32 && (s == 1 || s * 2 <= steps); ++s) {
+        const int64_t cost = (units * s + slots - 1) / slots * ((steps + s - 1) / s + 6) + s;
+        if (cost < least) least = cost, p.splits = s;
+    }
+    const int64_t tiles = (int64_t)p.g.tokens / p.tile_tokens + groups;
+    if (tiles * p.c.kv_heads * p.splits > INT_MAX) return "too many row tiles";
+    p.tiles = (int)tiles;
+    return nullptr;
+}
 
 static const char* choose_shared(const tpl_kv_cache* c, const tpl_kv_batch* g, const tpl_kv_groups* s, const tpl_kv_query* a,
                                  AttendArgs& p1, AttendArgs& p2, SharedChoice& x, int* status) {
@@ -239,14 +270,34 @@ static const char* choose_shared(const tpl_kv_cache* c, const tpl_kv_batch* g, c
     if (a->window || a->sinks) return "sequences that share tokens have no window and no sinks";
     if (s->count < 0 || s->count > (1 << 20)) return "groups must be 0 .. 2^20";
     x.bytes = x.q2.bytes();
+    x.few_bytes = x.q2.few_bytes;
+    x.rows = 0;
     x.q1 = Choice{};
     if (s->count == 0 || (!x.q2.few && !x.q2.tile)) return nullptr;
     if (!s->groups || !s->shared) return "groups and shared must not be NULL";
     p2.s = *s;
+    // Directly where an average sequence fills a row tile by itself: its
+    // products over the shared tokens are as many either way (16 questions of
+    // 300 tokens behind 2048, 8 heads a cache's: 242 against 290 us).  And
+    // where all sequences' reading of whole rows of the table comes to 256 MiB
+    // at most, which the caches beside HBM give in less time than a second
+    // launch with its chain of reads takes (e4m3, 8 heads of 128; directly
+    // against in two launches: 4 sequences of 530 tokens 12 against 21 us, 16 of
+    // 2200 25 against 32, 64 of 2200, 295 MB, 44 against 44, 32 of 8200 65
+    // against 49, 64 of 5120 76 against 58).
+    const int64_t rows = (int64_t)g->tokens * p2.group, w = c->type == TPL_KV_E4M3 ? 1 : 2;
+    const int64_t tiles = (rows + g->batch * 16 - 1) / ((int64_t)g->batch * 16);   // of 16 rows, of an average sequence
+    const double once = (double)(g->batch * tiles * c->kv_heads) * (double)(c->dim * 2 * w) * p2.cap;
+    if (rows >= (int64_t)g->batch * 128 || once <= 0x1p28) {
+        p2.direct = 1;
+        return nullptr;
+    }
     p1 = p2;
     p1.prefix = 1;
-    const int64_t rows = (int64_t)g->tokens * p1.group, mean = (rows + s->count - 1) / s->count;
-    if (p1.group > 128 || mean <= 64) {
+    // A group of up to 16 rows goes through the split kernel; with 32 and 64
+    // rows that took 72 and 47 us where row tiles take 67 and 32 (8 sequences of
+    // 32200 tokens, 16 of 2200).
+    if (p1.group > 128 || rows <= (int64_t)s->count * 16) {
         x.q1.few = true;
         p1.few = INT_MAX;
         if (const char* why = plan_few(p1, x.q1, rows, s->count, 64, true)) return why;
@@ -254,15 +305,19 @@ static const char* choose_shared(const tpl_kv_cache* c, const tpl_kv_batch* g, c
     } else {
         x.q1.tile = true;
         p1.few = 0;
-        if (const char* why = plan_tile(p1, x.q1, rows, s->count)) return why;
+        if (const char* why = plan_prefix_tile(p1, x.q1, rows, s->count)) return why;
         p1.before_splits = p1.splits;
     }
-    if (x.q2.few)   // how long sequences' own tokens are is not known: a head a workgroup
-        if (const char* why = plan_few(p2, x.q2, rows, g->batch, 64, false)) return why;
+    // Sequences' own tokens are taken to be few: one kernel for all of them, a
+    // head a workgroup.
+    x.q2 = Choice{};
+    x.q2.few = true;
+    p2.few = INT_MAX;
+    if (const char* why = plan_few(p2, x.q2, rows, g->batch, 64, false)) return why;
     p2.before_splits = p1.before_splits;
     x.few_bytes = x.q1.few_bytes > x.q2.few_bytes ? x.q1.few_bytes : x.q2.few_bytes;
     x.rows = (int64_t)p1.before_splits * g->tokens * a->heads;
-    x.bytes = kCounters * 4 + x.few_bytes + x.q2.tile_bytes + x.rows * (c->dim * 4 + 8);
+    x.bytes = kCounters * 4 + x.few_bytes + x.rows * (c->dim * 4 + 8);
     return nullptr;
 }
 
@@ -275,12 +330,17 @@ static int attend_shared_impl(const tpl_kv_cache* c, const tpl_kv_batch* g, cons
     if (!x.q2.few && !x.q2.tile) return TPL_OK;
     if (s->count == 0) return attend_impl(c, g, a, ws, ws_bytes, st);
     if (const int bad = check_query(a, ws, ws_bytes, x.bytes)) return bad;
-    p1.counters = p2.counters = (int*)ws;
-    p1.parts = p2.parts = (float*)((char*)ws + kCounters * 4);
+    p2.counters = (int*)ws;
+    p2.parts = (float*)((char*)ws + kCounters * 4);
     p2.tile_parts = (float*)((char*)p2.parts + x.few_bytes);
-    p1.before = p2.before = (float*)((char*)p2.tile_parts + x.q2.tile_bytes);
-    p1.before_ml = p2.before_ml = (float2*)(p1.before + x.rows * c->dim);
-    hipError_t e = x.q1.tile ? launch_tile_shared(p1, x.q1.dk, false, st) : launch_few_shared(p1, x.q1.dc, x.q1.mr, st);
+    hipError_t e = hipSuccess;
+    if (!p2.direct) {
+        p1.counters = p2.counters;
+        p1.parts = p2.parts;
+        p1.before = p2.before = p2.tile_parts;
+        p1.before_ml = p2.before_ml = (float2*)(p1.before + x.rows * c->dim);
+        e = x.q1.tile ? launch_tile_shared(p1, x.q1.dk, false, st) : launch_few_shared(p1, x.q1.dc, x.q1.mr, st);
+    }
     if (e == hipSuccess && x.q2.tile) e = launch_tile_shared(p2, x.q2.dk, false, st);
     if (e == hipSuccess && x.q2.few) e = launch_few_shared(p2, x.q2.dc, x.q2.mr, st);
     if (e == hipSuccess && x.q2.tile && p2.splits > 1) e = launch_tile_shared(p2, x.q2.dk, true, st);

@@ -42,8 +42,9 @@ struct AttendArgs {
     float* tile_parts;
     // Sequences that share their first tokens (the kernels' SHARED forms).
     tpl_kv_groups s;
-    int32_t prefix;        // 1: groups' rows and the tokens they share; 0: sequences and their own tokens
-    int32_t before_splits; // parts that the first of these launches leaves of each row
+    int32_t prefix;        // groups' rows and the tokens they share, not sequences
+    int32_t direct;        // sequences' rows and all their tokens, the shared ones too; otherwise those have been taken before:
+    int32_t before_splits; // in this many parts of each row
     float* before;         // [before_splits][tokens][heads][dim], weights' sums not yet divided by
     float2* before_ml;     // [before_splits][tokens][heads]: a row's reference and sum of weights
 };
@@ -59,12 +60,15 @@ struct Span {
     __device__ __forceinline__ int base(int t) const { return t < na ? t * 16 : lo + (t - na) * 16; }
 };
 
-// The groups that hold tokens lo .. hi - 1.
-__device__ __forceinline__ Span span_from(int lo, int hi) {
+// A sequence's groups of 16 tokens where its first `cut` tokens are another's:
+// those that hold them, in that one's pages, and those that hold tokens
+// cut .. end - 1, in its own.  Where the cut lies inside 16 tokens both have a
+// group there.
+__device__ __forceinline__ Span span_cut(int cut, int end, bool first, bool own) {
     Span s;
-    s.na = 0;
-    s.lo = lo & ~15;
-    s.n = hi > s.lo ? ((hi + 15) >> 4) - (lo >> 4) : 0;
+    s.na = first ? (cut + 15) >> 4 : 0;
+    s.lo = cut & ~15;
+    s.n = s.na + (own && end > s.lo ? ((end + 15) >> 4) - (cut >> 4) : 0);
     return s;
 }
 
@@ -88,10 +92,14 @@ __device__ __forceinline__ Group read_group(const AttendArgs& p, int g) {
     return x;
 }
 
-// How many of sequence b's first tokens are taken with its group: that group's,
-// or none where b has to look for itself.  Its group is the last of those in
-// order that begin at or before it.
-__device__ __forceinline__ int shared_of(const AttendArgs& p, int b, const Seq& s) {
+// How many of sequence b's first tokens are its group's, and the sequence that
+// has them: none and itself where b has to look for itself.  Its group is the
+// last of those in order that begin at or before it.
+struct Common {
+    int row, cut;
+};
+
+__device__ __forceinline__ Common common_of(const AttendArgs& p, int b, const Seq& s) {
     int lo = 0, hi = p.s.count;   // groups[lo] <= b, as far as they are in order
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -103,7 +111,7 @@ __device__ __forceinline__ int shared_of(const AttendArgs& p, int b, const Seq& 
     const Group g = read_group(p, lo);
     const bool ok = g.s.n > 0 && g.first <= b && b < g.end && s.n > 0 && g.s.row0 <= s.row0 && s.row0 + s.n <= g.s.row0 + g.s.n &&
                     g.s.length <= s.length - s.n;
-    return ok ? g.s.length : 0;
+    return ok ? Common{g.first, g.s.length} : Common{b, 0};
 }
 
 __device__ __forceinline__ Span span_of(const AttendArgs& p, int first_pos, int last_pos) {
@@ -172,8 +180,8 @@ struct FewSeq {
     Span span;
     int tiles;      // row tiles
     int steps;      // steps of one row tile, at least 1
-    int row;        // SHARED: its row of the table
-    int lo;         // SHARED: its first token here
+    int row;        // SHARED: the row of the table that names its first tokens,
+    int cut;        // SHARED: how many those are
     __device__ __forceinline__ uint64_t all() const { return (uint64_t)tiles * (uint32_t)steps; }
 };
 
@@ -185,11 +193,12 @@ template <int ROWS, bool SHARED>
 __device__ __forceinline__ FewSeq few_seq(const AttendArgs& p, int b) {
     FewSeq f;
     f.row = b;
-    f.lo = 0;
+    f.cut = 0;
     if (SHARED && p.prefix) {
         const Group g = read_group(p, b);
         f.s = g.s;
         f.row = g.first;
+        f.cut = g.s.length;
     } else {
         f.s = read_seq(p.g, b);
     }
@@ -197,8 +206,12 @@ __device__ __forceinline__ FewSeq few_seq(const AttendArgs& p, int b) {
     if (rows > p.few) f.s.n = 0;
     f.tiles = f.s.n ? (int)((rows + ROWS - 1) / ROWS) : 0;
     if constexpr (SHARED) {
-        if (!p.prefix) f.lo = shared_of(p, b, f.s);
-        f.span = span_from(f.lo, f.s.length < p.cap ? f.s.length : p.cap);
+        if (!p.prefix) {
+            const Common c = common_of(p, b, f.s);
+            f.row = c.row;
+            f.cut = c.cut;
+        }
+        f.span = span_cut(f.cut, f.s.length < p.cap ? f.s.length : p.cap, p.prefix || p.direct, !p.prefix);
     } else {
         f.span = span_of(p, f.s.length - f.s.n, f.s.length - 1);
     }
@@ -220,7 +233,7 @@ __device__ __forceinline__ FewSeq uniform(FewSeq f) {
     f.steps = uniform(f.steps);
     if constexpr (SHARED) {
         f.row = uniform(f.row);
-        f.lo = uniform(f.lo);
+        f.cut = uniform(f.cut);
     }
     return f;
 }
@@ -237,7 +250,7 @@ __device__ __forceinline__ FewSeq from_lane(FewSeq f, int lane) {
     f.steps = __builtin_amdgcn_readlane(f.steps, lane);
     if constexpr (SHARED) {
         f.row = __builtin_amdgcn_readlane(f.row, lane);
-        f.lo = __builtin_amdgcn_readlane(f.lo, lane);
+        f.cut = __builtin_amdgcn_readlane(f.cut, lane);
     }
     return f;
 }

@@ -81,16 +81,25 @@ struct Tile {
     Chunk<HELD8 ? DC : 2 * DC> v[4];
     float ks, vs;
     int base;     // first token, or a number beyond every position
+    int lo, hi;   // SHARED: its tokens that count
 };
 
 // Where a group of 16 tokens lies: its page's table entry, its first token's
 // place in the page, and that token (beyond every position past the span).
 struct Place {
-    int entry, slot, base;
+    int entry, slot, base, lo, hi;
 };
 
-__device__ __forceinline__ Place place_of(const AttendArgs& p, const int32_t* pages, const Span& span, int t) {
+// `first` names the pages of the span's first na groups, which end before token `cut`.
+template <bool SHARED>
+__device__ __forceinline__ Place place_of(const AttendArgs& p, const int32_t* pages, const int32_t* first, int cut, const Span& span, int t) {
     Place x;
+    if constexpr (SHARED) {
+        const bool own = (t < span.n ? t : span.n - 1) >= span.na;
+        pages = own ? pages : first;
+        x.lo = own ? cut : 0;
+        x.hi = own ? kNowhere : cut - 1;
+    }
     const int base = span.base(t < span.n ? t : span.n - 1);
     const int pg = (int)fdiv((uint32_t)base, p.div_page);
     x.entry = scalar(pages + pg);
@@ -108,13 +117,14 @@ struct Head {
 // Loads without a branch, so that they are in flight together: a group that
 // is not there reads page 0 and stands beyond every position; lanes beyond
 // the head's channels read its first ones.
-template <bool HELD8, int DC>
+template <bool HELD8, int DC, bool SHARED>
 __device__ __forceinline__ void load_tile(const AttendArgs& p, const Head& h, Place at, Tile<HELD8, DC>& x) {
     constexpr int W = HELD8 ? 1 : 2;
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
     const bool there = (uint32_t)at.entry < (uint32_t)p.c.pages;
     const uint32_t where = there ? at.entry : 0, slot = at.slot;
     x.base = there ? at.base : kNowhere;
+    if constexpr (SHARED) x.lo = at.lo, x.hi = at.hi;
     const uint8_t* k = h.k + (uint64_t)where * (uint32_t)(p.c.k_page * W) + slot * (uint32_t)(p.c.k_token * W);
     const uint8_t* v = h.v + (uint64_t)where * (uint32_t)(p.c.v_page * W) + slot * (uint32_t)(p.c.v_token * W);
     x.ks = x.vs = 1.0f;
@@ -201,18 +211,19 @@ __global__ void __launch_bounds__(256, few_blocks(HELD8, DC, MR)) k_few(AttendAr
     FewSeq f;
     const int total = locate<ROWS, SHARED>(p, share, &b, &f, &seq_step, &chunk);
     const int win = p.a.window ? p.a.window : 0x7fffffff;
-    // Whether a row at `at` sees token j, both ends of rows given.
-    auto sees = [&](int j, int at, int last) {
+    // Whether a row at `at` sees token j of a group, both ends of rows given;
+    // whether all rows see its 16 tokens.
+    auto sees = [&](const auto& x, int j, int at, int last) {
         if constexpr (SHARED)
-            return (j <= at) & (j >= f.lo);
+            return (j <= at) & (j >= x.lo) & (j <= x.hi);
         else
             return (j <= at) & ((last - j < win) | (j < p.a.sinks));
     };
-    auto all_see = [&](int base, int first_at, int last_at) {   // 16 tokens
+    auto all_see = [&](const auto& x, int first_at, int last_at) {
         if constexpr (SHARED)
-            return (base <= first_at - 15) & (base >= f.lo);
+            return (x.base <= first_at - 15) & (x.base >= x.lo) & (x.base <= x.hi - 15);
         else
-            return (base <= first_at - 15) & ((last_at - base < win) | (base + 15 < p.a.sinks));
+            return (x.base <= first_at - 15) & ((last_at - x.base < win) | (x.base + 15 < p.a.sinks));
     };
     const bool flat = SHARED && p.prefix;   // all rows see as far as the last shared token
     if (b < 0) return;
@@ -233,7 +244,8 @@ __global__ void __launch_bounds__(256, few_blocks(HELD8, DC, MR)) k_few(AttendAr
         const int s1 = uniform(f.steps - s0 < cend - c ? f.steps : s0 + (cend - c));
         const int rows = f.s.n * p.group - rt * ROWS;   // of this tile, may exceed ROWS
         const int first = flat ? f.s.length - 1 : f.s.length - f.s.n;
-        const int32_t* pages = p.g.table + (SHARED ? f.row : b) * p.g.table_row;
+        const int32_t* pages = p.g.table + b * p.g.table_row;
+        const int32_t* first_pages = SHARED ? p.g.table + f.row * p.g.table_row : pages;
         const int pmin = flat ? first : uniform(first + (int)fdiv((uint32_t)(rt * ROWS), p.div_group));
         const int lastrow = rt * ROWS + (rows < ROWS ? rows : ROWS) - 1;
         const int pmax = flat ? first : uniform(first + (int)fdiv((uint32_t)lastrow, p.div_group));
@@ -264,36 +276,50 @@ __global__ void __launch_bounds__(256, few_blocks(HELD8, DC, MR)) k_few(AttendAr
         }
 
         // What the rows found among the shared tokens, as if they had been the
-        // first ones here: the tile's first share takes it, a wave some parts.
+        // first ones here: the tile's first share takes it, each wave some of
+        // the parts, two at a time.
         if constexpr (SHARED) {
-            if (f.lo > 0 && s0 == 0) {
+            if (f.cut > 0 && s0 == 0 && !p.direct && !flat) {
+                constexpr int AT_ONCE = DC <= 8 ? 2 : 1;
+                const int step = 4 >> p.heads_log;
 #pragma unroll
                 for (int mr = 0; mr < MR; ++mr) {
                     const int row = mr * 16 + r;
                     if (row >= rows) continue;
                     const int i = (int)fdiv((uint32_t)(rt * ROWS + row), p.div_group);
                     const int head = h * p.group + rt * ROWS + row - i * p.group;
+                    const int64_t part = (int64_t)p.g.tokens * p.a.heads, at = (int64_t)(f.s.row0 + i) * p.a.heads + head;
 #pragma unroll 1
-                    for (int k = wt; k < p.before_splits; k += 4 >> p.heads_log) {
-                        const int64_t at = ((int64_t)k * p.g.tokens + f.s.row0 + i) * p.a.heads + head;
-                        const float2 ml = p.before_ml[at];
-                        if (ml.x == neg_inf()) continue;
-                        const float top = fmaxf(m[mr], ml.x);
-                        const float c0 = m[mr] == neg_inf() ? 0.0f : exp2_(m[mr] - top), c1 = exp2_(ml.x - top);
-                        l[mr] *= c0;
-                        if (g == 0) l[mr] += ml.y * c1;   // a lane's sum is of its own tokens
-                        m[mr] = top;
-                        const float* y = p.before + at * p.c.dim;
+                    for (int k = wt; k < p.before_splits; k += AT_ONCE * step) {
+                        float2 ml[AT_ONCE];
+                        f32x4 v[AT_ONCE][DC];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
+                        for (int d = 0; d < AT_ONCE; ++d) {
+                            const int kk = k + d * step < p.before_splits ? k + d * step : k;
+                            ml[d] = p.before_ml[kk * part + at];
+                            if (d && k + d * step >= p.before_splits) ml[d].x = neg_inf();
+                            const float* y = p.before + (kk * part + at) * p.c.dim;
 #pragma unroll
-                            for (int t = 0; t < DC; t += 4) {
-                                const int ch = (g * 4 + e) * DC + t;
-                                f32x4 v = {0, 0, 0, 0};
-                                if (ch < p.c.dim) v = *reinterpret_cast<const f32x4*>(y + ch);
+                            for (int e = 0; e < 4; ++e)
 #pragma unroll
-                                for (int d = 0; d < 4; ++d) o[mr][t + d][e] = o[mr][t + d][e] * c0 + v[d] * c1;
-                            }
+                                for (int t = 0; t < DC / 4; ++t) {
+                                    const int ch = (g * 4 + e) * DC + t * 4;
+                                    v[d][e * (DC / 4) + t] = *reinterpret_cast<const f32x4*>(y + (ch < p.c.dim ? ch : 0));
+                                }
+                        }
+#pragma unroll
+                        for (int d = 0; d < AT_ONCE; ++d) {
+                            if (ml[d].x == neg_inf()) continue;
+                            const float top = fmaxf(m[mr], ml[d].x);
+                            const float c0 = m[mr] == neg_inf() ? 0.0f : exp2_(m[mr] - top), c1 = exp2_(ml[d].x - top);
+                            l[mr] *= c0;
+                            if (g == 0) l[mr] += ml[d].y * c1;   // a lane's sum is of its own tokens
+                            m[mr] = top;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+#pragma unroll
+                                for (int t = 0; t < DC; ++t) o[mr][t][e] = o[mr][t][e] * c0 + v[d][e * (DC / 4) + (t >> 2)][t & 3] * c1;
+                        }
                     }
                 }
             }
@@ -304,8 +330,8 @@ __global__ void __launch_bounds__(256, few_blocks(HELD8, DC, MR)) k_few(AttendAr
                          p.c.k_scale + h * p.c.ks_head, p.c.v_scale + h * p.c.vs_head};
         auto places = [&](Place (&at)[2], int s) {
             const int t = s * (kStepGroups >> p.heads_log) + wt * 2;
-            at[0] = place_of(p, pages, f.span, t);
-            at[1] = place_of(p, pages, f.span, t + 1);
+            at[0] = place_of<SHARED>(p, pages, first_pages, f.cut, f.span, t);
+            at[1] = place_of<SHARED>(p, pages, first_pages, f.cut, f.span, t + 1);
         };
         bool left_out = false;
         auto step = [&](Tile<HELD8, DC> (&x)[2]) {
@@ -339,7 +365,7 @@ __global__ void __launch_bounds__(256, few_blocks(HELD8, DC, MR)) k_few(AttendAr
                 const int base = x[u].base;
                 // A masked score is minus infinity times this: it must not be zero.
                 f2[u] = HELD8 ? fmaxf(p.factor * x[u].ks, 1.17549435e-38f) : p.factor;
-                const bool full = all_see(base, pmin, pmax);
+                const bool full = all_see(x[u], pmin, pmax);
                 if (!full) {
                     // Rows that do not see a token multiply its values with
                     // zeros, which an infinity or NaN among them would show:
@@ -358,9 +384,9 @@ __global__ void __launch_bounds__(256, few_blocks(HELD8, DC, MR)) k_few(AttendAr
                         const int j = base + g * 4 + i;
 #pragma unroll
                         for (int mr = 0; mr < MR; ++mr)
-                            sc[mr][u][i] = sees(j, pos[mr], pos[mr]) ? sc[mr][u][i] : neg_inf();
+                            sc[mr][u][i] = sees(x[u], j, pos[mr], pos[mr]) ? sc[mr][u][i] : neg_inf();
                         // A token that no row sees weighs nothing, whatever its place holds.
-                        if (!sees(j, pmax, pmin))
+                        if (!sees(x[u], j, pmax, pmin))
 #pragma unroll
                             for (int k = 0; k < (int)(sizeof(x[u].v[i]) / 4); ++k) x[u].v[i].w[k] = 0;
                     }
@@ -431,8 +457,8 @@ __global__ void __launch_bounds__(256, few_blocks(HELD8, DC, MR)) k_few(AttendAr
             places(at, s0);
             for (int s = s0; s < s1; ++s) {
                 Tile<HELD8, DC> x[2];
-                load_tile<HELD8, DC>(p, hd, at[0], x[0]);
-                load_tile<HELD8, DC>(p, hd, at[1], x[1]);
+                load_tile<HELD8, DC, SHARED>(p, hd, at[0], x[0]);
+                load_tile<HELD8, DC, SHARED>(p, hd, at[1], x[1]);
                 places(at, s + 1);   // the table's entries for the next step
                 step(x);
             }
@@ -445,9 +471,9 @@ __global__ void __launch_bounds__(256, few_blocks(HELD8, DC, MR)) k_few(AttendAr
                 for (int u = 0; u < 2; ++u) {
                     const int t = s * (kStepGroups >> p.heads_log) + wt * 2 + u;
                     if (t >= f.span.n) break;
-                    const Place x = place_of(p, pages, f.span, t);
+                    const Place x = place_of<SHARED>(p, pages, first_pages, f.cut, f.span, t);
                     if ((uint32_t)x.entry >= (uint32_t)p.c.pages) continue;
-                    if (all_see(x.base, pmin, pmax)) continue;
+                    if (all_see(x, pmin, pmax)) continue;
 #pragma unroll 1
                     for (int j = 0; j < 16; ++j) {
                         const uint8_t* from = hd.v + (uint64_t)(uint32_t)x.entry * (uint32_t)(p.c.v_page * W) +
@@ -464,7 +490,7 @@ __global__ void __launch_bounds__(256, few_blocks(HELD8, DC, MR)) k_few(AttendAr
                                 if (!(__builtin_fabsf(v) < __builtin_inff()))
 #pragma unroll
                                     for (int mr = 0; mr < MR; ++mr)
-                                        if (sees(tok, pos[mr], pos[mr])) o[mr][t2][i] += v;
+                                        if (sees(x, tok, pos[mr], pos[mr])) o[mr][t2][i] += v;
                             }
                     }
                 }

@@ -44,17 +44,17 @@ namespace kv {
 constexpr int kTokens = 64;    // tokens of a step
 constexpr int kInfo = 128;     // 16-token groups whose pages are looked up at a time
 
-// The row tile x: its sequence (or group of them), its row of the table, and
-// the first of its tokens that counts here.
+// The row tile x: its sequence (or group of them), how many of its first tokens
+// are another's, and the row of the table that names those.
 struct TileAt {
-    int b, row, lo;
+    int b, row, cut;
     Seq s;
 };
 
 template <bool SHARED>
 __device__ __forceinline__ TileAt tile_at(const AttendArgs& p, int x) {
     TileAt t;
-    t.lo = 0;
+    t.cut = 0;
     if (SHARED && p.prefix) {
         // Groups are numbered as sequences are.
         const int lane = threadIdx.x & 63;
@@ -69,7 +69,7 @@ __device__ __forceinline__ TileAt tile_at(const AttendArgs& p, int x) {
                 t.row = __builtin_amdgcn_readlane(g.first, from);
                 t.s.row0 = __builtin_amdgcn_readlane(g.s.row0, from);
                 t.s.n = __builtin_amdgcn_readlane(g.s.n, from);
-                t.s.length = __builtin_amdgcn_readlane(g.s.length, from);
+                t.s.length = t.cut = __builtin_amdgcn_readlane(g.s.length, from);
             }
         }
         return t;
@@ -78,7 +78,11 @@ __device__ __forceinline__ TileAt tile_at(const AttendArgs& p, int x) {
     t.b = t.row = q.b;
     t.s = q.s;
     if constexpr (SHARED) {
-        if (t.b >= 0) t.lo = uniform(shared_of(p, t.b, t.s));
+        if (t.b >= 0) {
+            const Common c = common_of(p, t.b, t.s);
+            t.row = uniform(c.row);
+            t.cut = uniform(c.cut);
+        }
     }
     return t;
 }
@@ -131,7 +135,7 @@ __global__ void __launch_bounds__(WAVES * 64, D <= 128 ? 2 : 1) k_tile(AttendArg
     const int split = rest % p.splits;
     const int x = p.tiles - 1 - rest / p.splits;
     const TileAt mine = tile_at<SHARED>(p, x);
-    const int b = mine.b, lo = mine.lo;
+    const int b = mine.b, cut = mine.cut;
     const Seq s = mine.s;
     if (b < 0) return;
     if ((int64_t)s.n * p.group <= p.few) return;
@@ -141,26 +145,32 @@ __global__ void __launch_bounds__(WAVES * 64, D <= 128 ? 2 : 1) k_tile(AttendArg
     const int rows = tn * p.group;
     const bool flat = SHARED && p.prefix;   // all rows see as far as the last shared token
     const int pmin = flat ? s.length - 1 : s.length - s.n + t0, pmax = flat ? pmin : pmin + tn - 1;
-    const Span span = SHARED ? span_from(lo, pmax + 1 < p.cap ? pmax + 1 : p.cap) : span_of(p, pmin, pmax);
-    const int32_t* pages = p.g.table + mine.row * p.g.table_row;
+    const Span span = SHARED ? span_cut(cut, pmax + 1 < p.cap ? pmax + 1 : p.cap, true, !flat) : span_of(p, pmin, pmax);
+    const int32_t* pages = p.g.table + b * p.g.table_row;
+    const int32_t* first_pages = SHARED ? p.g.table + mine.row * p.g.table_row : pages;
     const int win = p.a.window ? p.a.window : 0x7fffffff;
+    // Group t's tokens that count: its first ones are another's up to the cut.
+    struct Range {
+        int lo, hi;
+    };
+    auto range_of = [&](int t) { return Range{SHARED && t >= span.na ? cut : 0, SHARED && t < span.na ? cut - 1 : kNowhere}; };
     // Whether a row at `at` sees token j, both ends of rows given; whether all
     // or any of them see the 16 from `base` on.
-    auto sees = [&](int j, int at, int last) {
+    auto sees = [&](Range rg, int j, int at, int last) {
         if constexpr (SHARED)
-            return (j <= at) & (j >= lo);
+            return (j <= at) & (j >= rg.lo) & (j <= rg.hi);
         else
             return (j <= at) & ((last - j < win) | (j < p.a.sinks));
     };
-    auto whole16 = [&](int base, int first_at, int last_at) {
+    auto whole16 = [&](Range rg, int base, int first_at, int last_at) {
         if constexpr (SHARED)
-            return (base <= first_at - 15) & (base >= lo);
+            return (base <= first_at - 15) & (base >= rg.lo) & (base <= rg.hi - 15);
         else
             return (base <= first_at - 15) & ((last_at - base < win) | (base + 15 < p.a.sinks));
     };
     auto some16 = [&](int base, int first_at, int last_at) {
         if constexpr (SHARED)
-            return base <= last_at;   // spans begin at the group that holds lo
+            return base <= last_at;
         else
             return (base <= last_at) & ((first_at - base - 15 < win) | (base < p.a.sinks));
     };
@@ -198,35 +208,6 @@ __global__ void __launch_bounds__(WAVES * 64, D <= 128 ? 2 : 1) k_tile(AttendArg
         for (int i = 0; i < 16; ++i) o[t][i] = 0.0f;
     float m = neg_inf(), l = 0.0f;
 
-    // What the rows found among the shared tokens, as if they had been the
-    // first ones here.
-    if constexpr (SHARED) {
-        if (lo > 0 && split == 0 && there) {
-#pragma unroll 1
-            for (int k = 0; k < p.before_splits; ++k) {
-                const int64_t at = ((int64_t)k * p.g.tokens + s.row0 + t0 + qi) * p.a.heads + head;
-                const float2 ml = p.before_ml[at];
-                if (ml.x == neg_inf()) continue;
-                const float top = fmaxf(m, ml.x);
-                const float c0 = m == neg_inf() ? 0.0f : exp2_(m - top), c1 = exp2_(ml.x - top);
-                l *= c0;
-                if (hh == 0) l += ml.y * c1;   // a lane's sum is of its own tokens
-                m = top;
-                const float* y = p.before + at * p.c.dim;
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-#pragma unroll
-                    for (int i = 0; i < 16; i += 4) {
-                        const int ch = t * 32 + i * 2 + hh * 4;
-                        f32x4 v = {0, 0, 0, 0};
-                        if (ch < p.c.dim) v = *reinterpret_cast<const f32x4*>(y + ch);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) o[t][i + e] = o[t][i + e] * c0 + v[e] * c1;
-                    }
-            }
-        }
-    }
-
     const int all = (span.n + 3) >> 2;   // steps of 64 tokens
     const int per = (all + p.splits - 1) / p.splits;
     const int st0 = split * per, st1 = st0 + per < all ? st0 + per : all;
@@ -256,7 +237,7 @@ __global__ void __launch_bounds__(WAVES * 64, D <= 128 ? 2 : 1) k_tile(AttendArg
         if (t < span.n) {
             base = span.base(t);
             const int pg = (int)fdiv((uint32_t)base, p.div_page);
-            where = pages[pg];
+            where = (SHARED && t < span.na ? first_pages : pages)[pg];
             if (where >= p.c.pages) where = -1;
             if (where >= 0) slot = base - pg * p.c.page;
             if (HELD8 && where >= 0) {
@@ -267,7 +248,7 @@ __global__ void __launch_bounds__(WAVES * 64, D <= 128 ? 2 : 1) k_tile(AttendArg
         }
         base = where < 0 ? kNowhere : base;
         gbase[to] = base;
-        const uint64_t seen = __ballot(whole16(base, pmin, pmax));
+        const uint64_t seen = __ballot(whole16(range_of(t), base, pmin, pmax));
         if (lane == 0) gfull[to >> 6] = seen;
         where = where < 0 ? 0 : where;
         gk[to] = (const uint8_t*)p.c.k + (where * p.c.k_page + slot * p.c.k_token + h * p.c.k_head) * W;
@@ -346,15 +327,16 @@ __global__ void __launch_bounds__(WAVES * 64, D <= 128 ? 2 : 1) k_tile(AttendArg
             for (int i = 0; i < VN; ++i) {
                 const int quad = (i * THREADS + tid) / CH8 % (kTokens / 4);
                 const int j = gbase[g0 + (quad >> 2)] + (quad & 3) * 4;
+                const Range rg = range_of(step * 4 + (quad >> 2));
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    if (!sees(j + e, pmax, pmin)) vreg[i][e] = VPiece{};
+                    if (!sees(rg, j + e, pmax, pmin)) vreg[i][e] = VPiece{};
                 // Rows that do not see a token multiply its values with zeros,
                 // which an infinity or NaN among them would show: such values
                 // are left out here, and added at the end to the rows that do
                 // see them.
                 const int gb = j - (quad & 3) * 4;
-                if (whole16(gb, pmin, pmax)) continue;   // all rows see these 16
+                if (whole16(rg, gb, pmin, pmax)) continue;   // all rows see these 16
                 bool some = false;
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
@@ -431,7 +413,7 @@ __global__ void __launch_bounds__(WAVES * 64, D <= 128 ? 2 : 1) k_tile(AttendArg
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int base = __builtin_amdgcn_readfirstlane(gbase[g0 + i]);
-            full = full & whole16(base, wmin, wmax);
+            full = full & whole16(range_of(step * 4 + i), base, wmin, wmax);
             any = any | some16(base, wmin, wmax);
         }
     };
@@ -440,9 +422,11 @@ __global__ void __launch_bounds__(WAVES * 64, D <= 128 ? 2 : 1) k_tile(AttendArg
 #pragma unroll
         for (int z = 0; z < 4; ++z) {   // 16 tokens; `d` tokens back from the row lies the lane's first
             const int base = __builtin_amdgcn_readfirstlane(gbase[g0 + z]);
-            const int d = pos - base - hh * 4;
-            // The last `w` tokens up to the row's are seen.
-            const uint32_t w = !SHARED ? (uint32_t)win : pos < lo ? 0u : (uint32_t)(pos - lo + 1);
+            const Range rg = range_of(step * 4 + z);
+            const int last = SHARED && rg.hi < pos ? rg.hi : pos;
+            const int d = last - base - hh * 4;
+            // The last `w` tokens up to there are seen.
+            const uint32_t w = !SHARED ? (uint32_t)win : last < rg.lo ? 0u : (uint32_t)(last - rg.lo + 1);
             const int sk = p.a.sinks - base - hh * 4;
             if (!SHARED && base < p.a.sinks) {
 #pragma unroll
@@ -613,12 +597,13 @@ __global__ void __launch_bounds__(WAVES * 64, D <= 128 ? 2 : 1) k_tile(AttendArg
 #pragma unroll 1
         for (int t = st0 * 4; t < st1 * 4 && t < span.n; ++t) {
             const int base = span.base(t), pg = (int)fdiv((uint32_t)base, p.div_page);
-            const int where = pages[pg];
+            const int where = (SHARED && t < span.na ? first_pages : pages)[pg];
+            const Range rg = range_of(t);
             if (where < 0 || where >= p.c.pages) continue;
-            if (whole16(base, pmin, pmax)) continue;   // all see it: nothing left out
+            if (whole16(rg, base, pmin, pmax)) continue;   // all see it: nothing left out
 #pragma unroll 1
             for (int j = base; j < base + 16; ++j) {
-                if (!sees(j, pos, pos)) continue;
+                if (!sees(rg, j, pos, pos)) continue;
                 const uint8_t* from = (const uint8_t*)p.c.v + (where * p.c.v_page + (j - pg * p.c.page) * p.c.v_token + h * p.c.v_head) * W;
                 int h4 = hh * 4, dim = p.c.dim;
                 asm volatile("" : "+v"(h4), "+s"(dim));   // no comparison is to be held in registers throughout

@@ -53,6 +53,12 @@ def poison(x, table, starts, lengths, groups, shared, page):
         x[~keep] = float("nan")
 
 
+def widened(table, page, kv_heads, dim, held8):
+    """The table with rows so wide (nothing is there) that reading all of them would be 256 MiB at least."""
+    width = 2 ** 28 // (len(table) * kv_heads * dim * 2 * (1 if held8 else 2) * page) + 1
+    return [row + [-1] * (width - len(row)) for row in table]
+
+
 def check(seed, news, lengths, groups, shared, *, heads=8, kv_heads=2, dim=64, dtype=torch.bfloat16, held8=True, page=32, block=16,
           by_head=False, lse=True, tweak=None, given=None, spread=2.0, scale=None):
     """`given`: (starts, groups, shared) as the call gets them, where those are out of order."""
@@ -71,8 +77,11 @@ def check(seed, news, lengths, groups, shared, *, heads=8, kv_heads=2, dim=64, d
     cache = kv.PagedCache(on_gpu(k), on_gpu(v), dev(ks), dev(vs))
     got = torch.full(q.shape, 7.0, dtype=dtype, device="cuda")
     got_lse = torch.full(q.shape[:2], 7.0, device="cuda") if lse else None
-    for _ in range(2):   # the second call finds what the first has left of the workspace
-        r = kv.attend_shared(dev(q), cache, dev(table), dev(starts), dev(lengths), dev(groups), dev(shared), scale=scale, out=got, lse=got_lse)
+    # A call chooses its kernels by what rows of the table could hold: with wide ones groups' shared tokens go through a
+    # launch of their own.  The last call finds what the others have left of the workspace.
+    for t in (table, widened(table, page, kv_heads, dim, held8), table):
+        got.fill_(7.0)
+        r = kv.attend_shared(dev(q), cache, dev(t), dev(starts), dev(lengths), dev(groups), dev(shared), scale=scale, out=got, lse=got_lse)
         assert r is got
         compare_attend(got.cpu(), None if got_lse is None else got_lse.cpu(), *want, v, vs, dtype, held8, dim, max(lengths + [1]))
     return cache, q, table, starts, want
@@ -186,7 +195,9 @@ def test_sequences_and_groups_out_of_order():
                                                                             for b in range(a, e) for i in range(n)])
     lengths = [150, 120, 130, 125, 140, 133]
 
-    def call(groups, shared, starts=starts, lengths=lengths):
+    wide = widened(table, 32, 2, 64, True)
+
+    def call(groups, shared, starts=starts, lengths=lengths, table=table):
         lse = torch.full(q.shape[:2], 7.0, device="cuda")
         out = kv.attend_shared(dev(q), cache, dev(table), dev(starts), dev(lengths), dev(groups), dev(shared), out=torch.full_like(q, 7.0, device="cuda"),
                                lse=lse)
@@ -194,33 +205,36 @@ def test_sequences_and_groups_out_of_order():
     # Groups that are none: their sequences look for themselves, in tables that name the shared pages too.
     for groups, shared in (([0, 3, 6], [64, 0]), ([0, 3, 6], [-1, 96]), ([0, 3, 6], [1 << 30, 96]), ([-5, 3, 6], [64, 96]), ([0, 3, 100], [64, 96]),
                            ([0, 100, 6], [64, 96]), ([3, 0], [64]), ([6, 6], [64]), ([-3, -1], [64])):
-        got, lse = call(groups, shared)
-        compare_attend(got, lse, *want, cache.v.cpu(), cache.v_scale.cpu(), torch.bfloat16, True, 64, 150)
+        for t in (table, wide):
+            got, lse = call(groups, shared, table=t)
+            compare_attend(got, lse, *want, cache.v.cpu(), cache.v_scale.cpu(), torch.bfloat16, True, 64, 150)
     # Skipped sequences: rows stay as they were, the others are served.
     for bad_starts, bad_lengths, skipped in ((starts, [150, 1, 130, 125, 140, 133], [1]), (starts, [0, 120, 130, 125, 140, 133], [0]),
                                              (starts, [150, 120, 130, 125, 140, -7], [5]), ([0, 1, -9, 4, 5, 7, 8], lengths, [1, 2]),
                                              ([0, 1, 3, 99, 5, 7, 8], lengths, [2, 3]), ([-1, 1, 3, 4, 5, 7, 8], lengths, [0])):
-        got, lse = call([0, 3, 6], [64, 96], bad_starts, bad_lengths)
-        for b in range(6):
-            rows = slice(starts[b], starts[b + 1])
-            if b in skipped:
-                assert bool((got[rows] == 7).all()) and bool((lse[rows] == 7).all())
-            else:
-                compare_attend(got[rows], lse[rows], *(x[rows] for x in want), cache.v.cpu(), cache.v_scale.cpu(), torch.bfloat16, True, 64, 150)
+        for t in (table, wide):
+            got, lse = call([0, 3, 6], [64, 96], bad_starts, bad_lengths, t)
+            for b in range(6):
+                rows = slice(starts[b], starts[b + 1])
+                if b in skipped:
+                    assert bool((got[rows] == 7).all()) and bool((lse[rows] == 7).all())
+                else:
+                    compare_attend(got[rows], lse[rows], *(x[rows] for x in want), cache.v.cpu(), cache.v_scale.cpu(), torch.bfloat16, True, 64, 150)
 
 
 def test_rows_of_no_sequence():
     from tensor_layout_amd import kv
     cache, q, table, starts, want = check(17, [1, 1, 1], [100, 90, 95], [0, 3], [64])
     wide = torch.cat([q, q, q])
-    for tokens in (4, 9):
+    for tokens, t in ((4, table), (9, table), (4, widened(table, 32, 2, 64, True))):
         out = torch.full((tokens, *q.shape[1:]), 7.0, dtype=q.dtype, device="cuda")
-        kv.attend_shared(dev(wide[:tokens]), cache, dev(table), dev(starts), dev([100, 90, 95]), dev([0, 3]), dev([64]), out=out)
+        kv.attend_shared(dev(wide[:tokens]), cache, dev(t), dev(starts), dev([100, 90, 95]), dev([0, 3]), dev([64]), out=out)
         assert bool((out[3:] == 7).all())
         compare_attend(out[:3].cpu(), None, *want, cache.v.cpu(), cache.v_scale.cpu(), torch.bfloat16, True, 64, 100)
 
 
-def test_strides_streams_and_a_graph():
+@pytest.mark.parametrize("wide", [False, True])
+def test_strides_streams_and_a_graph(wide):
     """Heads and rows apart, a named stream beside another's calls, and a captured call replayed on new numbers."""
     from tensor_layout_amd import kv
     g = torch.Generator().manual_seed(18)
@@ -229,7 +243,7 @@ def test_strides_streams_and_a_graph():
     for news, lengths, shared in (([1] * 6, [150, 140, 145, 139, 133, 170], [130, 100]), ([1] * 6, [170, 141, 160, 139, 133, 120], [96, 107]),
                                   ([1] * 6, [150, 140, 99, 139, 133, 170], [100, 133])):
         starts, table, pages = shared_batch(g, news, [170] * 6, groups, [0, 0], page)
-        cases.append((starts, table, lengths, shared))
+        cases.append((starts, widened(table, page, 2, dim, True) if wide else table, lengths, shared))
     pages = 6 * 6 + 3
     k, ks, v, vs = kv_cases.pools(g, pages, page, 2, dim, torch.bfloat16, True, 16, False)
     cache = kv.PagedCache(dev(k), dev(v), dev(ks), dev(vs))
@@ -277,8 +291,9 @@ def test_it_gives_what_attend_gives_in_turn_with_it():
     q = dev((torch.randn((12, 16, 128), generator=g) * 2).half())
     args = (q, cache, dev(table), dev(starts), dev(lengths))
     want = kv_oracle.attend(q.cpu(), k, v, ks, vs, table, starts, lengths, 128 ** -0.5)
+    wide = (*args[:2], dev(widened(table, 32, 4, 128, True)), *args[3:])
     for _ in range(3):
-        for got in (kv.attend(*args), kv.attend_shared(*args, dev([0, 12]), dev([992]))):
+        for got in (kv.attend(*args), kv.attend_shared(*args, dev([0, 12]), dev([992])), kv.attend_shared(*wide, dev([0, 12]), dev([992]))):
             compare_attend(got.cpu(), None, *want, v, vs, torch.float16, True, 128, 1100)
 
 
