@@ -28,8 +28,10 @@ FLAGS = [
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-I", os.path.join(ROOT, "include"),
 ]
-# An early pass makes one vector of a state's or an output's two blocks, which then goes through scratch memory (8 times the time).
-MORE_FLAGS = {"linear_chunk.hip": ["-mllvm", "-disable-promote-alloca-to-vector"]}
+# An early pass makes one vector of a state's 32 registers, which costs scratch memory (chunks: 8 times the time) or
+# three times the registers (single tokens: 171 against 109 us).
+_NO_VECTORS = ["-mllvm", "-disable-promote-alloca-to-vector"]
+MORE_FLAGS = {"linear_chunk.hip": _NO_VECTORS, "linear_step.hip": _NO_VECTORS}
 
 
 def _run(cmd, verbose):

@@ -71,11 +71,16 @@ static const char* choose(const tpl_linear_pool* c, const tpl_linear_batch* g, c
     }
     if (p.few != INT_MAX) {
         const int64_t units = heads * p.slices;
-        // Segments where whole sequences would leave CUs without work: as many
-        // as give every CU two, each of some chunks.
-        int64_t length = g->tokens / g->batch;
-        if (units < 2 * kCUs && length >= 4 * kChunk) {
-            int64_t n = (2 * kCUs + units - 1) / units;
+        // Segments where whole sequences would leave the CUs fewer waves than
+        // they hold (two a SIMD, one with over 128 key channels), as many as fill
+        // them, each of some chunks.  A prompt of 8192 tokens, 32 heads of 128, in
+        // segments of 512: 127 us; of 1024 156, of 256 159.  24 prompts of up to
+        // 2000 tokens, 12 heads of 64 by 96 (3 waves each): whole 165 us, in 2
+        // segments 188, in 3 158.
+        const int64_t want = kCUs * (c->key_dim <= 128 ? 8 : 4) / chunk_waves(c->value_dim);
+        const int64_t length = g->tokens / g->batch;
+        if (units < want && length >= 4 * kChunk) {
+            const int64_t n = (want + units - 1) / units;
             int64_t segment = (length + n - 1) / n;
             segment = (segment + kChunk - 1) / kChunk * kChunk;
             if (segment < 2 * kChunk) segment = 2 * kChunk;
@@ -105,7 +110,7 @@ static int attend_impl(const tpl_linear_pool* c, const tpl_linear_batch* g, cons
         return fail_status(TPL_E_LAYOUT, "q, k, v and out must start, and their rows and heads lie, on 16 bytes");
     // A chunk's rows have 32-bit offsets in the kernels.
     for (int64_t x : {a->q_token, a->k_token, a->v_token})
-        if (x < 0 || x > (INT_MAX >> 7)) return fail_status(TPL_E_LAYOUT, "rows of q, k and v must lie under 2^24 elements apart");
+        if (g->tokens > 1 && (x < 0 || x > (INT_MAX >> 7))) return fail_status(TPL_E_LAYOUT, "rows of q, k and v must lie under 2^24 elements apart");
     if (q.bytes > 0 && (!ws || ((uintptr_t)ws & 15))) return fail_status(TPL_E_ARG, "workspace must lie on 16 bytes");
     if (ws_bytes < q.bytes) return fail_status(TPL_E_ARG, "workspace is too small");
     p.parts = (float*)ws;

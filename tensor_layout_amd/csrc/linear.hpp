@@ -17,7 +17,7 @@ using kv::pack2;
 using kv::u32x2;
 using kv::u32x4;
 
-constexpr int kFew = 16;     // a sequence of up to this many new tokens goes token by token
+constexpr int kFew = 8;      // a sequence of up to this many new tokens goes token by token
 constexpr int kChunk = 64;   // tokens that longer ones take together
 
 struct LinearArgs {
@@ -61,7 +61,8 @@ hipError_t launch_step(const LinearArgs& p, bool narrow, hipStream_t st);
 enum { kWhole = 0, kState = 1, kOutput = 2 };   // what launch_chunk does with its sequences or segments
 hipError_t launch_chunk(const LinearArgs& p, int mode, int64_t units, hipStream_t st);
 hipError_t launch_scan(const LinearArgs& p, hipStream_t st);
-int chunk_slices(int value_dim);
+int chunk_waves(int value_dim);    // of a workgroup
+int chunk_slices(int value_dim);   // workgroups of a head
 
 }  // namespace linear
 }  // namespace tpl

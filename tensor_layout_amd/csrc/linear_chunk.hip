@@ -398,8 +398,9 @@ __global__ void __launch_bounds__(WAVES * 64, NK <= 4 ? 2 : 1) k_chunk(LinearArg
             for (int z = 0; z < 4; ++z) {
                 float w[8];
                 weighted(z, w);
-                // In bf16 three parts: two would leave a state 2^-18 off.
-                constexpr int PARTS = kScaled ? 2 : 3;
+                // In bf16 three parts where the state is kept: two would leave it
+                // 2^-18 off.
+                constexpr int PARTS = kScaled || MODE == kOutput ? 2 : 3;
                 u32x4 part[PARTS];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -483,12 +484,12 @@ __global__ void __launch_bounds__(256) k_scan(LinearArgs p) {
 }
 
 // Waves of a workgroup: a head's value channels by 32, at most 4, evenly.
-static int waves_of(int value_dim) {
+int chunk_waves(int value_dim) {
     const int blocks = (value_dim + 31) / 32, slices = (blocks + 3) / 4, w = (blocks + slices - 1) / slices;
     return w < 2 ? 2 : w;
 }
 int chunk_slices(int value_dim) {
-    const int w = waves_of(value_dim) * 32;
+    const int w = chunk_waves(value_dim) * 32;
     return (value_dim + w - 1) / w;
 }
 
@@ -505,7 +506,7 @@ static hipError_t go_mode(const LinearArgs& p, int mode, unsigned grid, hipStrea
 
 template <typename T, int NK>
 static hipError_t go_waves(const LinearArgs& p, int mode, unsigned grid, hipStream_t st) {
-    switch (waves_of(p.p.value_dim)) {
+    switch (chunk_waves(p.p.value_dim)) {
     case 2: return go_mode<T, NK, 2>(p, mode, grid, st);
     case 3: return go_mode<T, NK, 3>(p, mode, grid, st);
     default: return go_mode<T, NK, 4>(p, mode, grid, st);

@@ -9,19 +9,17 @@
 // values of up to kFew tokens stand in LDS as fp32; a token costs two fused
 // products a state's number, and its output's sums over key channels are left
 // in registers' partial sums, joined over lanes and waves once for all tokens.
-#include <climits>
-
 #include "linear.hpp"
 
 namespace tpl {
 namespace linear {
 
-template <typename T, int COLS, int NP>
+template <typename T, int COLS, int NP, int TOK>
 __global__ void __launch_bounds__(256) k_step(LinearArgs p) {
     typedef typename T::one one;
-    constexpr int ROWS = 256 / COLS, SLICE = COLS * 4;   // key channels of a pass; value channels
-    __shared__ float ks[kFew][256], qs[kFew][256];
-    __shared__ float part[kFew][4][SLICE];
+    constexpr int ROWS = 256 / COLS, SLICE = COLS * 4, DK = NP * ROWS;   // key channels of a pass; value channels; key channels
+    __shared__ float ks[TOK][DK], qs[TOK][DK];
+    __shared__ float part[TOK][4][SLICE];
 
     const int slices = (p.p.value_dim + SLICE - 1) / SLICE;
     const int sl = blockIdx.x % slices, rest = blockIdx.x / slices, h = rest % p.p.heads, b = rest / p.p.heads;
@@ -42,13 +40,13 @@ __global__ void __launch_bounds__(256) k_step(LinearArgs p) {
     const float keep = exp2_(decay_of(p, h));
     const int kh = h / p.share;
 
-    for (int t0 = 0; t0 < s.n; t0 += kFew) {
-        const int n = s.n - t0 < kFew ? s.n - t0 : kFew;
+    for (int t0 = 0; t0 < s.n; t0 += TOK) {
+        const int n = s.n - t0 < TOK ? s.n - t0 : TOK;
         const int64_t row0 = s.row0 + t0;
         if (t0) __syncthreads();
         // Zeros beyond the head's channels, where states are zero too.
-        for (int i = tid; i < n * (NP * ROWS / 2); i += 256) {
-            const int t = i / (NP * ROWS / 2), ch = (i - t * (NP * ROWS / 2)) * 2;
+        for (int i = tid; i < n * (DK / 2); i += 256) {
+            const int t = i / (DK / 2), ch = (i - t * (DK / 2)) * 2;
             uint32_t kw = 0, qw = 0;
             if (ch < p.p.key_dim) {
                 kw = *reinterpret_cast<const uint32_t*>((const one*)p.a.k + (row0 + t) * p.a.k_token + kh * p.a.k_head + ch);
@@ -99,25 +97,27 @@ __global__ void __launch_bounds__(256) k_step(LinearArgs p) {
     }
 }
 
-template <typename T, int COLS>
+template <typename T, int COLS, int TOK>
 static hipError_t go(const LinearArgs& p, hipStream_t st) {
     constexpr int ROWS = 256 / COLS;
-    const int np = (p.p.key_dim + 63) / 64 * 64 / ROWS;   // key channels up to the next multiple of 64
-    const unsigned grid = (unsigned)((int64_t)p.g.batch * p.p.heads * ((p.p.value_dim + COLS * 4 - 1) / (COLS * 4)));
-    if (np <= 64 / ROWS)
-        k_step<T, COLS, 64 / ROWS><<<grid, 256, 0, st>>>(p);
-    else if (np <= 128 / ROWS)
-        k_step<T, COLS, 128 / ROWS><<<grid, 256, 0, st>>>(p);
-    else if (np <= 192 / ROWS)
-        k_step<T, COLS, 192 / ROWS><<<grid, 256, 0, st>>>(p);
-    else
-        k_step<T, COLS, 256 / ROWS><<<grid, 256, 0, st>>>(p);
+    const int64_t grid = (int64_t)p.g.batch * p.p.heads * ((p.p.value_dim + COLS * 4 - 1) / (COLS * 4));
+    switch ((p.p.key_dim + 63) / 64) {   // key channels up to the next multiple of 64
+    case 1: k_step<T, COLS, 64 / ROWS, TOK><<<(unsigned)grid, 256, 0, st>>>(p); break;
+    case 2: k_step<T, COLS, 128 / ROWS, TOK><<<(unsigned)grid, 256, 0, st>>>(p); break;
+    case 3: k_step<T, COLS, 192 / ROWS, TOK><<<(unsigned)grid, 256, 0, st>>>(p); break;
+    default: k_step<T, COLS, 256 / ROWS, TOK><<<(unsigned)grid, 256, 0, st>>>(p); break;
+    }
     return hipGetLastError();
 }
 
+template <typename T, int COLS>
+static hipError_t go_tokens(const LinearArgs& p, hipStream_t st) {
+    return p.g.tokens <= p.g.batch ? go<T, COLS, 1>(p, st) : go<T, COLS, 4>(p, st);
+}
+
 hipError_t launch_step(const LinearArgs& p, bool narrow, hipStream_t st) {
-    if (p.a.type == TPL_KV_BF16) return narrow ? go<kv::Bf16, 8>(p, st) : go<kv::Bf16, 16>(p, st);
-    return narrow ? go<kv::Fp16, 8>(p, st) : go<kv::Fp16, 16>(p, st);
+    if (p.a.type == TPL_KV_BF16) return narrow ? go_tokens<kv::Bf16, 8>(p, st) : go_tokens<kv::Bf16, 16>(p, st);
+    return narrow ? go_tokens<kv::Fp16, 8>(p, st) : go_tokens<kv::Fp16, 16>(p, st);
 }
 
 }  // namespace linear
