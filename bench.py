@@ -37,7 +37,7 @@ TRAFFIC_FILE = os.path.join(ROOT, "profiles", "traffic.json")
 # entry, which the counters do not cover).
 _CSRC = os.path.join(ROOT, "tensor_layout_amd", "csrc")
 KERNEL_SOURCES = sorted(os.path.join(_CSRC, f) for f in os.listdir(_CSRC)
-                        if f.endswith((".hip", ".hpp", ".cpp")) and f != "staged.hip" and not f.startswith("kv"))
+                        if f.endswith((".hip", ".hpp", ".cpp")) and f != "staged.hip" and not f.startswith(("kv", "linear")))
 
 
 def _code_only(text: str) -> str:
