@@ -297,6 +297,45 @@ def test_it_gives_what_attend_gives_in_turn_with_it():
             compare_attend(got.cpu(), None, *want, v, vs, torch.float16, True, 128, 1100)
 
 
+def far_pool(pages, page, heads, dim):
+    """Storage whose last pages lie beyond 2^32 bytes and 2^31 elements, of which only what is used is written."""
+    return torch.empty((pages, page, heads, dim), dtype=torch.bfloat16, device="cuda")
+
+
+def test_pages_far_apart():
+    """Offsets past 32 bits: attention in both ways, reading."""
+    from tensor_layout_amd import kv
+    pages, page, heads, dim = 600_000, 16, 1, 256   # 2.5 * 10^9 elements
+    g = torch.Generator().manual_seed(29)
+    used = [599_999, 3, 599_000, 300_001, 1, 598_765, 400_000, 2, 599_998]
+    near = [torch.randn((len(used), page, heads, dim), generator=g).to(torch.bfloat16) for _ in range(2)]
+    pools = [far_pool(pages, page, heads, dim) for _ in range(2)]
+    where = torch.tensor(used, device="cuda")
+    for pool, x in zip(pools, near):
+        pool[where] = x.cuda()
+    cache = kv.PagedCache(*pools)
+    lengths, starts = [70, 75, 100], [0, 1, 2, 42]
+    table = [[0, 1, 2, 3, 4, -1, -1], [-1, -1, -1, 5, 6, -1, -1], [-1, -1, -1, 7, 8, 6, 5]]
+    there = [[used[x] if x >= 0 else -1 for x in row] for row in table]
+    q = torch.randn((42, 4, dim), generator=g).to(torch.bfloat16)
+    want = kv_oracle.attend(q, near[0], near[1], None, None, table, starts, lengths, dim ** -0.5, groups=[0, 3], shared=[48])
+    for t in (there, widened(there, page, heads, dim, False)):
+        lse = torch.empty((42, 4), device="cuda")
+        got = kv.attend_shared(dev(q), cache, dev(t), dev(starts), dev(lengths), dev([0, 3]), dev([48]), lse=lse)
+        compare_attend(got.cpu(), lse.cpu(), *want, near[1], None, torch.bfloat16, False, dim, 100)
+    rows = [torch.empty((42, heads, dim), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    kv.read(cache, dev(there), dev(starts), dev(lengths), *rows)
+    for x, pool in zip(rows, near):
+        assert torch.equal(x.cpu().double(), kv_oracle.read(pool, None, table, starts, lengths, 42, 0.0))
+
+
+def test_many_sequences_of_one_group():
+    """More than the 256 that a workgroup counts a thread each."""
+    n = 300
+    check(30, [1] * n, [70 + 7 * b % 60 for b in range(n)], [0, n], [64], heads=4, kv_heads=1, page=16)
+    check(31, [1 + b % 2 for b in range(n)], [70 + 7 * b % 60 for b in range(n)], [0, 100, 101, 290], [64, 30, 50], heads=2, kv_heads=2, page=16, held8=False)
+
+
 # ---------------------------------------------------------------- reading
 
 

@@ -310,3 +310,39 @@ def test_a_call_gives_the_same_again():
         outs.append((linear.attend(dev(q), dev(k), dev(v), pool, dev([0, 1]), dev([0, 1200, 1300])), pool.state))
     for o, s in outs[1:]:
         assert torch.equal(o, outs[0][0]) and torch.equal(s, outs[0][1])
+
+
+def test_slots_far_apart():
+    """States beyond 2^31 elements."""
+    from tensor_layout_amd import linear
+    g = torch.Generator().manual_seed(18)
+    slots, dk, dv = 40_000, 256, 256   # 2.6 * 10^9 numbers
+    far = torch.empty((slots, 1, dk, dv), device="cuda")
+    used = [39_999, 7, 39_000, 20_001]
+    q, k, v, some, decay = inputs(g, 91, 1, 1, dk, dv, 4, torch.bfloat16)
+    far[torch.tensor(used, device="cuda")] = some.cuda()
+    starts = [0, 1, 91]
+    want = linear_oracle.attend(q, k, v, some, decay, [0, 1], starts, [2, 3], dk ** -0.5)
+    out = linear.attend(dev(q), dev(k), dev(v), linear.StatePool(far, dev(decay)), dev(used[:2]), dev(starts), sources=dev(used[2:]))
+    tol = tolerances(want, [1, 90], dk, torch.bfloat16)
+    near(out.cpu(), want[0], tol[0])
+    near(far[torch.tensor(used, device="cuda")].cpu(), want[1], tol[1])
+
+
+@pytest.mark.parametrize("news", [[1], [7], [60], [600]])
+def test_values_in_place(news):
+    """The result over the values: each is read before its own row is written."""
+    from tensor_layout_amd import linear
+    g = torch.Generator().manual_seed(19)
+    q, k, v, state, decay = inputs(g, news[0], 2, 2, 64, 160, 1, torch.bfloat16)
+    want = linear_oracle.attend(q, k, v, state, decay, [0], [0, news[0]], None, 0.125)
+    x = dev(v)
+    linear.attend(dev(q), dev(k), x, linear.StatePool(dev(state), dev(decay)), dev([0]), dev([0, news[0]]), out=x)
+    near(x.cpu(), want[0], tolerances(want, news, 64, torch.bfloat16)[0])
+
+
+def test_many_sequences():
+    """More than the 64 that a wave looks through at a time, of all lengths; segments of some."""
+    check(20, [b % 23 for b in range(150)], heads=2, dk=32, dv=32)
+    check(21, [300 if b % 9 == 0 else 1 + b % 11 for b in range(100)], heads=1, dk=32, dv=32)
+    check(22, [1200, 900, 3, 1100], heads=1, dk=32, dv=64, dtype=torch.float16)
