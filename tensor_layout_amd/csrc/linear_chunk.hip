@@ -72,11 +72,30 @@ __device__ __forceinline__ Scale scale_of(float most) {
     return Scale{inverse2(down), down};
 }
 
+// Two numbers as 16-bit ones, and what those leave of them: the part that is
+// taken first may be rounded any way, so that fp16 takes the one instruction
+// that rounds both towards zero (two parts keep 21 bits at least).
+template <typename T>
+__device__ __forceinline__ uint32_t part2(float& a, float& b) {
+    if constexpr (std::is_same<T, kv::Fp16>::value) {
+        const auto h = __builtin_amdgcn_cvt_pkrtz(a, b);
+        a = __builtin_fmaf((float)h[0], -1.0f, a);
+        b = __builtin_fmaf((float)h[1], -1.0f, b);
+        return __builtin_bit_cast(uint32_t, h);
+    } else {
+        const uint32_t x = pack2<T>(a, b);
+        a -= lo16<T>(x), b -= hi16<T>(x);
+        return x;
+    }
+}
 // Two numbers as the sum of two 16-bit ones each.
 template <typename T>
 __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
-    hi = pack2<T>(a, b);
-    lo = pack2<T>(a - lo16<T>(hi), b - hi16<T>(hi));
+    hi = part2<T>(a, b);
+    if constexpr (std::is_same<T, kv::Fp16>::value)
+        lo = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(a, b));
+    else
+        lo = pack2<T>(a, b);
 }
 
 // The sequence that segment x belongs to (see seq_of_tile of kv.hpp).
@@ -114,6 +133,7 @@ __global__ void __launch_bounds__(WAVES * 64, NK <= 4 ? 2 : 1) k_chunk(LinearArg
     __shared__ u32x4 pbuf[BLOCKS + 1][2][2][64];   // block, part, product, lane
     __shared__ float pdown[BLOCKS + 1][64];
     __shared__ __attribute__((aligned(16))) float weight[kChunk];   // l^(n-1-j)
+    __shared__ __attribute__((aligned(16))) _Float16 weight16[kChunk];
     __shared__ int bad;
     uint16_t *qs = lds, *ks = lds + QUERIES, *vs = ks + kChunk * QP;
 
@@ -207,7 +227,11 @@ __global__ void __launch_bounds__(WAVES * 64, NK <= 4 ? 2 : 1) k_chunk(LinearArg
             if (vput && (VR * VN == kChunk || vtok + i * VR < kChunk)) *reinterpret_cast<u32x4*>(vs + (vtok + i * VR) * VP + vch) = vreg[i];
         }
         if (some && count > 1) bad = 1;
-        if (tid < kChunk) weight[tid] = tid < count ? exp2_(g2 * (float)(count - 1 - tid)) : 0.0f;
+        if (tid < kChunk) {
+            const float w = tid < count ? exp2_(g2 * (float)(count - 1 - tid)) : 0.0f;
+            weight[tid] = w;
+            if constexpr (kScaled) weight16[tid] = (_Float16)w;
+        }
     };
 
     if (tid == 0) bad = 0;
@@ -232,6 +256,7 @@ __global__ void __launch_bounds__(WAVES * 64, NK <= 4 ? 2 : 1) k_chunk(LinearArg
         if (t < n) fetch(t, count);
 
         f32x16 o[2];
+        float into[2];   // what the state's part of the outputs is multiplied with
         if constexpr (MODE != kState) {
             // P^T's blocks: rows of j = 0 and columns of i = 0, of j = 0 and i = 1, of j = 1 and i = 1.
 #pragma unroll 1
@@ -282,15 +307,22 @@ __global__ void __launch_bounds__(WAVES * 64, NK <= 4 ? 2 : 1) k_chunk(LinearArg
             if constexpr (kScaled) {
                 float most = 0.0f;
 #pragma unroll
-                for (int kb = 0; kb < NK; ++kb) {
-                    const f32x16 y = S[kb];
+                for (int kb = 0; kb < NK; ++kb)
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float x = __builtin_fabsf(y[i]);   // an infinity says nothing of the other channels
-                        most = fmaxf(most, x < __builtin_inff() ? x : 0.0f);
-                    }
+                    for (int i = 0; i < 16; ++i) most = fmaxf(most, __builtin_fabsf(S[kb][i]));
+                most = max_wave(most);
+                if (!(most < __builtin_inff())) {   // an infinity says nothing of the other channels
+                    most = 0.0f;
+#pragma unroll
+                    for (int kb = 0; kb < NK; ++kb)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const float x = __builtin_fabsf(S[kb][i]);
+                            most = fmaxf(most, x < __builtin_inff() ? x : 0.0f);
+                        }
+                    most = max_wave(most);
                 }
-                sc = scale_of(max_wave(most));
+                sc = scale_of(most);
             }
 #pragma unroll
             for (int kb = 0; kb < NK; ++kb)
@@ -314,9 +346,10 @@ __global__ void __launch_bounds__(WAVES * 64, NK <= 4 ? 2 : 1) k_chunk(LinearArg
                 }
 #pragma unroll
             for (int ib = 0; ib < 2; ++ib) {
-                const float f = exp2_(g2 * (float)(ib * 32 + r + 1)) * sc.down;
+                into[ib] = exp2_(g2 * (float)(ib * 32 + r + 1)) * sc.down;
+                if constexpr (!kScaled)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) o[ib][i] *= f;
+                    for (int i = 0; i < 16; ++i) o[ib][i] *= into[ib];
             }
             __syncthreads();   // P is there
         }
@@ -328,14 +361,15 @@ __global__ void __launch_bounds__(WAVES * 64, NK <= 4 ? 2 : 1) k_chunk(LinearArg
             return u32x4{a[0], a[1], c[0], c[1]};
         };
         if constexpr (MODE != kState) {
-            // A block of P^T with its 32 tokens' values, on top of what is there.
+            // A block of P^T with its 32 tokens' values, on top of what is there
+            // (brought to the block's power of two, from the one before).
             u32x4 vt[2];
 #pragma unroll
             for (int blk = 0; blk < 3; ++blk) {
                 const int jb = blk >> 1, ib = (blk + 1) >> 1;
                 if (blk != 1) vt[0] = column16(vs + wave * 32, VP, jb * 2), vt[1] = column16(vs + wave * 32, VP, jb * 2 + 1);
                 if constexpr (kScaled) {
-                    const float up = inverse2(pdown[blk][lane]);
+                    const float up = blk < 2 ? into[ib] * inverse2(pdown[blk][lane]) : pdown[1][lane] * inverse2(pdown[2][lane]);
 #pragma unroll
                     for (int i = 0; i < 16; ++i) o[ib][i] *= up;
                 }
@@ -344,12 +378,8 @@ __global__ void __launch_bounds__(WAVES * 64, NK <= 4 ? 2 : 1) k_chunk(LinearArg
 #pragma unroll
                     for (int part = 0; part < 2; ++part)
                         o[ib] = T::mfma32(__builtin_bit_cast(x8, vt[s]), __builtin_bit_cast(x8, pbuf[blk][part][s][lane]), o[ib]);
-                if constexpr (kScaled) {
-                    const float down = pdown[blk][lane];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) o[ib][i] *= down;
-                }
             }
+            const float last[2] = {kScaled ? pdown[0][lane] * p.a.scale : p.a.scale, kScaled ? pdown[2][lane] * p.a.scale : p.a.scale};
 #pragma unroll
             for (int ib = 0; ib < 2; ++ib) {
                 const int tok = ib * 32 + r;
@@ -359,8 +389,8 @@ __global__ void __launch_bounds__(WAVES * 64, NK <= 4 ? 2 : 1) k_chunk(LinearArg
                 for (int a = 0; a < 4; ++a)
                     if (dvw + a * 8 < p.p.value_dim)
                         *reinterpret_cast<u32x2*>(to + a * 8) =
-                            u32x2{pack2<T>(o[ib][a * 4] * p.a.scale, o[ib][a * 4 + 1] * p.a.scale),
-                                  pack2<T>(o[ib][a * 4 + 2] * p.a.scale, o[ib][a * 4 + 3] * p.a.scale)};
+                            u32x2{pack2<T>(o[ib][a * 4] * last[ib], o[ib][a * 4 + 1] * last[ib]),
+                                  pack2<T>(o[ib][a * 4 + 2] * last[ib], o[ib][a * 4 + 3] * last[ib])};
             }
         }
 
@@ -378,16 +408,22 @@ __global__ void __launch_bounds__(WAVES * 64, NK <= 4 ? 2 : 1) k_chunk(LinearArg
                 }
             };
             Scale sc = {1.0f, 1.0f};
-            if constexpr (kScaled) {   // a value channel's own, as a column of the state has one lane pair
-                float most = 0.0f;
+            if constexpr (kScaled) {
+                // A value channel's own, as a column of the state has one lane
+                // pair; how large the largest is in 16 bits tells its power of
+                // two (which leaves a binade for that).
+                kv::f16x2 most = {0, 0};
 #pragma unroll
                 for (int z = 0; z < 4; ++z) {
-                    float w[8];
-                    weighted(z, w);
+                    const u32x4 v = column16(vs + wave * 32, VP, z);
+                    const u32x2 a = *reinterpret_cast<const u32x2*>(weight16 + z * 16 + hh * 4), c = *reinterpret_cast<const u32x2*>(weight16 + z * 16 + 8 + hh * 4);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) most = fmaxf(most, __builtin_fabsf(w[i]));
+                    for (int i = 0; i < 4; ++i) {
+                        const kv::f16x2 x = __builtin_bit_cast(kv::f16x2, v[i] & 0x7fff7fffu) * __builtin_bit_cast(kv::f16x2, (uint32_t)(i < 2 ? a[i] : c[i - 2]));
+                        most = __builtin_elementwise_max(most, x);
+                    }
                 }
-                sc = scale_of(max_swap32(most));
+                sc = scale_of(max_swap32(fmaxf((float)most[0], (float)most[1])));
             }
             const float first = keep * sc.up;
 #pragma unroll
@@ -406,11 +442,7 @@ __global__ void __launch_bounds__(WAVES * 64, NK <= 4 ? 2 : 1) k_chunk(LinearArg
                 for (int i = 0; i < 4; ++i) {
                     float a = w[i * 2] * sc.up, c = w[i * 2 + 1] * sc.up;
 #pragma unroll
-                    for (int k = 0; k < PARTS; ++k) {
-                        const uint32_t x = pack2<T>(a, c);
-                        part[k][i] = x;
-                        a -= lo16<T>(x), c -= hi16<T>(x);
-                    }
+                    for (int k = 0; k < PARTS; ++k) part[k][i] = part2<T>(a, c);
                 }
 #pragma unroll
                 for (int kb = 0; kb < NK; ++kb) {
