@@ -45,7 +45,7 @@ static const char* choose(const tpl_linear_pool* c, const tpl_linear_batch* g, c
     p.a = *a;
     p.parts = nullptr;
     p.share = c->heads / a->key_heads;
-    p.slices = chunk_slices(c->value_dim);
+    p.slices = chunk_slices(c->key_dim, c->value_dim);
     p.segment = kChunk;
     p.few = kFew;
     if (g->batch == 0 || g->tokens == 0) return nullptr;
@@ -71,19 +71,22 @@ static const char* choose(const tpl_linear_pool* c, const tpl_linear_batch* g, c
     }
     if (p.few != INT_MAX) {
         const int64_t units = heads * p.slices;
-        // Segments where whole sequences would leave the CUs fewer waves than
-        // they hold (two a SIMD, one with over 128 key channels), as many as fill
-        // them, each of some chunks.  A prompt of 8192 tokens, 32 heads of 128, in
-        // segments of 512: 127 us; of 1024 156, of 256 159.  24 prompts of up to
-        // 2000 tokens, 12 heads of 64 by 96 (3 waves each): whole 165 us, in 2
-        // segments 188, in 3 158.
-        const int64_t want = kCUs * (c->key_dim <= 128 ? 8 : 4) / chunk_waves(c->value_dim);
-        const int64_t length = g->tokens / g->batch;
-        if (units < want && length >= 4 * kChunk) {
-            const int64_t n = (want + units - 1) / units;
-            int64_t segment = (length + n - 1) / n;
-            segment = (segment + kChunk - 1) / kChunk * kChunk;
-            if (segment < 2 * kChunk) segment = 2 * kChunk;
+        // Whole sequences, or segments of them where those are too few for the
+        // CUs: as many as the model below finds best.  A workgroup takes its
+        // chunks and two more's time to begin and end; CUs hold 8 waves each;
+        // segments take keys and values twice, which is counted as 1.3 times
+        // the work.  A prompt of 8192 tokens, 32 heads of 128, in 16 segments:
+        // 132 us; in 8 156, in 32 159.  24 prompts of up to 2000 tokens, 12 heads
+        // of 64 by 96: whole 165 us, in 2 segments 172, in 3 147, in 4 151.
+        const int64_t slots = kCUs * 8 / chunk_waves(c->key_dim, c->value_dim), chunks = (g->tokens / g->batch + kChunk - 1) / kChunk;
+        double least = (double)((units + slots - 1) / slots * (chunks + 2));
+        int64_t segments = 1;
+        for (int64_t n = 2; n <= chunks / 2 && units * n < 8 * slots; ++n) {
+            const double cost = 1.3 * (double)((units * n + slots - 1) / slots * ((chunks + n - 1) / n + 2));
+            if (cost < least) least = cost, segments = n;
+        }
+        if (segments > 1) {
+            const int64_t segment = (chunks + segments - 1) / segments * kChunk;
             q.parts = true;
             p.segment = (int)segment;
             q.segments = g->tokens / segment + g->batch;

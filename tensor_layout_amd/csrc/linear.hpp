@@ -61,8 +61,8 @@ hipError_t launch_step(const LinearArgs& p, bool narrow, hipStream_t st);
 enum { kWhole = 0, kState = 1, kOutput = 2 };   // what launch_chunk does with its sequences or segments
 hipError_t launch_chunk(const LinearArgs& p, int mode, int64_t units, hipStream_t st);
 hipError_t launch_scan(const LinearArgs& p, hipStream_t st);
-int chunk_waves(int value_dim);    // of a workgroup
-int chunk_slices(int value_dim);   // workgroups of a head
+int chunk_waves(int key_dim, int value_dim);    // of a workgroup
+int chunk_slices(int key_dim, int value_dim);   // workgroups of a head
 
 }  // namespace linear
 }  // namespace tpl

@@ -126,6 +126,9 @@ __global__ void __launch_bounds__(WAVES * 64, NK <= 4 ? 2 : 1) k_chunk(LinearArg
     typedef typename T::x8 x8;
     constexpr bool kScaled = std::is_same<T, kv::Fp16>::value;
     constexpr int THREADS = WAVES * 64, DK = NK * 32, VC = WAVES * 32;
+    // A chunk is read while the one before it is at work, where that leaves the
+    // state its registers.
+    constexpr bool kAhead = NK <= 4;
     // Rows padded by 16 bytes: 32 rows' pieces at one place reach all banks.
     constexpr int QP = DK + 8, VP = VC + 8;
     constexpr int QUERIES = MODE == kState ? 0 : kChunk * QP, BLOCKS = MODE == kState ? 0 : 3;
@@ -237,8 +240,9 @@ __global__ void __launch_bounds__(WAVES * 64, NK <= 4 ? 2 : 1) k_chunk(LinearArg
     if (tid == 0) bad = 0;
     __syncthreads();
     int t = 0, count = n < kChunk ? n : kChunk, single = 0;   // tokens before `single` are taken one by one
-    fetch(0, count);
+    if (kAhead) fetch(0, count);
     while (t < n) {
+        if (!kAhead) fetch(t, count);
         put(count);
         __syncthreads();
         if (MODE != kState && bad && count > 1) {
@@ -246,14 +250,14 @@ __global__ void __launch_bounds__(WAVES * 64, NK <= 4 ? 2 : 1) k_chunk(LinearArg
             if (tid == 0) bad = 0;
             single = t + count;
             count = 1;
-            fetch(t, 1);
+            if (kAhead) fetch(t, 1);
             __syncthreads();
             continue;
         }
         const int here = t, now = count;
         t += count;
         count = t < single ? 1 : n - t < kChunk ? n - t : kChunk;
-        if (t < n) fetch(t, count);
+        if (kAhead && t < n) fetch(t, count);
 
         f32x16 o[2];
         float into[2];   // what the state's part of the outputs is multiplied with
@@ -298,11 +302,13 @@ __global__ void __launch_bounds__(WAVES * 64, NK <= 4 ? 2 : 1) k_chunk(LinearArg
                     pbuf[blk][1][s][lane] = lo;
                 }
             }
-            // What the state before the chunk gives.
+            // What the state before the chunk gives (waves beyond the head's
+            // value channels bring rows and blocks of P only).
 #pragma unroll
             for (int ib = 0; ib < 2; ++ib)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) o[ib][i] = 0.0f;
+            if (active) {
             Scale sc = {1.0f, 1.0f};
             if constexpr (kScaled) {
                 float most = 0.0f;
@@ -351,6 +357,7 @@ __global__ void __launch_bounds__(WAVES * 64, NK <= 4 ? 2 : 1) k_chunk(LinearArg
 #pragma unroll
                     for (int i = 0; i < 16; ++i) o[ib][i] *= into[ib];
             }
+            }
             __syncthreads();   // P is there
         }
 
@@ -361,6 +368,7 @@ __global__ void __launch_bounds__(WAVES * 64, NK <= 4 ? 2 : 1) k_chunk(LinearArg
             return u32x4{a[0], a[1], c[0], c[1]};
         };
         if constexpr (MODE != kState) {
+            if (active) {
             // A block of P^T with its 32 tokens' values, on top of what is there
             // (brought to the block's power of two, from the one before).
             u32x4 vt[2];
@@ -383,7 +391,7 @@ __global__ void __launch_bounds__(WAVES * 64, NK <= 4 ? 2 : 1) k_chunk(LinearArg
 #pragma unroll
             for (int ib = 0; ib < 2; ++ib) {
                 const int tok = ib * 32 + r;
-                if (tok >= now || !active) continue;
+                if (tok >= now) continue;
                 one* to = go + (here + tok) * p.a.o_token + dvw + hh * 4;
 #pragma unroll
                 for (int a = 0; a < 4; ++a)
@@ -392,9 +400,10 @@ __global__ void __launch_bounds__(WAVES * 64, NK <= 4 ? 2 : 1) k_chunk(LinearArg
                             u32x2{pack2<T>(o[ib][a * 4] * last[ib], o[ib][a * 4 + 1] * last[ib]),
                                   pack2<T>(o[ib][a * 4 + 2] * last[ib], o[ib][a * 4 + 3] * last[ib])};
             }
+            }
         }
 
-        if (MODE != kOutput || t < n) {
+        if (active && (MODE != kOutput || t < n)) {
             const float keep = exp2_(g2 * (float)now);
             // The weighted values of 16 tokens.
             auto weighted = [&](int z, float (&w)[8]) {
@@ -515,13 +524,11 @@ __global__ void __launch_bounds__(256) k_scan(LinearArgs p) {
     if (to) *reinterpret_cast<f32x4*>(to + key * p.p.s_key + c) = x;
 }
 
-// Waves of a workgroup: a head's value channels by 32, at most 4, evenly.
-int chunk_waves(int value_dim) {
-    const int blocks = (value_dim + 31) / 32, slices = (blocks + 3) / 4, w = (blocks + slices - 1) / slices;
-    return w < 2 ? 2 : w;
-}
-int chunk_slices(int value_dim) {
-    const int w = chunk_waves(value_dim) * 32;
+// Waves of a workgroup: 2, each with 32 of up to 64 value channels, or 4 (for
+// up to 128, and where 2 would have to hold too much of a chunk on its way).
+int chunk_waves(int key_dim, int value_dim) { return value_dim <= 64 && key_dim <= 96 ? 2 : 4; }
+int chunk_slices(int key_dim, int value_dim) {
+    const int w = chunk_waves(key_dim, value_dim) * 32;
     return (value_dim + w - 1) / w;
 }
 
@@ -538,11 +545,10 @@ static hipError_t go_mode(const LinearArgs& p, int mode, unsigned grid, hipStrea
 
 template <typename T, int NK>
 static hipError_t go_waves(const LinearArgs& p, int mode, unsigned grid, hipStream_t st) {
-    switch (chunk_waves(p.p.value_dim)) {
-    case 2: return go_mode<T, NK, 2>(p, mode, grid, st);
-    case 3: return go_mode<T, NK, 3>(p, mode, grid, st);
-    default: return go_mode<T, NK, 4>(p, mode, grid, st);
+    if constexpr (NK <= 3) {
+        if (chunk_waves(p.p.key_dim, p.p.value_dim) == 2) return go_mode<T, NK, 2>(p, mode, grid, st);
     }
+    return go_mode<T, NK, 4>(p, mode, grid, st);
 }
 
 template <typename T>
