@@ -156,7 +156,8 @@ int64_t tpl_kv_attend_workspace(const tpl_kv_cache *cache, const tpl_kv_batch *b
  * group is not in order (groups and its first and last sequence's starts, a
  * shared number of 1 .. what a row of the table holds), or that has a new token
  * among its first shared[g] ones, attends to what its own row of the table
- * names: nothing changes where that row names the shared pages too.
+ * names: nothing changes where that row names the shared pages too.  Groups
+ * follow one another: rows of two that overlap have no defined result.
  *
  * `workspace` as tpl_kv_attend takes it (the two may use one in turn), of
  * tpl_kv_attend_shared_workspace() bytes.
@@ -171,8 +172,8 @@ int64_t tpl_kv_attend_shared_workspace(const tpl_kv_cache *cache, const tpl_kv_b
 /*
  * Enqueue: each sequence's last tokens (as many as it has rows) out of the
  * cache, rounded once to the rows' type; from a 16-bit cache, bit for bit.  A
- * token whose page is not there gives zeros.  Rows and heads of the result must
- * not lie over one another.
+ * token whose page is not there gives zeros.  Rows and heads of k and v must not
+ * lie over one another, nor k over v.
  */
 int tpl_kv_read(const tpl_kv_cache *cache, const tpl_kv_batch *batch,
                 const tpl_kv_rows *rows, hipStream_t stream);

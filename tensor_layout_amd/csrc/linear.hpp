@@ -17,7 +17,10 @@ using kv::pack2;
 using kv::u32x2;
 using kv::u32x4;
 
-constexpr int kFew = 8;      // a sequence of up to this many new tokens goes token by token
+// A sequence of up to this many new tokens goes token by token.  64 sequences, 32
+// heads of 128 by 128: of 4 tokens 68 us that way and 79 in a chunk, of 8 81 and
+// 79, of 16 111 and 82.  At 8 the two are even, and the recurrence is exact to fp32.
+constexpr int kFew = 8;
 constexpr int kChunk = 64;   // tokens that longer ones take together
 
 struct LinearArgs {

@@ -24,12 +24,29 @@
 // for all waves, a block of 32x32 each, and handed over in LDS as operands.
 //
 // Roundings: P, S and w V are fp32 numbers and go into the products as the sum
-// of two 16-bit ones (16 or 22 bits), bf16's w V of three (24): outputs are
-// rounded to 8 or 11 bits, but states stay.  In fp16 each is brought near 2^14 by a
+// of two 16-bit ones (16 or 22 bits): outputs are rounded to 8 or 11.  States
+// stay, so where the pool's are made bf16's w V is the sum of three (24).  In fp16 each is brought near 2^14 by a
 // power of two before, so that nothing leaves that type's range.
 //
 // A value that is no finite number would reach earlier rows of its chunk as its
 // product with a weight of zero: such a chunk is taken token by token.
+//
+// Where whole sequences are too few for the CUs a sequence goes in segments:
+// what each adds (k_chunk, kState), the states before each (k_scan), then the
+// outputs (kOutput).
+//
+// Bound: HBM bytes for long sequences of many; here the vector and matrix units,
+// whose work does not overlap.  Measured on an MI355X: a prompt of 8192 tokens,
+// 32 heads of 128 by 128 in bf16, 42 us for the segments' states, 12 for the
+// scan, 78 for the outputs (a copy of the bytes: 52).  Each left out by itself,
+// the last loses 18 us with the products into the state, 11 with those of states
+// and queries, 11 with P, 10 with the writing and 9 with the reading.  Vector and
+// matrix instructions take 38 % and 21 % of its time, 1100 of the former and 78 of
+// the latter a wave and chunk.  Steps: no scratch memory (its reads wait behind
+// the next chunk's) and operands by 16 tokens 133 -> 82 us; two parts of the
+// weighted values 82 -> 77.  Not faster: 8 waves of 16 channels (95 us), pieces
+// exchanged in LDS so that little conflicts (96), rows in LDS further apart (80 to
+// 84), the order of products and vector work set by hand (82 to 88).
 #include "linear.hpp"
 
 namespace tpl {

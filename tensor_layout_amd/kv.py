@@ -417,7 +417,7 @@ def attend_shared(q, cache: PagedCache, table, starts, lengths, groups, shared, 
     From there on each sequence has the tokens of its own row of ``table``.  A sequence in no group, or with new tokens
     among the shared ones, attends by itself to its own row's pages, which has the same result where those begin with the
     shared pages (a page that is shared in part is copied: ``read``, ``append``).  Groups follow one another: rows of two
-    that overlap may be served for either or not at all.
+    that overlap have no defined result.
 
     The rest is ``attend``'s; there is no window.  Returns ``out``."""
     if _lib is None:
@@ -491,7 +491,7 @@ def read(cache: PagedCache, table, starts, lengths, k=None, v=None, *, stream: O
     They are what ``append`` with the same ``table``, ``starts`` and ``lengths`` wrote: an e4m3 value times its block's
     scale, rounded once to the tensors' type (bf16 or fp16); a 16-bit cache is read as its own type, bit for bit.  Other
     tokens are read by naming other lengths: ``lengths`` = n and n rows read a sequence's first n.  Either of ``k`` and
-    ``v`` may be None.  A token whose page is not there gives zeros."""
+    ``v`` may be None; they must not lie over each other.  A token whose page is not there gives zeros."""
     if _lib is None:
         load()
     index = cache._index
