@@ -44,9 +44,10 @@
 // these three) and the next each sequence's own tokens, starting from them in
 // place of zeros.  Directly, one launch takes both ranges, a step in one only.
 // 64 sequences behind 4096 shared tokens, up to 1024 of their own, 8 heads of 128
-// in e4m3: 33 us of 59 for the own (a copy of their bytes: 14), 20 % of the
-// vector units' time; what bounds it is the chain of reads, of which a
-// workgroup has two or three steps to hide each other's.
+// in e4m3: 49 us, 25 of them for the shared (a copy of all bytes: 15); what bounds
+// both is the chain of reads (lengths, groups, table, keys), of which a workgroup
+// has few steps to hide.  Reading the first step's keys before the shared tokens'
+// results, which takes 130 registers more, was slower (50 us).
 #pragma once
 
 #include "kv_attend.hpp"
@@ -210,7 +211,7 @@ __global__ void __launch_bounds__(256, few_blocks(HELD8, DC, MR)) k_few(AttendAr
     const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     int b;
-    int seq_step, chunk;
+    int seq_step, chunk, even;
     // Its heads, this wave's among them and its place among their waves.
     const int hw = 1 << p.heads_log, sets = p.c.kv_heads >> p.heads_log;
     // Workgroups are dealt to the 8 dies in turn: the same share of all heads
@@ -220,7 +221,7 @@ __global__ void __launch_bounds__(256, few_blocks(HELD8, DC, MR)) k_few(AttendAr
     if (share >= p.shares) return;
     const int wd = wave & (hw - 1), wt = wave >> p.heads_log, h = h0 + wd;
     FewSeq f;
-    const int total = locate<ROWS, SHARED>(p, share, &b, &f, &seq_step, &chunk);
+    const int total = locate<ROWS, SHARED>(p, share, &b, &f, &seq_step, &chunk, &even);
     const int win = p.a.window ? p.a.window : 0x7fffffff;
     // Whether a row at `at` sees token j of a group, both ends of rows given;
     // whether all rows see its 16 tokens.
@@ -248,6 +249,7 @@ __global__ void __launch_bounds__(256, few_blocks(HELD8, DC, MR)) k_few(AttendAr
             seq_step += all;
             if (++b >= few_items<SHARED>(p)) return;
             f = uniform<SHARED>(few_seq<ROWS, SHARED>(p, b));
+            if (SHARED && even) f.steps = even;
             continue;
         }
         const int rt = uniform((int)((uint32_t)off / (uint32_t)f.steps));
@@ -291,7 +293,7 @@ __global__ void __launch_bounds__(256, few_blocks(HELD8, DC, MR)) k_few(AttendAr
         // the parts, two at a time.
         if constexpr (SHARED) {
             if (f.cut > 0 && s0 == 0 && !p.direct && !flat) {
-                constexpr int AT_ONCE = DC <= 8 ? 2 : 1;
+                constexpr int AT_ONCE = MR * DC <= 8 ? 2 : 1;
                 const int step = 4 >> p.heads_log;
 #pragma unroll
                 for (int mr = 0; mr < MR; ++mr) {
@@ -472,6 +474,7 @@ __global__ void __launch_bounds__(256, few_blocks(HELD8, DC, MR)) k_few(AttendAr
                 load_tile<HELD8, DC, SHARED>(p, hd, at[1], x[1]);
                 places(at, s + 1);   // the table's entries for the next step
                 step(x);
+                if (SHARED && (s + 1) * (kStepGroups >> p.heads_log) >= f.span.n) break;   // a tile's share may be longer
             }
         }
 

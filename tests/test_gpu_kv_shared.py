@@ -336,6 +336,17 @@ def test_many_sequences_of_one_group():
     check(31, [1 + b % 2 for b in range(n)], [70 + 7 * b % 60 for b in range(n)], [0, 100, 101, 290], [64, 30, 50], heads=2, kv_heads=2, page=16, held8=False)
 
 
+@pytest.mark.parametrize("n", [40, 100, 300])
+def test_own_tokens_of_several_tiles_a_workgroup(n):
+    """16 heads leave fewer workgroups a head than there are sequences: each takes several whole tiles, of unequal lengths,
+    some of no rows; then with one long sequence among them equal parts of all steps."""
+    news = [0 if b % 11 == 5 else 1 + (b % 7 == 3) * 20 for b in range(n)]
+    own = [1 + 23 * b % 200 for b in range(n)]
+    check(32, news, [64 + a + b for a, b in zip(own, news)], [0, n], [64], heads=16, kv_heads=16, dim=16, page=16)
+    own[n // 2] = 2500
+    check(33, news, [64 + a + b for a, b in zip(own, news)], [0, n // 3, n], [64, 50], heads=16, kv_heads=16, dim=16, page=16, held8=False)
+
+
 # ---------------------------------------------------------------- reading
 
 
