@@ -72,18 +72,28 @@ static const char* choose(const tpl_linear_pool* c, const tpl_linear_batch* g, c
     }
     if (p.few != INT_MAX) {
         const int64_t units = heads * p.slices;
-        // Whole sequences, or segments of them where those are too few for the
-        // CUs: as many as the model below finds best.  A workgroup takes its
-        // chunks and two more's time to begin and end; CUs hold 8 waves each;
-        // segments take keys and values twice, which is counted as 1.3 times
-        // the work.  A prompt of 8192 tokens, 32 heads of 128, in 16 segments:
-        // 132 us; in 8 156, in 32 159.  24 prompts of up to 2000 tokens, 12 heads
-        // of 64 by 96: whole 165 us, in 2 segments 172, in 3 147, in 4 151.
+        // Whole sequences, or segments of them: as many as the model below finds
+        // best, in units of a chunk by a workgroup that has its SIMDs to itself.
+        // A workgroup takes its chunks and two more's time to begin and end; two
+        // waves a SIMD, as many as up to 128 key channels allow, take 1.6 times
+        // as long; segments take keys and values twice, 1.3 times the work, and
+        // the scan; sequences of unlike lengths end apart, which is counted as a
+        // tenth.  Measured, whole and in the segments that are chosen: a prompt of
+        // 8192 tokens, 32 heads of 128, 713 and 131 us (16 of them; 8: 143, 12:
+        // 146, 24: 150); 4 of 2000 190 and 144 (4; 2: 189, 8: 156); 8 of 4000,
+        // whole, 375 (2: 471, 3: 463); 24 of up to 4000, 12 heads of 64 by 96, 317
+        // and 264 (3).
         const int64_t slots = kCUs * 8 / chunk_waves(c->key_dim, c->value_dim), chunks = (g->tokens / g->batch + kChunk - 1) / kChunk;
-        double least = (double)((units + slots - 1) / slots * (chunks + 2));
+        const auto rounds = [&](int64_t n) {
+            const int64_t half = slots / 2;
+            if (c->key_dim > 128) return (double)((n + half - 1) / half);
+            const int64_t rest = n % slots;
+            return 1.6 * (double)(n / slots) + (rest == 0 ? 0.0 : rest <= half ? 1.0 : 1.6);
+        };
+        double least = 1.1 * rounds(units) * (double)(chunks + 2);
         int64_t segments = 1;
-        for (int64_t n = 2; n <= chunks / 2 && units * n < 8 * slots; ++n) {
-            const double cost = 1.3 * (double)((units * n + slots - 1) / slots * ((chunks + n - 1) / n + 2));
+        for (int64_t n = 2; n * 3 <= chunks * 2 && units * n < 8 * slots; ++n) {
+            const double cost = 1.3 * rounds(units * n) * (double)((chunks + n - 1) / n + 2) + 2.0 * (double)(units * n) / (double)slots;
             if (cost < least) least = cost, segments = n;
         }
         if (segments > 1) {
