@@ -53,9 +53,10 @@ __device__ __forceinline__ const float* source_of(const LinearArgs& p, int b, in
 }
 
 // The logarithm to base 2 of a head's decay: at most zero, and finite, so that
-// a decay to nothing leaves exp2(0 * it) at one.
+// a decay to nothing leaves exp2(0 * it) at one.  No number stays none.
 __device__ __forceinline__ float decay_of(const LinearArgs& p, int head) {
-    return fmaxf(fminf(p.p.decay[head], 0.0f) * 1.44269504088896340736f, -1.0e6f);
+    const float d = p.p.decay[head];
+    return d != d ? d : fmaxf(fminf(d, 0.0f) * 1.44269504088896340736f, -1.0e6f);
 }
 
 __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
