@@ -238,9 +238,13 @@ struct SharedChoice {
 // the CUs speaks against row tiles of 256: they are taken from 512 rows a group
 // on (256 samples of 32768 tokens, 2048 rows for each of 8 heads, in 4 parts:
 // 318 against 363 us with tiles of 128; 256 rows over 4096 tokens 62 against 59).
-// The number of parts weighs rounds of workgroups, each some steps' time to
-// begin and end, against the parts that every sequence has to read (those 256
-// rows with 4, 8, 16 and 32 parts: 70, 59, 61, 77 us).
+// The number of parts is what the model below finds best, in steps of a workgroup
+// with a CU to itself (3.5 us): rounds of workgroups, of which two on a CU take
+// 1.5 times as long, each two steps' time to begin and end, and the writing and
+// reading of what a part leaves of every row.  With 8, 16 and 32 parts: 64
+// sequences behind 4096 tokens, 256 rows for each of 8 heads, 48, 46 and 53 us; 16
+// behind 8192 47, 35 and 32; 24 behind 16000 105, 75 and 65; 256 behind 4096 74,
+// 98 and 162.
 static const char* plan_prefix_tile(AttendArgs& p, Choice& q, int64_t rows, int64_t groups) {
     q.dk = p.c.dim <= 64 ? 64 : p.c.dim <= 96 ? 96 : p.c.dim <= 128 ? 128 : p.c.dim <= 192 ? 192 : 256;
     const int64_t mean = (rows + groups - 1) / groups;
@@ -248,10 +252,14 @@ static const char* plan_prefix_tile(AttendArgs& p, Choice& q, int64_t rows, int6
     p.tile_rows = large ? 256 : 128;
     p.tile_tokens = p.tile_rows / p.group;
     const int64_t per = (int64_t)p.tile_tokens * p.group, units = groups * ((mean + per - 1) / per) * p.c.kv_heads;
-    const int64_t slots = large || q.dk > 128 ? kCUs : 2 * kCUs, steps = ((int64_t)p.cap + 63) / 64;
-    int64_t least = INT64_MAX;
-    for (int s = 1; s <= 32 && (s == 1 || s * 2 <= steps); ++s) {
-        const int64_t cost = (units * s + slots - 1) / slots * ((steps + s - 1) / s + 6) + s;
+    const int64_t steps = ((int64_t)p.cap + 63) / 64;
+    const bool pairs = !large && q.dk <= 128;   // two workgroups fit a CU
+    const double part = (double)rows * p.c.kv_heads * p.c.dim * 8.0 / 14e6;   // bytes to and from memory, of a step's time
+    double least = 1e300;
+    for (int s = 1; s <= 64 && (s == 1 || s * 2 <= steps); ++s) {
+        const int64_t n = units * s, slots = pairs ? 2 * kCUs : kCUs, rest = n % slots;
+        const double rounds = (pairs ? 1.5 : 1.0) * (double)(n / slots) + (rest == 0 ? 0.0 : rest <= kCUs ? 1.0 : 1.5);
+        const double cost = rounds * (double)((steps + s - 1) / s + 2) + part * s;
         if (cost < least) least = cost, p.splits = s;
     }
     const int64_t tiles = (int64_t)p.g.tokens / p.tile_tokens + groups;
