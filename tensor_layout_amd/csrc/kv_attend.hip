@@ -287,16 +287,17 @@ static const char* choose_shared(const tpl_kv_cache* c, const tpl_kv_batch* g, c
     // Directly where an average sequence fills a row tile by itself: its
     // products over the shared tokens are as many either way (16 questions of
     // 300 tokens behind 2048, 8 heads a cache's: 242 against 290 us).  And
-    // where all sequences' reading of whole rows of the table comes to 256 MiB
+    // where all sequences' reading of whole rows of the table comes to 96 MiB
     // at most, which the caches beside HBM give in less time than a second
     // launch with its chain of reads takes (e4m3, 8 heads of 128; directly
-    // against in two launches: 4 sequences of 530 tokens 12 against 21 us, 16 of
-    // 2200 25 against 32, 64 of 2200, 295 MB, 44 against 44, 32 of 8200 65
-    // against 49, 64 of 5120 76 against 58).
+    // against in two launches: 4 sequences of 530 tokens 12 against 22 us, 4 of
+    // 8200 24 against 34, 64 of 530 18 against 25, 16 of 2200, 72 MB, 25 against
+    // 26, 16 of 4200, 138 MB, 33 against 29, 64 of 1800 42 against 31; 256 of
+    // 500, 262 MB, 50 against 53).
     const int64_t rows = (int64_t)g->tokens * p2.group, w = c->type == TPL_KV_E4M3 ? 1 : 2;
     const int64_t tiles = (rows + g->batch * 16 - 1) / ((int64_t)g->batch * 16);   // of 16 rows, of an average sequence
     const double once = (double)(g->batch * tiles * c->kv_heads) * (double)(c->dim * 2 * w) * p2.cap;
-    if (rows >= (int64_t)g->batch * 128 || once <= 0x1p28) {
+    if (rows >= (int64_t)g->batch * 128 || once <= 0x1.8p26) {
         p2.direct = 1;
         return nullptr;
     }

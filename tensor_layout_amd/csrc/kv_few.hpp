@@ -44,10 +44,10 @@
 // these three) and the next each sequence's own tokens, starting from them in
 // place of zeros.  Directly, one launch takes both ranges, a step in one only.
 // 64 sequences behind 4096 shared tokens, up to 1024 of their own, 8 heads of 128
-// in e4m3: 48 us, 25 of them for the shared (a copy of all bytes: 15); what bounds
+// in e4m3: 46 us, 20 of them for the shared (a copy of all bytes: 15); what bounds
 // both is the chain of reads (lengths, groups, table, keys), of which a workgroup
 // has few steps to hide.  Reading the first step's keys before the shared tokens'
-// results, which takes 130 registers more, was slower (50 us).
+// results, which takes 130 registers more, was slower (by 2 us).
 #pragma once
 
 #include "kv_attend.hpp"

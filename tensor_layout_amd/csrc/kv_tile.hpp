@@ -39,8 +39,8 @@
 // every row sees all shared tokens, and parts (m, sum w, sum w v) are left for
 // the launch over the sequences' own tokens.  256 samples of one prompt of 32768
 // tokens, 64 heads of 128 on 8 in e4m3: 293 us of 325 (275 GFLOP, 940 TFLOP/s),
-// 49 % and 44 % of the vector and matrix units' time.  64 of one of 4096: 25 us,
-// three rounds' worth of waits for pages and keys, 9 % and 5 %.
+// 49 % and 44 % of the vector and matrix units' time.  64 of one of 4096: 20 us in
+// 16 parts of 4 steps, 9 % and 5 %: waits for pages, keys and each other.
 #pragma once
 
 #include "kv_attend.hpp"
